@@ -42,8 +42,10 @@ typedef enum {
   SS2D_ERR_ALIGN = -6,          /* a pointer is not aligned to its element size   */
   SS2D_ERR_NO_DEVICE = -7,      /* no HIP device, or the device query failed      */
   SS2D_ERR_HIP = -8,            /* a HIP call or kernel launch failed             */
-  SS2D_ERR_NOALLOC_LIMIT = -9   /* ss2d_forward_noalloc: the shape's temporary    */
+  SS2D_ERR_NOALLOC_LIMIT = -9,  /* ss2d_forward_noalloc: the shape's temporary    */
                                 /* exceeds the library's static array (128 MiB)   */
+  SS2D_ERR_WORKSPACE = -10      /* a caller's workspace (ss2d_tokens.h) is NULL,  */
+                                /* too small or not aligned to 16 bytes           */
 } ss2d_status;
 
 /*

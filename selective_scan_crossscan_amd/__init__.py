@@ -8,89 +8,25 @@ library is missing or the tensors are not on a ROCm device, calls raise.
 from __future__ import annotations
 
 import ctypes
-import os
-import threading
+
+from ._lib import SS2D_BF16, SS2D_F32, Peaks, SS2DError, lib, library_path, status_string
+from ._lib import check as _raise
 
 __all__ = ["forward", "ss2d_forward", "project", "ss2d_project", "forward_from_x", "ss2d_forward_from_x",
            "channel_last", "ss2d_channel_last", "backward", "ss2d_backward", "measure_peaks", "describe", "bidir_forward", "ss2d_bidir_forward", "bidir_backward", "ss2d_bidir_backward", "ss2d_forward_noalloc", "trim_memory", "status_string", "version", "library_path", "lib",
-           "SS2D_F32", "SS2D_BF16", "SS2DError"]
+           "SS2D_F32", "SS2D_BF16", "SS2DError",
+           "linear_attention", "linear_attention_step", "rms_norm", "rms_norm_fp8", "rms_norm_backward"]
 
-SS2D_F32 = 0
-SS2D_BF16 = 1
-
-_HERE = os.path.dirname(os.path.abspath(__file__))
-_LIB_PATH = os.path.join(_HERE, "libss2d.so")
-_lock = threading.Lock()
-_lib = None
+# The token-sequence operators (tokens.py), imported with torch when first used.
+_TOKENS = ("linear_attention", "linear_attention_step", "rms_norm", "rms_norm_fp8", "rms_norm_backward")
 
 
-class SS2DError(RuntimeError):
-    def __init__(self, code: int, message: str):
-        super().__init__(f"libss2d call failed ({code}): {message}")
-        self.code = code
+def __getattr__(name):
+    if name in _TOKENS:
+        from . import tokens
 
-
-def library_path() -> str:
-    return _LIB_PATH
-
-
-class Peaks(ctypes.Structure):
-    """ss2d_peaks: rates measured on the device by ss2d_measure_peaks."""
-    _fields_ = [("exp_per_s", ctypes.c_double), ("fma_per_s", ctypes.c_double),
-                ("update_mix_per_s", ctypes.c_double), ("hbm_read_Bps", ctypes.c_double),
-                ("hbm_copy_Bps", ctypes.c_double), ("lds_read_Bps", ctypes.c_double),
-                ("compute_units", ctypes.c_int), ("state_loop_per_s", ctypes.c_double)]
-
-
-def lib():
-    """The loaded libss2d.so (ctypes), with argument types declared."""
-    global _lib
-    with _lock:
-        if _lib is None:
-            if not os.path.exists(_LIB_PATH):
-                raise ImportError(f"{_LIB_PATH} is not built; run __graft_entry__.build() or "
-                                  "python -m selective_scan_crossscan_amd._build")
-            L = ctypes.CDLL(_LIB_PATH)
-            vp, i64 = ctypes.c_void_p, ctypes.c_int64
-            L.ss2d_forward.argtypes = [vp] * 8 + [i64] * 5 + [ctypes.c_int, vp]
-            L.ss2d_forward.restype = ctypes.c_int
-            L.ss2d_status_string.argtypes = [ctypes.c_int]
-            L.ss2d_status_string.restype = ctypes.c_char_p
-            L.ss2d_last_hip_error.argtypes = []
-            L.ss2d_last_hip_error.restype = ctypes.c_char_p
-            L.ss2d_version.argtypes = []
-            L.ss2d_version.restype = ctypes.c_int
-            L.ss2d_describe.argtypes = [i64] * 5 + [ctypes.c_int, ctypes.c_char_p, i64]
-            L.ss2d_describe.restype = ctypes.c_int
-            L.ss2d_describe_lanes.argtypes = [i64] * 5 + [ctypes.c_int, ctypes.c_int, ctypes.c_char_p, i64]
-            L.ss2d_describe_lanes.restype = ctypes.c_int
-            L.ss2d_forward_lanes.argtypes = [vp] * 8 + [i64] * 5 + [ctypes.c_int, ctypes.c_int, vp]
-            L.ss2d_forward_lanes.restype = ctypes.c_int
-            L.ss2d_bidir_forward.argtypes = [vp] * 8 + [i64] * 4 + [ctypes.c_int, vp]
-            L.ss2d_bidir_forward.restype = ctypes.c_int
-            L.ss2d_forward_noalloc.argtypes = [vp] * 8 + [i64] * 5 + [ctypes.c_int, vp]
-            L.ss2d_forward_noalloc.restype = ctypes.c_int
-            L.ss2d_trim_memory.argtypes = []
-            L.ss2d_trim_memory.restype = ctypes.c_int
-            L.ss2d_project.argtypes = [vp] * 6 + [i64] * 6 + [ctypes.c_int, vp]
-            L.ss2d_project.restype = ctypes.c_int
-            L.ss2d_forward_from_x.argtypes = [vp] * 7 + [i64] * 6 + [ctypes.c_int, vp]
-            L.ss2d_forward_from_x.restype = ctypes.c_int
-            L.ss2d_channel_last.argtypes = [vp, vp, vp, ctypes.c_float, ctypes.c_int, vp] + [i64] * 4 + [
-                ctypes.c_int, vp]
-            L.ss2d_channel_last.restype = ctypes.c_int
-            L.ss2d_backward.argtypes = [vp] * 15 + [i64] * 5 + [ctypes.c_int, vp]
-            L.ss2d_backward.restype = ctypes.c_int
-            L.ss2d_bidir_backward.argtypes = [vp] * 15 + [i64] * 4 + [ctypes.c_int, vp]
-            L.ss2d_bidir_backward.restype = ctypes.c_int
-            L.ss2d_measure_peaks.argtypes = [ctypes.POINTER(Peaks), i64, vp]
-            L.ss2d_measure_peaks.restype = ctypes.c_int
-            _lib = L
-    return _lib
-
-
-def status_string(code: int) -> str:
-    return lib().ss2d_status_string(int(code)).decode()
+        return getattr(tokens, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def version() -> int:
@@ -349,13 +285,6 @@ def measure_peaks(hbm_bytes: int = 1 << 30, stream: int = 0) -> dict:
     if rc != 0:
         _raise(rc)
     return {name: getattr(p, name) for name, _ in Peaks._fields_}
-
-
-def _raise(rc: int):
-    msg = status_string(rc)
-    if rc == -8:
-        msg += ": " + lib().ss2d_last_hip_error().decode()
-    raise SS2DError(rc, msg)
 
 
 def forward(x, dt, A_log, dt_bias, Bs, Cs, Ds, out=None, stream=None, lanes: int = 0):

@@ -13,7 +13,7 @@
 
 namespace {
 
-constexpr int kVersion = 1 * 10000 + 2 * 100 + 0;  // 1.2.0
+constexpr int kVersion = 1 * 10000 + 3 * 100 + 0;  // 1.3.0
 thread_local char g_last_hip_error[256] = "";
 
 void remember(hipError_t e) {
@@ -131,6 +131,10 @@ hipError_t tmp_free(void* p, hipStream_t st) { return p ? hipFreeAsync(p, st) : 
 
 }  // namespace
 
+namespace ss2d {
+void remember_hip_error(hipError_t e) { remember(e); }
+}  // namespace ss2d
+
 extern "C" {
 
 int ss2d_version(void) { return kVersion; }
@@ -185,6 +189,7 @@ const char* ss2d_status_string(int status) {
     case SS2D_ERR_NO_DEVICE: return "no usable HIP device";
     case SS2D_ERR_HIP: return "a HIP call or kernel launch failed";
     case SS2D_ERR_NOALLOC_LIMIT: return "the shape needs more temporary memory than ss2d_forward_noalloc holds";
+    case SS2D_ERR_WORKSPACE: return "the workspace is missing, too small or not aligned to 16 bytes";
     default: return "unknown status";
   }
 }

@@ -35,6 +35,9 @@ struct LaunchArgs {
   const float* wdt = nullptr;
 };
 
+// Keeps the text of `e` for ss2d_last_hip_error (per thread).
+void remember_hip_error(hipError_t e);
+
 // Largest rank of the low-rank step input the scan expands itself.
 constexpr int kMaxLowRankInput = 8;
 

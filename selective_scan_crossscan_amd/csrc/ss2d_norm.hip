@@ -1,0 +1,261 @@
+// Root-mean-square norm of rows with the residual's addition, and its gradients.
+//
+//   r = x + residual,  y = r rstd weight,  rstd = 1 / sqrt(mean(r^2) + eps);
+//   8-bit output: per 128 channels s = max(max|y| / 448, 2^-126), q = e4m3(y / s);
+//   dx = dresidual + rstd (weight dy - xhat mean(weight dy xhat)),  xhat = r rstd,
+//   dweight = sum over rows of dy xhat.
+//
+// Bound by memory: every value is read once and written once.  A row is held in
+// registers, eight consecutive channels per thread, between the sum over it and
+// the output, so no value is read twice.  A row gets one wave up to 512 channels
+// (four rows per workgroup) and otherwise one workgroup with as many waves as
+// there are groups of 512 channels up to 16, which also keeps a single row's
+// latency at one load, one sum and one store.  The sums are fp32.
+#include "ss2d_token_ops.h"
+
+namespace ss2d {
+namespace {
+
+using namespace tok;
+
+// Sum over the THREADS threads that share a row (`red`: one float per wave).
+template <int THREADS>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if (THREADS > 64) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();  // the previous sum has been read
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) v += red[i];
+  }
+  return v;
+}
+
+// Threads of a workgroup: one row's, or four rows of one wave each.
+constexpr int block_threads(int per_row) { return per_row == 64 ? 256 : per_row; }
+
+template <typename S, int THREADS, int NV, bool FP8>
+__global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
+    const S* x, const S* residual, const float* __restrict__ weight, S* residual_out, void* yv,
+    float* __restrict__ scales, float eps, int64_t rows, int dim) {
+  __shared__ float red[THREADS > 64 ? THREADS / 64 : 1];
+  const int t = threadIdx.x % THREADS;
+  const int64_t row = (int64_t)blockIdx.x * (block_threads(THREADS) / THREADS) + threadIdx.x / THREADS;
+  if (row >= rows) return;  // whole waves, and only where a row is one wave: no barrier follows there
+  const int64_t at = row * dim;
+  float v[NV][8];
+  float sq = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (t + j * THREADS) * 8;
+    load8(x + at + c, dim - c, v[j]);
+    if (residual) {
+      float r[8];
+      load8(residual + at + c, dim - c, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(v[j][i], v[j][i], sq);
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red) / (float)dim + eps);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (t + j * THREADS) * 8;
+    if (residual_out) store8(residual_out + at + c, dim - c, v[j]);
+    float w[8];
+    if (weight) load8(weight + c, dim - c, w);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[j][i] *= rstd;
+      if (weight) v[j][i] *= w[i];
+      if (FP8) amax = fmaxf(amax, fabsf(v[j][i]));  // a NaN is passed over here and stays one below
+    }
+    if (!FP8) {
+      store8(static_cast<S*>(yv) + at + c, dim - c, v[j]);
+    } else {
+      // 16 consecutive threads hold one block of 128 channels
+#pragma unroll
+      for (int m = 1; m < 16; m <<= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+      const float s = fmaxf(amax / 448.0f, 1.17549435e-38f);
+      const int blocks = (dim + kScaleBlock - 1) / kScaleBlock;
+      if ((t & 15) == 0 && c < dim) scales[row * blocks + c / kScaleBlock] = s;
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float z = v[j][i] / s;
+        u[i] = z > 448.f ? 448.f : z < -448.f ? -448.f : z;  // keeps NaN
+      }
+      uint32_t q[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int p = __builtin_amdgcn_cvt_pk_fp8_f32(u[4 * i], u[4 * i + 1], 0, false);
+        q[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(u[4 * i + 2], u[4 * i + 3], p, true);
+      }
+      uint8_t* y = static_cast<uint8_t*>(yv) + at + c;
+      if (dim - c >= 8) {
+        __builtin_memcpy(y, q, 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < dim - c) y[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+      }
+    }
+  }
+}
+
+// Each workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ... and keeps its
+// part of the weight's gradient in registers; norm_sum_partials adds the parts.
+template <typename S, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(
+    const S* __restrict__ r, const float* __restrict__ weight, const S* dy, const S* dresidual, S* dx,
+    float* __restrict__ partial, float eps, int64_t rows, int dim) {
+  __shared__ float red[THREADS > 64 ? 2 * THREADS / 64 : 1];
+  const int t = threadIdx.x;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (t + j * THREADS) * 8;
+    if (weight) load8(weight + c, dim - c, w[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!weight) w[j][i] = 1.f;
+      dw[j][i] = 0.f;
+    }
+  }
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int64_t at = row * dim;
+    float x[NV][8], g[NV][8];
+    float sq = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + j * THREADS) * 8;
+      load8(r + at + c, dim - c, x[j]);
+      load8(dy + at + c, dim - c, g[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sq = fmaf(x[j][i], x[j][i], sq);
+        dot = fmaf(x[j][i], g[j][i] * w[j][i], dot);
+      }
+    }
+    sq = row_sum<THREADS>(sq, red);
+    dot = row_sum<THREADS>(dot, red + (THREADS > 64 ? THREADS / 64 : 0));
+    const float rstd = 1.0f / sqrtf(sq / (float)dim + eps);
+    const float mean = dot * rstd / (float)dim;  // mean of weight dy xhat
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + j * THREADS) * 8;
+      float d[8];
+      if (dresidual) load8(dresidual + at + c, dim - c, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = x[j][i] * rstd;
+        dw[j][i] = fmaf(g[j][i], xh, dw[j][i]);
+        const float v = rstd * (w[j][i] * g[j][i] - xh * mean);
+        d[i] = dresidual ? d[i] + v : v;
+      }
+      store8(dx + at + c, dim - c, d);
+    }
+  }
+  if (partial) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + j * THREADS) * 8;
+      store8(partial + (int64_t)blockIdx.x * dim + c, dim - c, dw[j]);
+    }
+  }
+}
+
+// dweight[c] = sum over the workgroups' parts: 64 channels by 16 ranges of parts
+// per workgroup, the ranges' sums added in order.
+__global__ __launch_bounds__(1024) void norm_sum_partials(const float* __restrict__ partial, float* __restrict__ dw,
+                                                          int parts, int dim) {
+  __shared__ float sums[16][64];
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), range = threadIdx.x >> 6;
+  float s = 0.f;
+  if (c < dim)
+    for (int p = range; p < parts; p += 16) s += partial[(int64_t)p * dim + c];
+  sums[range][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (range == 0 && c < dim) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += sums[i][threadIdx.x];
+    dw[c] = s;
+  }
+}
+
+template <typename S, int THREADS, int NV>
+void launch_norm_t(const NormArgs& a) {
+  const int per = block_threads(THREADS) / THREADS;
+  const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(block_threads(THREADS));
+  if (a.scales)
+    rms_norm_kernel<S, THREADS, NV, true><<<grid, block, 0, a.stream>>>(
+        (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, a.scales, a.eps, a.rows, (int)a.dim);
+  else
+    rms_norm_kernel<S, THREADS, NV, false><<<grid, block, 0, a.stream>>>(
+        (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, nullptr, a.eps, a.rows, (int)a.dim);
+}
+
+template <typename S>
+hipError_t launch_norm_s(const NormArgs& a) {
+  if (a.dim <= 512)
+    launch_norm_t<S, 64, 1>(a);
+  else if (a.dim <= 2048)
+    launch_norm_t<S, 256, 1>(a);
+  else if (a.dim <= 4096)
+    launch_norm_t<S, 512, 1>(a);
+  else if (a.dim <= 8192)
+    launch_norm_t<S, 1024, 1>(a);
+  else
+    launch_norm_t<S, 1024, 2>(a);
+  return hipGetLastError();
+}
+
+template <typename S, int THREADS, int NV>
+void launch_norm_backward_t(const NormBackwardArgs& a) {
+  rms_norm_backward_kernel<S, THREADS, NV><<<dim3((unsigned)norm_backward_blocks(a.rows, a.dim)), dim3(THREADS), 0,
+                                             a.stream>>>((const S*)a.r, a.weight, (const S*)a.dy,
+                                                         (const S*)a.dresidual, (S*)a.dx,
+                                                         a.dweight ? a.partial : nullptr, a.eps, a.rows, (int)a.dim);
+}
+
+template <typename S>
+hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
+  if (a.dim <= 512)
+    launch_norm_backward_t<S, 64, 1>(a);
+  else if (a.dim <= 2048)
+    launch_norm_backward_t<S, 256, 1>(a);
+  else if (a.dim <= 4096)
+    launch_norm_backward_t<S, 512, 1>(a);
+  else if (a.dim <= 8192)
+    launch_norm_backward_t<S, 1024, 1>(a);
+  else
+    launch_norm_backward_t<S, 1024, 2>(a);
+  if (a.dweight)
+    norm_sum_partials<<<dim3((unsigned)((a.dim + 63) / 64)), dim3(1024), 0, a.stream>>>(
+        a.partial, a.dweight, (int)norm_backward_blocks(a.rows, a.dim), (int)a.dim);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_backward_blocks(int64_t rows, int64_t dim) {
+  // enough waves to fill 256 CUs twice over at 8 waves each, and no more parts than rows
+  const int64_t waves = dim <= 512 ? 1 : dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16;
+  const int64_t want = 256 * 16 / waves;
+  return rows < want ? rows : want;
+}
+
+hipError_t launch_rms_norm(const NormArgs& a) {
+  return a.dtype == 1 ? launch_norm_s<uint16_t>(a) : launch_norm_s<float>(a);
+}
+
+hipError_t launch_rms_norm_backward(const NormBackwardArgs& a) {
+  return a.dtype == 1 ? launch_norm_backward_s<uint16_t>(a) : launch_norm_backward_s<float>(a);
+}
+
+}  // namespace ss2d

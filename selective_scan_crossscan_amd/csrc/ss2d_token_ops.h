@@ -1,0 +1,161 @@
+// Internal interface of the token-sequence operators (include/ss2d_tokens.h):
+// launch arguments, already validated by ss2d_tokens_api.hip, and the device
+// helpers their kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ss2d {
+
+constexpr int kMaxKeyDim = 256;
+constexpr int kMaxValueDim = 1024;
+constexpr int kMaxNormDim = 16384;
+constexpr int kScaleBlock = 128;  // channels per scale of the 8-bit values
+
+struct NormArgs {
+  const void* x;
+  const void* residual;   // or null
+  const float* weight;    // or null
+  void* residual_out;     // or null
+  void* y;
+  float* scales;          // or null: y in the storage type
+  float eps;
+  int64_t rows, dim;
+  int dtype;
+  hipStream_t stream;
+};
+hipError_t launch_rms_norm(const NormArgs& a);
+
+struct NormBackwardArgs {
+  const void* r;
+  const float* weight;    // or null
+  const void* dy;
+  const void* dresidual;  // or null
+  void* dx;
+  float* dweight;         // or null
+  float* partial;         // norm_backward_blocks(rows, dim, dtype) x dim, with dweight
+  float eps;
+  int64_t rows, dim;
+  int dtype;
+  hipStream_t stream;
+};
+hipError_t launch_rms_norm_backward(const NormBackwardArgs& a);
+// Workgroups of the backward, each with a row of partial weight gradients.
+int64_t norm_backward_blocks(int64_t rows, int64_t dim);
+
+struct StepArgs {
+  const void *q, *k, *v;
+  const float* log_decay;
+  float* state;
+  const int32_t* index;  // or null
+  void* o;
+  int64_t rows, slots, groups, heads, key_dim, value_dim, q_row, k_row, v_row;
+  float scale;
+  int dtype;
+  hipStream_t stream;
+};
+hipError_t launch_attention_step(const StepArgs& a);
+
+// ------------------------------------------------------------------ device helpers
+namespace tok {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// A decay under exp(-104) is 0 in fp32; sums of clamped logarithms stay finite.
+constexpr float kMinLogDecay = -104.f;
+
+__device__ __forceinline__ float clamp_log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
+
+__device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Two floats to two packed bf16, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2 f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+}
+
+// 16 bytes at an address that need only be aligned to its elements: gfx950's
+// global memory takes such accesses as they are.
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t w[4];
+};
+struct __attribute__((packed, aligned(2))) Bytes8 {
+  uint32_t w[2];
+};
+
+// Eight elements p[0..7], of which the first n are there (the others are 0).
+__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const Bytes16 a = *reinterpret_cast<const Bytes16*>(p), b = *reinterpret_cast<const Bytes16*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(a.w[i]);
+      v[4 + i] = __uint_as_float(b.w[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const Bytes16 a = *reinterpret_cast<const Bytes16*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_bits_to_f32(a.w[i] & 0xffffu);
+      v[2 * i + 1] = __uint_as_float(a.w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_bits_to_f32(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    Bytes16 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a.w[i] = __float_as_uint(v[i]);
+      b.w[i] = __float_as_uint(v[4 + i]);
+    }
+    *reinterpret_cast<Bytes16*>(p) = a;
+    *reinterpret_cast<Bytes16*>(p + 4) = b;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[8]) {
+  Bytes16 a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  if (n >= 8) {
+    *reinterpret_cast<Bytes16*>(p) = a;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint16_t)(i & 1 ? a.w[i / 2] >> 16 : a.w[i / 2]);
+  }
+}
+
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, 0.f); }
+
+// Sum over the 64 lanes of a wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+}  // namespace tok
+}  // namespace ss2d

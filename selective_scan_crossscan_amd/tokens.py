@@ -1,0 +1,256 @@
+"""Token-sequence operators of libss2d.so (include/ss2d_tokens.h) on torch tensors.
+
+Linear attention with a decay per head (prompts, gradients, single tokens over a
+cache of states), the root-mean-square norm with the residual's addition (storage
+type or 8 bits with scales, gradients).  As in the rest of the package the binding
+only checks and marshals arguments, and there is no CPU fallback.
+
+Every function runs on `stream`, or on the current stream of the tensors' device,
+and allocates its outputs and workspace from torch's allocator on that stream, so
+it can run under torch.cuda.graph.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import SS2D_BF16, SS2D_F32, check, lib
+
+_CODES = {torch.float32: SS2D_F32, torch.bfloat16: SS2D_BF16}
+_SIZES = ctypes.c_int64 * 21  # ss2d_attention_sizes: six sizes, five times three strides
+
+
+def _code(x) -> int:
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    return code
+
+
+def _require(name, x, device, dtype, shape=None, dense=True):
+    """x is a tensor of this device, dtype and shape (None: not checked)."""
+    if not x.is_cuda:
+        raise ValueError("all tensors must be on the GPU (no CPU fallback)")
+    if x.device != device:
+        raise ValueError("all tensors must be on the same device")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and x.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    if dense and not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _call(fn, device, *args):
+    """fn(*args, current stream) with `device` current; raises on a status code."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != 0:
+        check(rc)
+
+
+def _on_stream(stream, device, fn, *args, **kwargs):
+    if stream.device != device:
+        raise ValueError("stream must belong to the tensors' device")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _workspace(bytes_, device):
+    """(tensor or None, address) of a workspace; a negative size is a status code."""
+    if bytes_ < 0:
+        check(int(bytes_))
+    if bytes_ == 0:
+        return None, None
+    w = torch.empty(bytes_, dtype=torch.uint8, device=device)
+    return w, w.data_ptr()
+
+
+# ------------------------------------------------------------------ linear attention
+def _token_strides(name, x, lead):
+    """(sequence, token, head) strides of x (*lead, heads, dim), dim dense; lead is (T,) or (S, L)."""
+    st = x.stride()
+    if x.dim() == len(lead) + 2 and x.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}'s last axis must be dense")
+    return (st[0], st[1], st[2]) if len(lead) == 2 else (0, st[0], st[1])
+
+
+def _attention_sizes(q, k, v, log_decay, cu_seqlens, do=None):
+    """Checked (sizes array, lead, S, G, H, K, V, code)."""
+    packed = cu_seqlens is not None
+    n = 3 if packed else 4
+    if v.dim() != n or q.dim() != n or k.dim() != n:
+        raise ValueError("q, k, v must be (T, heads, dim) with cu_seqlens, else (S, L, heads, dim)")
+    code, device = _code(v), v.device
+    lead = tuple(v.shape[:-2])
+    H, V = v.shape[-2:]
+    G, K = q.shape[-2:]
+    _require("v", v, device, v.dtype, dense=False)
+    _require("q", q, device, v.dtype, lead + (G, K), dense=False)
+    _require("k", k, device, v.dtype, lead + (G, K), dense=False)
+    _require("log_decay", log_decay, device, torch.float32, lead + (H,), dense=False)
+    if G < 1 or H % G != 0:
+        raise ValueError("the heads of v must be a multiple of those of q and k")
+    if packed:
+        _require("cu_seqlens", cu_seqlens, device, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must be (sequences + 1,)")
+        S, T = cu_seqlens.shape[0] - 1, lead[0]
+    else:
+        S, T = lead[0], lead[0] * lead[1]
+    sizes = [S, T, G, H, K, V, *_token_strides("q", q, lead), *_token_strides("k", k, lead),
+             *_token_strides("v", v, lead), *_token_strides("log_decay", log_decay, lead)]
+    if do is not None:
+        _require("do", do, device, v.dtype, v.shape, dense=False)
+        sizes += _token_strides("do", do, lead)
+    return _SIZES(*sizes), lead, S, G, H, K, V, code
+
+
+def linear_attention(q, k, v, log_decay, state=None, cu_seqlens=None, scale: float = 1.0, final_state: bool = False,
+                     out=None, stream=None):
+    """Linear attention with a decay per head over prompts (ss2d_linear_attention):
+    h_t = exp(g_t) h_{t-1} + k_t v_t', o_t = scale h_t' q_t, causal.
+
+    q, k (S,L,G,K), v (S,L,H,V): float32 or bfloat16, H a multiple of G; log_decay (S,L,H) float32 (g, usually <= 0).
+    With cu_seqlens (S+1,) int32 on the device the sequences are packed: q, k (T,G,K), v (T,H,V), log_decay (T,H),
+    sequence s being tokens cu_seqlens[s]..cu_seqlens[s+1]-1; outputs of tokens in no sequence are left as they were.
+    Any strides with a dense last axis (slices of one projection's output, expanded decays); K <= 256, V <= 1024.
+    state (S,H,K,V) float32: the states to start from (None: 0).
+    Returns o (v's shape, contiguous), and with final_state also the states after the last tokens (S,H,K,V) float32.
+    """
+    if stream is not None:
+        return _on_stream(stream, v.device, linear_attention, q, k, v, log_decay, state, cu_seqlens, scale,
+                          final_state, out)
+    sizes, lead, S, G, H, K, V, code = _attention_sizes(q, k, v, log_decay, cu_seqlens)
+    device = v.device
+    if state is not None:
+        _require("state", state, device, torch.float32, (S, H, K, V))
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=device)
+    else:
+        _require("out", out, device, v.dtype, v.shape)
+    last = torch.empty((S, H, K, V), dtype=torch.float32, device=device) if final_state else None
+    L = lib()
+    nbytes = L.ss2d_linear_attention_workspace(sizes, 0 if cu_seqlens is None else 1, code)
+    ws, at = _workspace(nbytes, device)
+    _call(L.ss2d_linear_attention, device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          _ptr(state), _ptr(cu_seqlens), out.data_ptr(), _ptr(last), sizes, scale, code, at, nbytes)
+    return (out, last) if final_state else out
+
+
+def linear_attention_step(q, k, v, log_decay, state, state_index=None, scale: float = 1.0, out=None, stream=None):
+    """One token per row over a cache of states, updated in place (ss2d_linear_attention_step).
+
+    q, k (B,G,K), v (B,H,V): float32 or bfloat16, rows any stride apart, dense inside; log_decay (B,H) float32.
+    state (slots,H,K,V) float32.  state_index (B,) int32: each row's slot (None: row i has slot i).  A row with an index
+    outside 0..slots-1 is padding (output 0, no state touched); rows of one slot are its consecutive tokens.
+    Returns o (B,H,V) in v's dtype.
+    """
+    if stream is not None:
+        return _on_stream(stream, v.device, linear_attention_step, q, k, v, log_decay, state, state_index, scale, out)
+    if v.dim() != 3 or q.dim() != 3 or state.dim() != 4:
+        raise ValueError("q, k must be (B,G,K), v (B,H,V), state (slots,H,K,V)")
+    code, device = _code(v), v.device
+    B, H, V = v.shape
+    G, K = q.shape[1:]
+    slots = state.shape[0]
+    _require("v", v, device, v.dtype, dense=False)
+    _require("q", q, device, v.dtype, (B, G, K), dense=False)
+    _require("k", k, device, v.dtype, (B, G, K), dense=False)
+    _require("log_decay", log_decay, device, torch.float32, (B, H))
+    _require("state", state, device, torch.float32, (slots, H, K, V))
+    if G < 1 or H % G != 0:
+        raise ValueError("the heads of v must be a multiple of those of q and k")
+    if state_index is not None:
+        _require("state_index", state_index, device, torch.int32, (B,))
+    for name, x, d in (("q", q, K), ("k", k, K), ("v", v, V)):
+        st = x.stride()
+        if (x.shape[1] > 1 and st[1] != d) or (d > 1 and st[2] != 1):
+            raise ValueError(f"{name} must be dense inside a row")
+    if out is None:
+        out = torch.empty((B, H, V), dtype=v.dtype, device=device)
+    else:
+        _require("out", out, device, v.dtype, (B, H, V))
+    _call(lib().ss2d_linear_attention_step, device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          state.data_ptr(), _ptr(state_index), out.data_ptr(), B, slots, G, H, K, V, q.stride(0), k.stride(0),
+          v.stride(0), scale, code)
+    return out
+
+
+# ------------------------------------------------------------------ norm
+def _norm_inputs(x, weight, others):
+    code, device = _code(x), x.device
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be (..., dim)")
+    dim = x.shape[-1]
+    _require("x", x, device, x.dtype)
+    if weight is not None:
+        _require("weight", weight, device, torch.float32, (dim,))
+    for name, t in others:
+        if t is not None:
+            _require(name, t, device, x.dtype, x.shape)
+    return code, device, x.numel() // dim, dim
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out=None, residual_out=None, stream=None):
+    """Root-mean-square norm over the last axis, with the residual's addition (ss2d_rms_norm):
+    r = x + residual, y = r / sqrt(mean(r^2) + eps) * weight.
+
+    x, residual (...,dim): float32 or bfloat16; weight (dim,) float32 or None.  out and residual_out may be x or residual.
+    Returns y, or (y, r) when a residual is given.
+    """
+    if stream is not None:
+        return _on_stream(stream, x.device, rms_norm, x, weight, residual, eps, out, residual_out)
+    code, device, rows, dim = _norm_inputs(x, weight, (("residual", residual), ("out", out),
+                                                       ("residual_out", residual_out)))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    _call(lib().ss2d_rms_norm, device, x.data_ptr(), _ptr(residual), _ptr(weight), eps, _ptr(residual_out),
+          out.data_ptr(), None, rows, dim, code)
+    return out if residual is None else (out, residual_out)
+
+
+def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, residual_out=None, stream=None):
+    """rms_norm with y in 8 bits: returns (y float8_e4m3fn (...,dim), scales float32 (...,ceil(dim/128))) and, when a
+    residual is given, r as a third; y times its block's scale is the norm's output (the left operand of matmul_fp8)."""
+    if stream is not None:
+        return _on_stream(stream, x.device, rms_norm_fp8, x, weight, residual, eps, residual_out)
+    code, device, rows, dim = _norm_inputs(x, weight, (("residual", residual), ("residual_out", residual_out)))
+    y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=device)
+    scales = torch.empty(x.shape[:-1] + ((dim + 127) // 128,), dtype=torch.float32, device=device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    _call(lib().ss2d_rms_norm, device, x.data_ptr(), _ptr(residual), _ptr(weight), eps, _ptr(residual_out),
+          y.data_ptr(), scales.data_ptr(), rows, dim, code)
+    return (y, scales) if residual is None else (y, scales, residual_out)
+
+
+def rms_norm_backward(r, weight, dy, dresidual=None, eps: float = 1e-6, stream=None) -> dict:
+    """Gradients of rms_norm (ss2d_rms_norm_backward): r the normalised sum (rms_norm's second output, or x),
+    dy the gradient of y, dresidual that of r's other use or None.  Returns dx (the gradient of x and of the
+    residual alike, r's dtype) and, with a weight, dweight (dim,) float32."""
+    if stream is not None:
+        return _on_stream(stream, r.device, rms_norm_backward, r, weight, dy, dresidual, eps)
+    code, device, rows, dim = _norm_inputs(r, weight, (("dy", dy), ("dresidual", dresidual)))
+    dx = torch.empty(r.shape, dtype=r.dtype, device=device)
+    L = lib()
+    dweight = ws = at = None
+    nbytes = 0
+    if weight is not None:
+        dweight = torch.empty((dim,), dtype=torch.float32, device=device)
+        nbytes = L.ss2d_rms_norm_backward_workspace(rows, dim, code)
+        ws, at = _workspace(nbytes, device)
+    _call(L.ss2d_rms_norm_backward, device, r.data_ptr(), _ptr(weight), dy.data_ptr(), _ptr(dresidual), eps,
+          dx.data_ptr(), _ptr(dweight), rows, dim, code, at, nbytes)
+    return {"dx": dx} if weight is None else {"dx": dx, "dweight": dweight}
