@@ -2,8 +2,8 @@
  * ss2d_tokens.h -- C ABI of libss2d.so's token-sequence operators: what a
  * language model's layer runs next to the scans of ss2d.h.
  *   linear attention with a decay per head   the state recurrence of the scans
- *       with one decay for a head's whole state: over prompts, and one token per
- *       row over a cache of states;
+ *       with one decay for a head's whole state: forward over prompts, its
+ *       gradients, and one token per row over a cache of states;
  *   root-mean-square norm                    with the residual's addition, in the
  *       storage type or in 8 bits with scales, and its gradients.
  *
@@ -82,6 +82,30 @@ int ss2d_linear_attention(const void* q, const void* k, const void* v, const flo
 /* Bytes of workspace ss2d_linear_attention needs (0: none), or a negative status.
  * packed: 1 if it will be given cu_seqlens, else 0. */
 int64_t ss2d_linear_attention_workspace(const ss2d_attention_sizes* sizes, int packed, int dtype);
+
+/*
+ * ss2d_linear_attention_backward -- the gradients of ss2d_linear_attention.
+ *   inputs  q, k, v, log_decay, state_in, cu_seqlens as for the forward;
+ *           d_o         [tokens, heads, value_dim] dtype, strided
+ *           dstate_out  gradient of state_out, fp32, dense, or NULL for 0
+ *   outputs dq, dk      [tokens, groups, key_dim] dtype, dense, summed over a group's
+ *                       heads in a fixed order
+ *           dv          [tokens, heads, value_dim] dtype, dense
+ *           dlog_decay  [tokens, heads] fp32, dense (a decay repeated by stride 0 gets
+ *                       the gradient of each of its uses)
+ *           dstate_in   [sequences, heads, key_dim, value_dim] fp32 or NULL
+ * Outputs are overwritten, not added to; tokens outside the sequences keep what they
+ * were.  Outputs must not overlap inputs or each other.  Rounding, validation and the
+ * rest as for the forward.
+ */
+int ss2d_linear_attention_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                                   const float* state_in, const int32_t* cu_seqlens, const void* d_o,
+                                   const float* dstate_out, void* dq, void* dk, void* dv, float* dlog_decay,
+                                   float* dstate_in, const ss2d_attention_sizes* sizes, float scale, int dtype,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ss2d_linear_attention_backward needs, or a negative status. */
+int64_t ss2d_linear_attention_backward_workspace(const ss2d_attention_sizes* sizes, int packed, int dtype);
 
 /*
  * ss2d_linear_attention_step -- one token for each row, over a cache of states:

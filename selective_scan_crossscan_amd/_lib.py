@@ -81,6 +81,10 @@ def lib():
             L.ss2d_linear_attention.restype = ci
             L.ss2d_linear_attention_workspace.argtypes = [sizes, ci, ci]
             L.ss2d_linear_attention_workspace.restype = i64
+            L.ss2d_linear_attention_backward.argtypes = [vp] * 13 + [sizes, f32, ci, vp, i64, vp]
+            L.ss2d_linear_attention_backward.restype = ci
+            L.ss2d_linear_attention_backward_workspace.argtypes = [sizes, ci, ci]
+            L.ss2d_linear_attention_backward_workspace.restype = i64
             L.ss2d_linear_attention_step.argtypes = [vp] * 7 + [i64] * 9 + [f32, ci, vp]
             L.ss2d_linear_attention_step.restype = ci
             L.ss2d_rms_norm.argtypes = [vp] * 3 + [f32] + [vp] * 3 + [i64] * 2 + [ci, vp]

@@ -54,8 +54,10 @@ struct AttentionPlan {
   int kp;           // key_dim rounded up to 32, 64, 128 or 256
   int vt;           // value columns per workgroup
   int vtiles;
-  int64_t seg_len;  // tokens per segment
+  int chunk;        // tokens per chunk
+  int64_t seg_len;  // tokens per segment, whole chunks
   int64_t slots;    // segments, an upper bound for packed sequences
+  int64_t chunks;   // chunks, an upper bound for packed sequences
   int nseg;         // per sequence of equal lengths
   bool split;       // some sequence may have more than one segment
 };
@@ -63,10 +65,49 @@ AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, i
                              bool packed, int dtype);
 size_t attention_workspace_bytes(const AttentionPlan& pl, int64_t heads, int64_t key_dim, int64_t value_dim);
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& pl);
+SequenceMap sequence_map(const AttentionArgs& a, const AttentionPlan& pl);
+
+struct AttentionBackwardArgs {
+  AttentionArgs f;  // the forward's inputs; workspace, stream
+  const void* d_o;
+  int64_t do_stride[3];
+  const float* dstate_out;  // or null
+  void *dq, *dk, *dv;
+  float* dlog_decay;
+  float* dstate_in;  // or null
+};
+AttentionPlan plan_attention_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim,
+                                      int64_t value_dim, bool packed, int dtype);
+size_t attention_backward_workspace_bytes(const AttentionPlan& pl, int64_t tokens, int64_t groups, int64_t heads,
+                                          int64_t key_dim, int64_t value_dim);
+hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const AttentionPlan& pl);
+
+// The state's passes over keys and values alone (ss2d_attention_state.hip).
+enum StatePass {
+  kSegmentStates,   // what each segment (but a sequence's last) adds to the state, from 0, and its whole decay
+  kChunkStates,     // the state before every chunk
+  kSegmentGradients // what each segment (but the first) adds to the state's gradient, from 0, walking backwards
+};
+struct StateParams {
+  const void *k, *v;  // kSegmentGradients: q and d_o
+  const float* g;
+  const float* state_in;     // or null
+  float* seg_state;          // (slot, head, K, V)
+  float* seg_decay;          // (slot, head)
+  float* chunk_state;        // kChunkStates: (chunk, head, value tile, KP x VT as the kernel lays it out)
+  SequenceMap map;
+  int64_t k_stride[3], v_stride[3], g_stride[3];
+  int groups, heads, K, V, vtiles;
+  float scale;
+  bool split;                // segments start from seg_state
+};
+hipError_t launch_state_pass(StatePass pass, const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
+// seg_state: from what each segment adds to the state before it (forward) or the
+// gradient of the state behind it (reverse); `from` is the sequences' initial
+// state or final gradient, or null.
+hipError_t launch_state_carry(bool reverse, const StateParams& p, const float* from, hipStream_t st);
 
 namespace tok {
-
-constexpr int kAttThreads = 256;
 
 // Where a segment lies: sequence s, its first token and length, and the
 // segment's range [begin, end) inside the sequence.
@@ -79,6 +120,13 @@ struct Segment {
 __device__ __forceinline__ int64_t cu_at(const SequenceMap& m, int s) {
   const int64_t c = m.cu[s];
   return c < 0 ? 0 : c > m.tokens ? m.tokens : c;
+}
+
+// Number of the chunk of C tokens that holds token `at` of segment g's sequence,
+// counted like the segments' slots.
+template <int C>
+__device__ __forceinline__ int64_t chunk_number(const SequenceMap& m, const Segment& g, int64_t at) {
+  return (m.cu ? g.start / C + g.s : g.s * ((m.len + C - 1) / C)) + at / C;
 }
 
 // False where no segment has this slot.
@@ -229,19 +277,18 @@ __device__ __forceinline__ Frag<float> frag_col_split(const Tile<float, R, C>& m
 }
 
 // A tile on its way from global memory to LDS, in registers.
-template <typename E, int ROWS, int COLS>
+template <typename E, int ROWS, int COLS, int THREADS = 256>
 struct TileLoad {
   static constexpr int kPer = 16 / (int)sizeof(E);  // elements per 16 bytes
   static constexpr int kRowPieces = COLS / kPer;
-  static constexpr int kPieces = ROWS * kRowPieces / kAttThreads;
-  static_assert(ROWS * kRowPieces % kAttThreads == 0, "whole pieces per thread");
+  static constexpr int kPieces = (ROWS * kRowPieces + THREADS - 1) / THREADS;
   Bytes16 r[kPieces];
 
   // Rows 0..nrows-1 of `base` (stride elements apart), columns 0..ncols-1; the rest is 0.
   __device__ __forceinline__ void load(const E* base, int64_t stride, int nrows, int ncols) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int idx = threadIdx.x + i * kAttThreads;
+      const int idx = threadIdx.x + i * THREADS;
       const int row = idx / kRowPieces, c = (idx % kRowPieces) * kPer;
       r[i] = Bytes16{{0, 0, 0, 0}};
       if (row < nrows && c < ncols) {
@@ -260,9 +307,10 @@ struct TileLoad {
   __device__ __forceinline__ void store(Tile<E, ROWS, COLS>& m) const {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int idx = threadIdx.x + i * kAttThreads;
+      const int idx = threadIdx.x + i * THREADS;
       const int row = idx / kRowPieces, c = (idx % kRowPieces) * kPer;
-      __builtin_memcpy(__builtin_assume_aligned(&m.e[row * m.stride + c], 16), &r[i], 16);
+      if (ROWS * kRowPieces % THREADS == 0 || row < ROWS)
+        __builtin_memcpy(__builtin_assume_aligned(&m.e[row * m.stride + c], 16), &r[i], 16);
     }
   }
 };

@@ -17,9 +17,9 @@
 // consecutive columns of one token per lane.
 //
 // Few sequences and heads leave CUs idle, so sequences are then cut into
-// segments: a first pass computes what each segment adds to a state from 0 and
-// its whole decay, attention_carry turns these into the states before the
-// segments, and the second pass starts from them.
+// segments: a pass over keys and values computes what each segment adds to a
+// state from 0 and its whole decay, a carry turns these into the states before
+// the segments (ss2d_attention_state.hip), and the walk starts from them.
 #include "ss2d_attention.h"
 
 namespace ss2d {
@@ -32,25 +32,23 @@ struct AttentionParams {
   const float* state_in;
   void* o;
   float* state_out;
-  float* seg_state;  // (slot, head, K, V): what a segment adds, then the state before it
-  float* seg_decay;  // (slot, head): the segment's whole decay
+  const float* seg_state;  // (slot, head, K, V): the state before a segment
   SequenceMap map;
   int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3];
   int groups, heads, K, V, vtiles;
   float scale;
-  bool split;  // second pass of segments: they start from seg_state
+  bool split;  // segments behind a sequence's first start from seg_state
 };
 
-template <typename E, int C, int KP, int VT, bool STATE_ONLY>
-__global__ __launch_bounds__(kAttThreads) void attention_kernel(AttentionParams p) {
+template <typename E, int C, int KP, int VT>
+__global__ __launch_bounds__(256) void attention_kernel(AttentionParams p) {
   constexpr int NI = C / 16;        // token tiles
   constexpr int NK = KP / 16;       // key tiles
   constexpr int NV = VT / 64;       // value tiles of a wave
   constexpr int PF = kFullParts<E>, PH = kHalfParts<E>;
-  __shared__ Tile<E, STATE_ONLY ? 1 : C, STATE_ONLY ? 1 : KP> qs;
-  __shared__ Tile<E, C, KP> ks;
+  __shared__ Tile<E, C, KP> qs, ks;
   __shared__ Tile<E, C, VT> vs;
-  __shared__ Tile<E, STATE_ONLY ? 1 : C, STATE_ONLY ? 1 : C> ps;
+  __shared__ Tile<E, C, C> ps;
   __shared__ Decays<C> dec;
 
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
@@ -59,7 +57,6 @@ __global__ __launch_bounds__(kAttThreads) void attention_kernel(AttentionParams 
   const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
   Segment seg;
   if (!find_segment(p.map, slot, seg)) return;
-  if (STATE_ONLY && seg.last) return;  // nothing follows it
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
   const int vw = wave * (VT / 4);  // this wave's first column in the tile
@@ -74,8 +71,7 @@ __global__ __launch_bounds__(kAttThreads) void attention_kernel(AttentionParams 
   f32x4 h[NK][NV];
   const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
   {
-    const float* from = STATE_ONLY ? nullptr : p.split && seg.begin > 0 ? p.seg_state + sh
-                                           : p.state_in ? p.state_in + qh : nullptr;
+    const float* from = p.split && seg.begin > 0 ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
@@ -92,104 +88,101 @@ __global__ __launch_bounds__(kAttThreads) void attention_kernel(AttentionParams 
   float gl = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-    if (!STATE_ONLY) ql.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+    ql.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
     kl.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
     vl.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
     if (wave == 0) gl = lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
   };
-  float whole = 0.f, frac = 0.f;  // the segment's log2 decay so far
   if (seg.begin < seg.end) fetch(seg.begin);
   for (int64_t at = seg.begin; at < seg.end; at += C) {
     const int n = (int)min((int64_t)C, seg.end - at);
     __syncthreads();  // the previous chunk has been read
-    if constexpr (!STATE_ONLY) ql.store(qs);
+    ql.store(qs);
     kl.store(ks);
     vl.store(vs);
     if (wave == 0) scan_decays<C>(gl, dec);
     __syncthreads();
     if (at + C < seg.end) fetch(at + C);
 
-    if constexpr (!STATE_ONLY) {
-      // scores, transposed: rows j (keys), columns i (tokens); 16 tokens per wave (two waves per 16 where C = 32)
-      const int it = NI == 4 ? wave : wave >> 1;
-      f32x4 s[NI];
+    // scores, transposed: rows j (keys), columns i (tokens); 16 tokens per wave (two waves per 16 where C = 32)
+    const int it = NI == 4 ? wave : wave >> 1;
+    f32x4 s[NI];
 #pragma unroll
-      for (int jt = 0; jt < NI; ++jt) s[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int jt = 0; jt < NI; ++jt) s[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < KP; c += 32) {
-        const Frag<E> b = frag_row(qs, it * 16 + l, c);
-#pragma unroll
-        for (int jt = 0; jt < NI; ++jt)
-          if (jt <= it && (NI == 4 || jt == (wave & 1))) s[jt] = mma(frag_row(ks, jt * 16 + l, c), b, s[jt]);
-      }
-      const int i = it * 16 + l;
+    for (int c = 0; c < KP; c += 32) {
+      const Frag<E> b = frag_row(qs, it * 16 + l, c);
 #pragma unroll
       for (int jt = 0; jt < NI; ++jt)
-        if (jt <= (it | 1) && (NI == 4 || jt == (wave & 1))) {  // the last may be all masked: the output reads pairs
-          f32x4 w;
+        if (jt <= it && (NI == 4 || jt == (wave & 1))) s[jt] = mma(frag_row(ks, jt * 16 + l, c), b, s[jt]);
+    }
+    const int i = it * 16 + l;
+#pragma unroll
+    for (int jt = 0; jt < NI; ++jt)
+      if (jt <= (it | 1) && (NI == 4 || jt == (wave & 1))) {  // the last may be all masked: the output reads pairs
+        f32x4 w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = jt * 16 + 4 * g + r;
+          w[r] = j <= i ? s[jt][r] * (p.scale * dec.between(i, j)) : 0.f;
+        }
+        put4(&ps.e[i * ps.stride + jt * 16 + 4 * g], w);
+      }
+    __syncthreads();
+
+    if (active) {
+      f32x4 o[NV][NI];
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+#pragma unroll
+        for (int x = 0; x < NI; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // h' q'
+#pragma unroll
+      for (int c = 0; c < NK; c += 2) {
+        Frag<E> a[NV][PH];
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          float x[8];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int j = jt * 16 + 4 * g + r;
-            w[r] = j <= i ? s[jt][r] * (p.scale * dec.between(i, j)) : 0.f;
+            x[r] = h[c][t][r];
+            x[4 + r] = h[c + 1][t][r];
           }
-          put4(&ps.e[i * ps.stride + jt * 16 + 4 * g], w);
-        }
-      __syncthreads();
-
-      if (active) {
-        f32x4 o[NV][NI];
-#pragma unroll
-        for (int t = 0; t < NV; ++t)
-#pragma unroll
-          for (int x = 0; x < NI; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // h' q'
-#pragma unroll
-        for (int c = 0; c < NK; c += 2) {
-          Frag<E> a[NV][PH];
-#pragma unroll
-          for (int t = 0; t < NV; ++t) {
-            float x[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              x[r] = h[c][t][r];
-              x[4 + r] = h[c + 1][t][r];
-            }
-            split_parts(x, a[t]);
-          }
-#pragma unroll
-          for (int x = 0; x < NI; ++x) {
-            const Frag<E> b = frag_row_split(qs, x * 16 + l, c * 16);
-#pragma unroll
-            for (int t = 0; t < NV; ++t)
-#pragma unroll
-              for (int q = 0; q < PH; ++q) o[t][x] = mma(a[t][q], b, o[t][x]);
-          }
+          split_parts(x, a[t]);
         }
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
-          const float f = p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
+          const Frag<E> b = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-          for (int t = 0; t < NV; ++t) o[t][x] *= f;
+          for (int t = 0; t < NV; ++t)
+#pragma unroll
+            for (int q = 0; q < PH; ++q) o[t][x] = mma(a[t][q], b, o[t][x]);
         }
-        // v' scores'
+      }
 #pragma unroll
-        for (int j = 0; j < NI; j += 2)
+      for (int x = 0; x < NI; ++x) {
+        const float f = p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
+#pragma unroll
+        for (int t = 0; t < NV; ++t) o[t][x] *= f;
+      }
+      // v' scores'
+#pragma unroll
+      for (int j = 0; j < NI; j += 2)
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          const Frag<E> a = frag_col_split(vs, j * 16, vw + t * 16);
+#pragma unroll
+          for (int x = j; x < NI; ++x) o[t][x] = mma(a, frag_row_split(ps, x * 16 + l, j * 16), o[t][x]);
+        }
+      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
+#pragma unroll
+      for (int x = 0; x < NI; ++x)
+        if (x * 16 + l < n)
 #pragma unroll
           for (int t = 0; t < NV; ++t) {
-            const Frag<E> a = frag_col_split(vs, j * 16, vw + t * 16);
-#pragma unroll
-            for (int x = j; x < NI; ++x) o[t][x] = mma(a, frag_row_split(ps, x * 16 + l, j * 16), o[t][x]);
+            const int v = vw + t * 16 + 4 * g;
+            store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[t][x]);
           }
-        E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-#pragma unroll
-        for (int x = 0; x < NI; ++x)
-          if (x * 16 + l < n)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) {
-              const int v = vw + t * 16 + 4 * g;
-              store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[t][x]);
-            }
-      }
     }
 
     if (active) {
@@ -222,13 +215,9 @@ __global__ __launch_bounds__(kAttThreads) void attention_kernel(AttentionParams 
         }
       }
     }
-    if (STATE_ONLY) {
-      whole += dec.whole[C - 1];
-      frac += dec.frac[C - 1];
-    }
   }
 
-  float* to = STATE_ONLY ? p.seg_state + sh : seg.last && p.state_out ? p.state_out + qh : nullptr;
+  float* to = seg.last && p.state_out ? p.state_out + qh : nullptr;
   if (to)
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
@@ -239,74 +228,31 @@ __global__ __launch_bounds__(kAttThreads) void attention_kernel(AttentionParams 
           const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
           if (k < K && v < nv) to[(int64_t)k * p.V + v0 + v] = h[kt][t][r];
         }
-  if (STATE_ONLY && vt == 0 && threadIdx.x == 0)
-    p.seg_decay[slot * p.heads + head] = __builtin_amdgcn_exp2f(whole + frac);
-}
-
-// seg_state: from what each segment adds to the state before it.  One thread per
-// state entry walks its sequence's segments.
-__global__ __launch_bounds__(kAttThreads) void attention_carry(AttentionParams p) {
-  const int64_t kv = (int64_t)p.K * p.V;
-  const int64_t blocks = (kv + kAttThreads - 1) / kAttThreads;
-  const int64_t e = blockIdx.x % blocks * kAttThreads + threadIdx.x;
-  const int head = (int)(blockIdx.x / blocks % p.heads), s = (int)(blockIdx.x / blocks / p.heads);
-  if (e >= kv) return;
-  int64_t slot, len;
-  if (p.map.cu) {
-    const int64_t start = cu_at(p.map, s), end = cu_at(p.map, s + 1);
-    slot = start / p.map.seg_len + s;
-    len = end - start;
-  } else {
-    slot = (int64_t)s * p.map.nseg;
-    len = p.map.len;
-  }
-  float h = p.state_in ? p.state_in[((int64_t)s * p.heads + head) * kv + e] : 0.f;
-  const int64_t step = p.heads * kv;
-  float* u = p.seg_state + slot * step + head * kv + e;
-  float add = len > p.map.seg_len ? *u : 0.f;  // what the segment adds
-  for (int64_t at = 0; at + p.map.seg_len < len; at += p.map.seg_len, ++slot) {
-    h = fmaf(p.seg_decay[slot * p.heads + head], h, add);
-    u += step;
-    if (at + 2 * p.map.seg_len < len) add = *u;
-    *u = h;  // the state before the next segment
-  }
 }
 
 namespace {
 
-template <typename E, int C, int KP, int VT>
-hipError_t launch_kv(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(kAttThreads);
-  if (pl.split) {
-    attention_kernel<E, C, KP, VT, true><<<grid, block, 0, st>>>(p);
-    const int64_t blocks = ((int64_t)p.K * p.V + kAttThreads - 1) / kAttThreads;
-    attention_carry<<<dim3((unsigned)(blocks * p.heads * p.map.sequences)), block, 0, st>>>(p);
+template <typename E, int C, int VT>
+hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
+  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(256);
+  switch (pl.kp) {
+    case 32: attention_kernel<E, C, 32, VT><<<grid, block, 0, st>>>(p); break;
+    case 64: attention_kernel<E, C, 64, VT><<<grid, block, 0, st>>>(p); break;
+    case 128: attention_kernel<E, C, 128, VT><<<grid, block, 0, st>>>(p); break;
+    default: attention_kernel<E, C, 256, VT><<<grid, block, 0, st>>>(p);
   }
-  attention_kernel<E, C, KP, VT, false><<<grid, block, 0, st>>>(p);
   return hipGetLastError();
 }
 
-template <typename E, int C, int VT>
-hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
-  switch (pl.kp) {
-    case 32: return launch_kv<E, C, 32, VT>(p, pl, st);
-    case 64: return launch_kv<E, C, 64, VT>(p, pl, st);
-    case 128: return launch_kv<E, C, 128, VT>(p, pl, st);
-    default: return launch_kv<E, C, 256, VT>(p, pl, st);
-  }
-}
-
-}  // namespace
-
-AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
-                             bool packed, int dtype) {
+// The plan for tiles of vt value columns and segments of about tokens x heads x
+// tiles / want tokens: `want` workgroups, of four chunks each at least.
+AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
+                        bool packed, int dtype, int vt, int64_t want) {
   AttentionPlan pl;
   pl.kp = key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
-  pl.vt = 64;
-  pl.vtiles = (int)((value_dim + pl.vt - 1) / pl.vt);
-  const int64_t chunk = dtype == 1 ? 64 : 32;
-  // about two workgroups per CU, at least four chunks each
-  const int64_t want = 512;
+  pl.vt = vt;
+  pl.vtiles = (int)((value_dim + vt - 1) / vt);
+  const int64_t chunk = pl.chunk = dtype == 1 ? 64 : 32;
   int64_t seg = (tokens * heads * pl.vtiles + want - 1) / want;
   if (seg < 4 * chunk) seg = 4 * chunk;
   seg = (seg + chunk - 1) / chunk * chunk;
@@ -316,7 +262,26 @@ AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, i
   pl.seg_len = seg;
   pl.nseg = (int)((longest + seg - 1) / seg);
   pl.slots = packed ? tokens / seg + sequences : sequences * pl.nseg;
+  pl.chunks = packed ? tokens / chunk + sequences : sequences * ((longest + chunk - 1) / chunk);
   return pl;
+}
+
+}  // namespace
+
+AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
+                             bool packed, int dtype) {
+  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, 64, 512);
+}
+
+AttentionPlan plan_attention_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim,
+                                      int64_t value_dim, bool packed, int dtype) {
+  // one tile of value columns where they fit: a second one would make dq and dk sums of two parts in memory
+  const int vt = value_dim <= 64 ? 64 : 128;
+  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, vt, vt == 64 ? 512 : 256);
+}
+
+SequenceMap sequence_map(const AttentionArgs& a, const AttentionPlan& pl) {
+  return SequenceMap{a.cu, a.tokens, pl.seg_len, (int)a.sequences, pl.nseg, a.cu ? 0 : a.tokens / a.sequences};
 }
 
 size_t attention_workspace_bytes(const AttentionPlan& pl, int64_t heads, int64_t key_dim, int64_t value_dim) {
@@ -332,7 +297,7 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& pl) {
   p.state_in = a.state_in;
   p.o = a.o;
   p.state_out = a.state_out;
-  p.map = SequenceMap{a.cu, a.tokens, pl.seg_len, (int)a.sequences, pl.nseg, a.cu ? 0 : a.tokens / a.sequences};
+  p.map = sequence_map(a, pl);
   for (int i = 0; i < 3; ++i) {
     p.q_stride[i] = a.q_stride[i];
     p.k_stride[i] = a.k_stride[i];
@@ -347,8 +312,27 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& pl) {
   p.scale = a.scale;
   p.split = pl.split;
   if (pl.split) {
-    p.seg_state = static_cast<float*>(a.workspace);
-    p.seg_decay = p.seg_state + pl.slots * a.heads * a.key_dim * a.value_dim;
+    StateParams s{};
+    s.k = a.k;
+    s.v = a.v;
+    s.g = a.log_decay;
+    s.seg_state = static_cast<float*>(a.workspace);
+    s.seg_decay = s.seg_state + pl.slots * a.heads * a.key_dim * a.value_dim;
+    s.map = p.map;
+    for (int i = 0; i < 3; ++i) {
+      s.k_stride[i] = a.k_stride[i];
+      s.v_stride[i] = a.v_stride[i];
+      s.g_stride[i] = a.g_stride[i];
+    }
+    s.groups = p.groups;
+    s.heads = p.heads;
+    s.K = p.K;
+    s.V = p.V;
+    s.vtiles = pl.vtiles;
+    p.seg_state = s.seg_state;
+    hipError_t e = launch_state_pass(kSegmentStates, s, pl, a.dtype, a.stream);
+    if (e == hipSuccess) e = launch_state_carry(false, s, a.state_in, a.stream);
+    if (e != hipSuccess) return e;
   }
   if (a.dtype == 1) return launch_k<uint16_t, 64, 64>(p, pl, a.stream);
   return launch_k<float, 32, 64>(p, pl, a.stream);

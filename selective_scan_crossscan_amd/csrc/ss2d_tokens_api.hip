@@ -96,9 +96,113 @@ ss2d::AttentionPlan plan_of(const ss2d_attention_sizes* z, bool packed, int dtyp
   return ss2d::plan_attention(z->sequences, z->tokens, z->heads, z->key_dim, z->value_dim, packed, dtype);
 }
 
+ss2d::AttentionPlan backward_plan_of(const ss2d_attention_sizes* z, bool packed, int dtype) {
+  return ss2d::plan_attention_backward(z->sequences, z->tokens, z->heads, z->key_dim, z->value_dim, packed, dtype);
+}
+
+ss2d::AttentionArgs attention_args(const void* q, const void* k, const void* v, const float* log_decay,
+                                   const float* state_in, const int32_t* cu_seqlens, void* o, float* state_out,
+                                   const ss2d_attention_sizes& z, float scale, int dtype, void* workspace,
+                                   void* stream) {
+  ss2d::AttentionArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.log_decay = log_decay;
+  a.state_in = state_in;
+  a.cu = cu_seqlens;
+  a.o = o;
+  a.state_out = state_out;
+  a.sequences = z.sequences;
+  a.tokens = z.tokens;
+  a.groups = z.groups;
+  a.heads = z.heads;
+  a.key_dim = z.key_dim;
+  a.value_dim = z.value_dim;
+  for (int i = 0; i < 3; ++i) {
+    a.q_stride[i] = z.q_stride[i];
+    a.k_stride[i] = z.k_stride[i];
+    a.v_stride[i] = z.v_stride[i];
+    a.g_stride[i] = z.decay_stride[i];
+  }
+  a.scale = scale;
+  a.dtype = dtype;
+  a.workspace = workspace;
+  a.stream = static_cast<hipStream_t>(stream);
+  return a;
+}
+
+// Whether a plan's launches fit a grid.
+bool grid_ok(const ss2d::AttentionPlan& pl, const ss2d_attention_sizes& z) {
+  return pl.slots * z.heads * pl.vtiles <= INT32_MAX &&
+         z.sequences * z.heads * ((z.key_dim * z.value_dim + 255) / 256) <= INT32_MAX;
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t ss2d_linear_attention_backward_workspace(const ss2d_attention_sizes* sizes, int packed, int dtype) {
+  const int rc = check_attention_sizes(sizes, packed != 0, dtype);
+  if (rc != SS2D_OK) return rc;
+  const ss2d::AttentionPlan pl = backward_plan_of(sizes, packed != 0, dtype);
+  return (int64_t)ss2d::attention_backward_workspace_bytes(pl, sizes->tokens, sizes->groups, sizes->heads,
+                                                           sizes->key_dim, sizes->value_dim);
+}
+
+int ss2d_linear_attention_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                                   const float* state_in, const int32_t* cu_seqlens, const void* d_o,
+                                   const float* dstate_out, void* dq, void* dk, void* dv, float* dlog_decay,
+                                   float* dstate_in, const ss2d_attention_sizes* sizes, float scale, int dtype,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv || !dlog_decay || !sizes) return SS2D_ERR_NULL;
+  const bool packed = cu_seqlens != nullptr;
+  int rc = check_attention_sizes(sizes, packed, dtype);
+  if (rc != SS2D_OK) return rc;
+  const ss2d_attention_sizes& z = *sizes;
+  const int64_t e = elem_bytes(dtype), st = z.sequences * z.heads * z.key_dim * z.value_dim * 4;
+  const Range in[8] = {{q, extent(z.q_stride, z.sequences, z.tokens, z.groups, z.key_dim, packed, e)},
+                       {k, extent(z.k_stride, z.sequences, z.tokens, z.groups, z.key_dim, packed, e)},
+                       {v, extent(z.v_stride, z.sequences, z.tokens, z.heads, z.value_dim, packed, e)},
+                       {log_decay, extent(z.decay_stride, z.sequences, z.tokens, z.heads, 1, packed, 4)},
+                       {d_o, extent(z.do_stride, z.sequences, z.tokens, z.heads, z.value_dim, packed, e)},
+                       {cu_seqlens, (z.sequences + 1) * 4},
+                       {state_in, st},
+                       {dstate_out, st}};
+  for (const Range& r : in)
+    if (r.bytes < 0) return SS2D_ERR_SHAPE;
+  const ss2d::AttentionPlan pl = backward_plan_of(sizes, packed, dtype);
+  const int64_t need = ss2d_linear_attention_backward_workspace(sizes, packed ? 1 : 0, dtype);
+  if (!grid_ok(pl, z) || z.tokens * z.groups * z.key_dim / 256 >= INT32_MAX) return SS2D_ERR_SHAPE;
+  const Range out[6] = {{dq, z.tokens * z.groups * z.key_dim * e},   {dk, z.tokens * z.groups * z.key_dim * e},
+                        {dv, z.tokens * z.heads * z.value_dim * e},  {dlog_decay, z.tokens * z.heads * 4},
+                        {dstate_in, st},                             {need > 0 ? workspace : nullptr, need}};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return SS2D_ERR_ALIAS;
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(out[i], out[j])) return SS2D_ERR_ALIAS;
+  }
+  if (misaligned(q, e) || misaligned(k, e) || misaligned(v, e) || misaligned(d_o, e) || misaligned(dq, e) ||
+      misaligned(dk, e) || misaligned(dv, e) || misaligned(log_decay, 4) || misaligned(dlog_decay, 4) ||
+      misaligned(state_in, 4) || misaligned(dstate_out, 4) || misaligned(dstate_in, 4) || misaligned(cu_seqlens, 4))
+    return SS2D_ERR_ALIGN;
+  rc = check_workspace(workspace, workspace_bytes, need);
+  if (rc != SS2D_OK) return rc;
+  rc = check_device();
+  if (rc != SS2D_OK) return rc;
+  ss2d::AttentionBackwardArgs a{};
+  a.f = attention_args(q, k, v, log_decay, state_in, cu_seqlens, nullptr, nullptr, z, scale, dtype, workspace, stream);
+  a.d_o = d_o;
+  for (int i = 0; i < 3; ++i) a.do_stride[i] = z.do_stride[i];
+  a.dstate_out = dstate_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dlog_decay = dlog_decay;
+  a.dstate_in = dstate_in;
+  return finish(ss2d::launch_attention_backward(a, pl));
+}
 
 int64_t ss2d_linear_attention_workspace(const ss2d_attention_sizes* sizes, int packed, int dtype) {
   const int rc = check_attention_sizes(sizes, packed != 0, dtype);
@@ -127,9 +231,7 @@ int ss2d_linear_attention(const void* q, const void* k, const void* v, const flo
   const Range ro{o, z.tokens * z.heads * z.value_dim * e}, rs{state_out, in[5].bytes};
   const ss2d::AttentionPlan pl = plan_of(sizes, packed, dtype);
   const int64_t need = (int64_t)ss2d::attention_workspace_bytes(pl, z.heads, z.key_dim, z.value_dim);
-  if (pl.slots * z.heads * pl.vtiles > INT32_MAX ||
-      z.sequences * z.heads * ((z.key_dim * z.value_dim + 255) / 256) > INT32_MAX)
-    return SS2D_ERR_SHAPE;
+  if (!grid_ok(pl, z)) return SS2D_ERR_SHAPE;
   const Range rw{need > 0 ? workspace : nullptr, need};
   for (int i = 0; i < 6; ++i)
     if (overlap(ro, in[i]) || overlap(rw, in[i]) || (i < 5 ? overlap(rs, in[i]) : partly(rs, in[i])))
@@ -142,31 +244,8 @@ int ss2d_linear_attention(const void* q, const void* k, const void* v, const flo
   if (rc != SS2D_OK) return rc;
   rc = check_device();
   if (rc != SS2D_OK) return rc;
-  ss2d::AttentionArgs a{};
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.log_decay = log_decay;
-  a.state_in = state_in;
-  a.cu = cu_seqlens;
-  a.o = o;
-  a.state_out = state_out;
-  a.sequences = z.sequences;
-  a.tokens = z.tokens;
-  a.groups = z.groups;
-  a.heads = z.heads;
-  a.key_dim = z.key_dim;
-  a.value_dim = z.value_dim;
-  for (int i = 0; i < 3; ++i) {
-    a.q_stride[i] = z.q_stride[i];
-    a.k_stride[i] = z.k_stride[i];
-    a.v_stride[i] = z.v_stride[i];
-    a.g_stride[i] = z.decay_stride[i];
-  }
-  a.scale = scale;
-  a.dtype = dtype;
-  a.workspace = workspace;
-  a.stream = static_cast<hipStream_t>(stream);
+  const ss2d::AttentionArgs a = attention_args(q, k, v, log_decay, state_in, cu_seqlens, o, state_out, z, scale, dtype,
+                                               workspace, stream);
   return finish(ss2d::launch_attention(a, pl));
 }
 

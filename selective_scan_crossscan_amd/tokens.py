@@ -147,6 +147,38 @@ def linear_attention(q, k, v, log_decay, state=None, cu_seqlens=None, scale: flo
     return (out, last) if final_state else out
 
 
+def linear_attention_backward(q, k, v, log_decay, do, state=None, dfinal_state=None, cu_seqlens=None,
+                              scale: float = 1.0, stream=None) -> dict:
+    """Gradients of linear_attention (ss2d_linear_attention_backward): do the gradient of o (v's shape and dtype, any
+    strides with a dense last axis), dfinal_state that of the final states (S,H,K,V) float32 or None.
+
+    Returns dq, dk, dv (shapes and dtypes of q, k, v, contiguous), dlog_decay (float32, one value per token and head)
+    and, with a state, dstate.  Values of packed tokens in no sequence are undefined.
+    """
+    if stream is not None:
+        return _on_stream(stream, v.device, linear_attention_backward, q, k, v, log_decay, do, state, dfinal_state,
+                          cu_seqlens, scale)
+    sizes, lead, S, G, H, K, V, code = _attention_sizes(q, k, v, log_decay, cu_seqlens, do)
+    device = v.device
+    out = {"dq": torch.empty(q.shape, dtype=v.dtype, device=device),
+           "dk": torch.empty(q.shape, dtype=v.dtype, device=device),
+           "dv": torch.empty(v.shape, dtype=v.dtype, device=device),
+           "dlog_decay": torch.empty(lead + (H,), dtype=torch.float32, device=device)}
+    for name, t in (("state", state), ("dfinal_state", dfinal_state)):
+        if t is not None:
+            _require(name, t, device, torch.float32, (S, H, K, V))
+    if state is not None:
+        out["dstate"] = torch.empty((S, H, K, V), dtype=torch.float32, device=device)
+    L = lib()
+    nbytes = L.ss2d_linear_attention_backward_workspace(sizes, 0 if cu_seqlens is None else 1, code)
+    ws, at = _workspace(nbytes, device)
+    _call(L.ss2d_linear_attention_backward, device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          _ptr(state), _ptr(cu_seqlens), do.data_ptr(), _ptr(dfinal_state), out["dq"].data_ptr(),
+          out["dk"].data_ptr(), out["dv"].data_ptr(), out["dlog_decay"].data_ptr(), _ptr(out.get("dstate")), sizes,
+          scale, code, at, nbytes)
+    return out
+
+
 def linear_attention_step(q, k, v, log_decay, state, state_index=None, scale: float = 1.0, out=None, stream=None):
     """One token per row over a cache of states, updated in place (ss2d_linear_attention_step).
 
