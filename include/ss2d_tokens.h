@@ -5,7 +5,9 @@
  *       with one decay for a head's whole state: forward over prompts, its
  *       gradients, and one token per row over a cache of states;
  *   root-mean-square norm                    with the residual's addition, in the
- *       storage type or in 8 bits with scales, and its gradients.
+ *       storage type or in 8 bits with scales, and its gradients;
+ *   8-bit matrix product                     e4m3 values with a scale per block
+ *       of 128, what the norm's 8-bit output is projected with.
  *
  * Status codes, the storage types (ss2d_dtype) and the error texts are those of
  * ss2d.h.  Every tensor pointer is DEVICE memory owned by the caller.  Arguments
@@ -163,6 +165,23 @@ int ss2d_rms_norm_backward(const void* r, const float* weight, const void* dy, c
                            void* dx, float* dweight, int64_t rows, int64_t dim, int dtype, void* workspace,
                            int64_t workspace_bytes, void* stream);
 int64_t ss2d_rms_norm_backward_workspace(int64_t rows, int64_t dim, int dtype);
+
+/*
+ * ss2d_matmul_fp8 -- out = a b', both in e4m3 with scales:
+ *     out[m, n] = sum_j a_scales[m, j] b_scales[n / 128, j] sum_{k in block j} a[m, k] b[n, k],
+ * block j the inner indices 128 j .. 128 j + 127 (the last may be shorter).
+ *   a         [m, k] e4m3         a_scales  [m, ceil(k/128)] fp32
+ *   b         [n, k] e4m3         b_scales  [ceil(n/128), ceil(k/128)] fp32
+ *   out       [m, n] dtype (fp32 or bf16, rounded once)
+ * All dense; out must not overlap an input.  Sums are fp32 on the matrix cores, in a
+ * fixed order.  For a bf16 output the products run in 8 bits, where the instruction
+ * drops, in each group of eight inner indices, what lies below 2^-13 of the group's
+ * largest product; for an fp32 output they run in bf16 (exact values), all bits kept.  m, n >= 1 and at most 2^30, k 1..2^20 (SS2D_ERR_SHAPE
+ * otherwise).  One kernel, no workspace; any k and any addresses, fastest with k a
+ * multiple of 16 and a and b aligned to 16 bytes.
+ */
+int ss2d_matmul_fp8(const void* a, const float* a_scales, const void* b, const float* b_scales, void* out, int64_t m,
+                    int64_t n, int64_t k, int dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,11 +16,11 @@ __all__ = ["forward", "ss2d_forward", "project", "ss2d_project", "forward_from_x
            "channel_last", "ss2d_channel_last", "backward", "ss2d_backward", "measure_peaks", "describe", "bidir_forward", "ss2d_bidir_forward", "bidir_backward", "ss2d_bidir_backward", "ss2d_forward_noalloc", "trim_memory", "status_string", "version", "library_path", "lib",
            "SS2D_F32", "SS2D_BF16", "SS2DError",
            "linear_attention", "linear_attention_backward", "linear_attention_step", "rms_norm",
-           "rms_norm_fp8", "rms_norm_backward"]
+           "rms_norm_fp8", "rms_norm_backward", "matmul_fp8"]
 
 # The token-sequence operators (tokens.py), imported with torch when first used.
 _TOKENS = ("linear_attention", "linear_attention_backward", "linear_attention_step", "rms_norm",
-           "rms_norm_fp8", "rms_norm_backward")
+           "rms_norm_fp8", "rms_norm_backward", "matmul_fp8")
 
 
 def __getattr__(name):

@@ -87,6 +87,8 @@ def lib():
             L.ss2d_linear_attention_backward_workspace.restype = i64
             L.ss2d_linear_attention_step.argtypes = [vp] * 7 + [i64] * 9 + [f32, ci, vp]
             L.ss2d_linear_attention_step.restype = ci
+            L.ss2d_matmul_fp8.argtypes = [vp] * 5 + [i64] * 3 + [ci, vp]
+            L.ss2d_matmul_fp8.restype = ci
             L.ss2d_rms_norm.argtypes = [vp] * 3 + [f32] + [vp] * 3 + [i64] * 2 + [ci, vp]
             L.ss2d_rms_norm.restype = ci
             L.ss2d_rms_norm_backward.argtypes = [vp] * 4 + [f32] + [vp] * 2 + [i64] * 2 + [ci, vp, i64, vp]

@@ -57,6 +57,18 @@ struct StepArgs {
 };
 hipError_t launch_attention_step(const StepArgs& a);
 
+struct MatmulArgs {
+  const void* a;          // (m, k) e4m3
+  const float* a_scales;  // (m, ceil(k / 128))
+  const void* b;          // (n, k) e4m3
+  const float* b_scales;  // (ceil(n / 128), ceil(k / 128))
+  void* out;              // (m, n)
+  int64_t m, n, k;
+  int dtype;
+  hipStream_t stream;
+};
+hipError_t launch_matmul_fp8(const MatmulArgs& a);
+
 // ------------------------------------------------------------------ device helpers
 namespace tok {
 

@@ -337,4 +337,23 @@ int ss2d_rms_norm_backward(const void* r, const float* weight, const void* dy, c
   return finish(ss2d::launch_rms_norm_backward(a));
 }
 
+int ss2d_matmul_fp8(const void* a, const float* a_scales, const void* b, const float* b_scales, void* out, int64_t m,
+                    int64_t n, int64_t k, int dtype, void* stream) {
+  if (!a || !a_scales || !b || !b_scales || !out) return SS2D_ERR_NULL;
+  constexpr int64_t most = (int64_t)1 << 30;
+  if (m < 1 || m > most || n < 1 || n > most || k < 1 || k > (1 << 20)) return SS2D_ERR_SHAPE;
+  if (((m + 15) / 16) * ((n + 15) / 16) > INT32_MAX) return SS2D_ERR_SHAPE;  // workgroups
+  if (!dtype_ok(dtype)) return SS2D_ERR_DTYPE;
+  const int64_t e = elem_bytes(dtype), kb = (k + 127) / 128;
+  const Range ro{out, m * n * e};
+  for (const Range& r : {Range{a, m * k}, Range{b, n * k}, Range{a_scales, m * kb * 4},
+                         Range{b_scales, (n + 127) / 128 * kb * 4}})
+    if (overlap(ro, r)) return SS2D_ERR_ALIAS;
+  if (misaligned(out, e) || misaligned(a_scales, 4) || misaligned(b_scales, 4)) return SS2D_ERR_ALIGN;
+  const int rc = check_device();
+  if (rc != SS2D_OK) return rc;
+  const ss2d::MatmulArgs x{a, a_scales, b, b_scales, out, m, n, k, dtype, static_cast<hipStream_t>(stream)};
+  return finish(ss2d::launch_matmul_fp8(x));
+}
+
 }  // extern "C"

@@ -2,8 +2,9 @@
 
 Linear attention with a decay per head (prompts, gradients, single tokens over a
 cache of states), the root-mean-square norm with the residual's addition (storage
-type or 8 bits with scales, gradients).  As in the rest of the package the binding
-only checks and marshals arguments, and there is no CPU fallback.
+type or 8 bits with scales, gradients) and the 8-bit matrix product with a scale
+per block of 128.  As in the rest of the package the binding only checks and
+marshals arguments, and there is no CPU fallback.
 
 Every function runs on `stream`, or on the current stream of the tensors' device,
 and allocates its outputs and workspace from torch's allocator on that stream, so
@@ -286,3 +287,34 @@ def rms_norm_backward(r, weight, dy, dresidual=None, eps: float = 1e-6, stream=N
     _call(L.ss2d_rms_norm_backward, device, r.data_ptr(), _ptr(weight), dy.data_ptr(), _ptr(dresidual), eps,
           dx.data_ptr(), _ptr(dweight), rows, dim, code, at, nbytes)
     return {"dx": dx} if weight is None else {"dx": dx, "dweight": dweight}
+
+
+# ------------------------------------------------------------------ 8-bit matrix product
+def matmul_fp8(a, a_scales, b, b_scales, out_dtype=torch.bfloat16, out=None, stream=None):
+    """a b' in 8 bits (ss2d_matmul_fp8): a (...,K), b (N,K) float8_e4m3fn with a scale per 128 inner indices,
+    a_scales (...,ceil(K/128)) for every row of a, b_scales (ceil(N/128),ceil(K/128)) for blocks of 128 x 128 of b,
+    float32, as rms_norm_fp8 and block-quantised weights give them.  All contiguous.
+    Returns (...,N) in out_dtype (float32 or bfloat16), or in `out` and its dtype if given.
+    """
+    if stream is not None:
+        return _on_stream(stream, a.device, matmul_fp8, a, a_scales, b, b_scales, out_dtype, out)
+    device = a.device
+    if a.dim() < 1 or b.dim() != 2:
+        raise ValueError("a must be (...,K) and b (N,K)")
+    N, K = b.shape
+    lead = tuple(a.shape[:-1])
+    blocks = (K + 127) // 128
+    _require("a", a, device, torch.float8_e4m3fn, lead + (K,))
+    _require("b", b, device, torch.float8_e4m3fn)
+    _require("a_scales", a_scales, device, torch.float32, lead + (blocks,))
+    _require("b_scales", b_scales, device, torch.float32, ((N + 127) // 128, blocks))
+    if out is None:
+        out = torch.empty(lead + (N,), dtype=out_dtype, device=device)
+    else:
+        _require("out", out, device, out.dtype, lead + (N,))
+    M = 1
+    for n in lead:
+        M *= n
+    _call(lib().ss2d_matmul_fp8, device, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
+          out.data_ptr(), M, N, K, _code(out))
+    return out
