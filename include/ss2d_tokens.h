@@ -34,7 +34,8 @@ extern "C" {
 
 /*
  * Sizes and strides of linear attention.  Strides are in elements, for each of
- * sequence, token and head, at least 0 (0 repeats one value along that axis);
+ * sequence, token and head, at least 0 (0 repeats one value along that axis) and
+ * for tokens at most 2^24;
  * the innermost axis (key_dim or value_dim) is dense.  With packed sequences the
  * sequence stride is unused.  do_stride is used by the backward only.
  */

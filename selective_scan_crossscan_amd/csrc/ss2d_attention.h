@@ -276,41 +276,64 @@ __device__ __forceinline__ Frag<float> frag_col_split(const Tile<float, R, C>& m
   return f;
 }
 
-// A tile on its way from global memory to LDS, in registers.
+// A tile on its way from global memory to LDS, in registers, by THREADS threads
+// with 16 bytes a piece.  Every piece is loaded, with no branch around it, so all
+// are in flight together: rows behind the last read the last one, pieces behind
+// the row's end and the piece across it read the row's last 16 bytes, and store()
+// puts zeros or the piece's own part in their place.  Rows shorter than 16 bytes
+// are loaded value by value.
 template <typename E, int ROWS, int COLS, int THREADS = 256>
 struct TileLoad {
-  static constexpr int kPer = 16 / (int)sizeof(E);  // elements per 16 bytes
+  static constexpr int kPer = 16 / (int)sizeof(E);  // elements per piece
   static constexpr int kRowPieces = COLS / kPer;
   static constexpr int kPieces = (ROWS * kRowPieces + THREADS - 1) / THREADS;
   Bytes16 r[kPieces];
 
-  // Rows 0..nrows-1 of `base` (stride elements apart), columns 0..ncols-1; the rest is 0.
+  // nrows >= 1 rows of `base`, stride elements apart, of ncols >= 1 columns.
   __device__ __forceinline__ void load(const E* base, int64_t stride, int nrows, int ncols) {
+    if (ncols >= kPer) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int idx = threadIdx.x + i * THREADS;
-      const int row = idx / kRowPieces, c = (idx % kRowPieces) * kPer;
-      r[i] = Bytes16{{0, 0, 0, 0}};
-      if (row < nrows && c < ncols) {
-        const E* p = base + row * stride + c;
-        if (ncols - c >= kPer) {
-          r[i] = *reinterpret_cast<const Bytes16*>(p);
-        } else {
-          E e[kPer];
+      for (int i = 0; i < kPieces; ++i) {
+        const int idx = threadIdx.x + i * THREADS;
+        const int row = min(idx / kRowPieces, nrows - 1), c = min((idx % kRowPieces) * kPer, ncols - kPer);
+        // 32-bit offsets: a chunk's rows span less than 2^31 elements (the strides are checked)
+        r[i] = *reinterpret_cast<const Bytes16*>(base + ((uint32_t)row * (uint32_t)stride + (uint32_t)c));
+      }
+    } else {
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) e[j] = c + j < ncols ? p[j] : (E)0;
-          __builtin_memcpy(&r[i], e, 16);
-        }
+      for (int i = 0; i < kPieces; ++i) {
+        const int idx = threadIdx.x + i * THREADS, row = min(idx / kRowPieces, nrows - 1);
+        E e[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) e[j] = base[(uint32_t)row * (uint32_t)stride + (uint32_t)min(j, ncols - 1)];
+        __builtin_memcpy(&r[i], e, 16);
       }
     }
   }
-  __device__ __forceinline__ void store(Tile<E, ROWS, COLS>& m) const {
+  // The same nrows and ncols.
+  __device__ __forceinline__ void store(Tile<E, ROWS, COLS>& m, int nrows, int ncols) const {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int idx = threadIdx.x + i * THREADS;
       const int row = idx / kRowPieces, c = (idx % kRowPieces) * kPer;
-      if (ROWS * kRowPieces % THREADS == 0 || row < ROWS)
-        __builtin_memcpy(__builtin_assume_aligned(&m.e[row * m.stride + c], 16), &r[i], 16);
+      if (ROWS * kRowPieces % THREADS != 0 && row >= ROWS) continue;
+      E* to = &m.e[row * m.stride + c];
+      const int n = row < nrows ? ncols - c : 0;  // elements of the piece that are there
+      Bytes16 x = r[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.w[j] = n > 0 ? x.w[j] : 0;
+      __builtin_memcpy(__builtin_assume_aligned(to, 16), &x, 16);
+      if (n > 0 && n < kPer) {  // across the end: the loaded bytes end where the row does
+        E e[kPer];
+        __builtin_memcpy(e, &r[i], 16);
+        const int shift = ncols >= kPer ? kPer - n : 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (j >= shift && j - shift < n) to[j - shift] = e[j];
+#pragma unroll
+        for (int j = 1; j < kPer; ++j)
+          if (j >= n) to[j] = (E)0;
+      }
     }
   }
 };
@@ -332,12 +355,7 @@ struct Decays {
 template <int C>
 __device__ __forceinline__ void scan_decays(float g, Decays<C>& d) {
   const int lane = threadIdx.x & 63;
-  double s = (double)clamp_log_decay(g) * 1.4426950408889634074;
-#pragma unroll
-  for (int m = 1; m < C; m <<= 1) {
-    const double u = __shfl_up(s, m);
-    if (lane >= m) s += u;
-  }
+  const double s = wave_scan((double)clamp_log_decay(g) * 1.4426950408889634074);
   if (lane < C) {
     const double w = rint(s);
     d.whole[lane] = (float)w;

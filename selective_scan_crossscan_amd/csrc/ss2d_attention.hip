@@ -7,10 +7,10 @@
 //   o_i = scale (sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j + exp(G_i) h' q_i),
 //   h  <- exp(G_last) h + sum_j exp(G_last - G_j) k_j v_j'.
 //
-// One workgroup of four waves walks a segment of one sequence and head for VT
-// value columns, chunk after chunk; the state never leaves its registers.  Each
-// wave owns VT / 4 value columns: their part of the state (all key rows, fp32,
-// as result tiles whose rows are the key index), of v and of the output.  The
+// One workgroup walks a segment of one sequence and head for VT value columns,
+// chunk after chunk; the state never leaves its registers.  Each wave owns 16
+// value columns: their part of the state (all key rows, fp32, as result tiles
+// whose rows are the key index), of v and of the output.  The
 // scores are the one thing waves share: each computes 16 tokens' (transposed,
 // so that a lane has four consecutive keys' scores of one token), applies decay
 // and mask, and puts them into LDS.  The output is formed transposed too, four
@@ -41,10 +41,11 @@ struct AttentionParams {
 };
 
 template <typename E, int C, int KP, int VT>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionParams p) {
-  constexpr int NI = C / 16;        // token tiles
-  constexpr int NK = KP / 16;       // key tiles
-  constexpr int NV = VT / 64;       // value tiles of a wave
+__global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
+  constexpr int NW = VT / 16, THREADS = NW * 64;
+  constexpr int NI = C / 16;                            // token tiles
+  constexpr int NK = KP / 16;                           // key tiles
+  constexpr int JS = NW / NI < NI ? NW / NI : NI;       // waves that share 16 tokens' scores
   constexpr int PF = kFullParts<E>, PH = kHalfParts<E>;
   __shared__ Tile<E, C, KP> qs, ks;
   __shared__ Tile<E, C, VT> vs;
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionParams p) {
   if (!find_segment(p.map, slot, seg)) return;
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
-  const int vw = wave * (VT / 4);  // this wave's first column in the tile
+  const int vw = wave * 16;        // this wave's first column in the tile
   const bool active = vw < nv;     // it has columns at all
   const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
   const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + first * p.q_stride[1] + group * p.q_stride[2];
@@ -67,24 +68,20 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionParams p) {
   const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + first * p.v_stride[1] + head * p.v_stride[2] + v0;
   const float* gb = p.g + sq * p.g_stride[0] + first * p.g_stride[1] + head * p.g_stride[2];
 
-  // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
-  f32x4 h[NK][NV];
+  // the state: rows 16 kt + 4 g + r, column vw + l
+  f32x4 h[NK];
   const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
-  {
-    const float* from = p.split && seg.begin > 0 ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
+  const float* from = p.split && seg.begin > 0 ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
 #pragma unroll
-    for (int kt = 0; kt < NK; ++kt)
+  for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
-          h[kt][t][r] = from && k < K && v < nv ? from[(int64_t)k * p.V + v0 + v] : 0.f;
-        }
-  }
+    for (int r = 0; r < 4; ++r) {
+      const int k = kt * 16 + 4 * g + r;
+      h[kt][r] = from && k < K && vw + l < nv ? from[(int64_t)k * p.V + v0 + vw + l] : 0.f;
+    }
 
-  TileLoad<E, C, KP> ql, kl;
-  TileLoad<E, C, VT> vl;
+  TileLoad<E, C, KP, THREADS> ql, kl;
+  TileLoad<E, C, VT, THREADS> vl;
   float gl = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
@@ -97,144 +94,106 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionParams p) {
   for (int64_t at = seg.begin; at < seg.end; at += C) {
     const int n = (int)min((int64_t)C, seg.end - at);
     __syncthreads();  // the previous chunk has been read
-    ql.store(qs);
-    kl.store(ks);
-    vl.store(vs);
+    ql.store(qs, n, K);
+    kl.store(ks, n, K);
+    vl.store(vs, n, nv);
     if (wave == 0) scan_decays<C>(gl, dec);
     __syncthreads();
     if (at + C < seg.end) fetch(at + C);
 
-    // scores, transposed: rows j (keys), columns i (tokens); 16 tokens per wave (two waves per 16 where C = 32)
-    const int it = NI == 4 ? wave : wave >> 1;
-    f32x4 s[NI];
-#pragma unroll
-    for (int jt = 0; jt < NI; ++jt) s[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < KP; c += 32) {
-      const Frag<E> b = frag_row(qs, it * 16 + l, c);
+    // scores, transposed (rows j, columns i): 16 tokens i per JS waves, which take every JS-th tile of keys j
+    {
+      const int it = wave % NI, share = wave / NI, i = it * 16 + l;
 #pragma unroll
       for (int jt = 0; jt < NI; ++jt)
-        if (jt <= it && (NI == 4 || jt == (wave & 1))) s[jt] = mma(frag_row(ks, jt * 16 + l, c), b, s[jt]);
-    }
-    const int i = it * 16 + l;
+        if (share < JS && jt % JS == share && jt <= (it | 1)) {  // the last may be all masked: pairs are read
+          f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (jt <= it)
 #pragma unroll
-    for (int jt = 0; jt < NI; ++jt)
-      if (jt <= (it | 1) && (NI == 4 || jt == (wave & 1))) {  // the last may be all masked: the output reads pairs
-        f32x4 w;
+            for (int c = 0; c < KP; c += 32) s = mma(frag_row(ks, jt * 16 + l, c), frag_row(qs, i, c), s);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = jt * 16 + 4 * g + r;
-          w[r] = j <= i ? s[jt][r] * (p.scale * dec.between(i, j)) : 0.f;
+          for (int r = 0; r < 4; ++r) {
+            const int j = jt * 16 + 4 * g + r;
+            s[r] = j <= i ? s[r] * (p.scale * dec.between(i, j)) : 0.f;
+          }
+          put4(&ps.e[i * ps.stride + jt * 16 + 4 * g], s);
         }
-        put4(&ps.e[i * ps.stride + jt * 16 + 4 * g], w);
-      }
+    }
     __syncthreads();
 
     if (active) {
-      f32x4 o[NV][NI];
+      f32x4 o[NI];
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int x = 0; x < NI; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < NI; ++x) o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
       // h' q'
 #pragma unroll
       for (int c = 0; c < NK; c += 2) {
-        Frag<E> a[NV][PH];
+        Frag<E> a[PH];
+        float u[8];
 #pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float x[8];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] = h[c][t][r];
-            x[4 + r] = h[c + 1][t][r];
-          }
-          split_parts(x, a[t]);
+        for (int r = 0; r < 4; ++r) {
+          u[r] = h[c][r];
+          u[4 + r] = h[c + 1][r];
         }
+        split_parts(u, a);
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const Frag<E> b = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-          for (int t = 0; t < NV; ++t)
-#pragma unroll
-            for (int q = 0; q < PH; ++q) o[t][x] = mma(a[t][q], b, o[t][x]);
+          for (int q = 0; q < PH; ++q) o[x] = mma(a[q], b, o[x]);
         }
       }
-#pragma unroll
-      for (int x = 0; x < NI; ++x) {
-        const float f = p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) o[t][x] *= f;
-      }
-      // v' scores'
-#pragma unroll
-      for (int j = 0; j < NI; j += 2)
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          const Frag<E> a = frag_col_split(vs, j * 16, vw + t * 16);
-#pragma unroll
-          for (int x = j; x < NI; ++x) o[t][x] = mma(a, frag_row_split(ps, x * 16 + l, j * 16), o[t][x]);
-        }
-      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
 #pragma unroll
       for (int x = 0; x < NI; ++x)
-        if (x * 16 + l < n)
+        o[x] *= p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
+      // v' scores' for the output, k' (decayed v) for the state
+      const float all = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
 #pragma unroll
-          for (int t = 0; t < NV; ++t) {
-            const int v = vw + t * 16 + 4 * g;
-            store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[t][x]);
-          }
-    }
-
-    if (active) {
-      const float a = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int t = 0; t < NV; ++t) h[kt][t] *= a;
+      for (int kt = 0; kt < NK; ++kt) h[kt] *= all;
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        Frag<E> b[NV][PF];
+        const Frag<E> a = frag_col_split(vs, j * 16, vw);
 #pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float x[8];
-          frag_values(frag_col_split(vs, j * 16, vw + t * 16), x);
+        for (int x = j; x < NI; ++x) o[x] = mma(a, frag_row_split(ps, x * 16 + l, j * 16), o[x]);
+        Frag<E> b[PF];
+        float u[8];
+        frag_values(a, u);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] *= dec.between(C - 1, j * 16 + 4 * g + r);
-            x[4 + r] *= dec.between(C - 1, j * 16 + 16 + 4 * g + r);
-          }
-          split_parts(x, b[t]);
+        for (int r = 0; r < 4; ++r) {
+          u[r] *= dec.between(C - 1, j * 16 + 4 * g + r);
+          u[4 + r] *= dec.between(C - 1, j * 16 + 16 + 4 * g + r);
         }
+        split_parts(u, b);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
           const Frag<E> k = frag_col_split(ks, j * 16, kt * 16);
 #pragma unroll
-          for (int t = 0; t < NV; ++t)
-#pragma unroll
-            for (int q = 0; q < PF; ++q) h[kt][t] = mma(k, b[t][q], h[kt][t]);
+          for (int q = 0; q < PF; ++q) h[kt] = mma(k, b[q], h[kt]);
         }
       }
+      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
+      const int v = vw + 4 * g;
+#pragma unroll
+      for (int x = 0; x < NI; ++x)
+        if (x * 16 + l < n) store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[x]);
     }
   }
 
-  float* to = seg.last && p.state_out ? p.state_out + qh : nullptr;
-  if (to)
+  if (seg.last && p.state_out)
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
-          if (k < K && v < nv) to[(int64_t)k * p.V + v0 + v] = h[kt][t][r];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int k = kt * 16 + 4 * g + r;
+        if (k < K && vw + l < nv) p.state_out[qh + (int64_t)k * p.V + v0 + vw + l] = h[kt][r];
+      }
 }
 
 namespace {
 
 template <typename E, int C, int VT>
 hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(256);
+  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(VT * 4);
   switch (pl.kp) {
     case 32: attention_kernel<E, C, 32, VT><<<grid, block, 0, st>>>(p); break;
     case 64: attention_kernel<E, C, 64, VT><<<grid, block, 0, st>>>(p); break;
@@ -270,7 +229,7 @@ AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_
 
 AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
                              bool packed, int dtype) {
-  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, 64, 512);
+  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, value_dim <= 64 ? 64 : 128, 512);
 }
 
 AttentionPlan plan_attention_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim,
@@ -334,8 +293,9 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& pl) {
     if (e == hipSuccess) e = launch_state_carry(false, s, a.state_in, a.stream);
     if (e != hipSuccess) return e;
   }
-  if (a.dtype == 1) return launch_k<uint16_t, 64, 64>(p, pl, a.stream);
-  return launch_k<float, 32, 64>(p, pl, a.stream);
+  if (a.dtype == 1)
+    return pl.vt == 64 ? launch_k<uint16_t, 64, 64>(p, pl, a.stream) : launch_k<uint16_t, 64, 128>(p, pl, a.stream);
+  return pl.vt == 64 ? launch_k<float, 32, 64>(p, pl, a.stream) : launch_k<float, 32, 128>(p, pl, a.stream);
 }
 
 }  // namespace ss2d

@@ -52,18 +52,6 @@ struct BackwardParams {
   bool split;
 };
 
-// Sum over the 16 lanes of a group, in every lane.
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-// Sum over the four groups, in every lane.
-__device__ __forceinline__ float across_groups(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
-
 template <typename E, int C, int KP, int VT, int NW>
 __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardParams p) {
   constexpr int THREADS = NW * 64;
@@ -135,14 +123,9 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
     }
 #pragma unroll
     for (int w = 0; w < NW; ++w) x += xs[w];
-    float before = __shfl_up(e, 1);  // exclusive sum of e, inclusive sum of f from the end
-    if (lane == 0) before = 0.f;
-#pragma unroll
-    for (int m = 1; m < C; m <<= 1) {
-      const float u = __shfl_down(f, m), w = __shfl_up(before, m);
-      if (lane + m < C) f += u;
-      if (lane >= m) before += w;
-    }
+    float before = __shfl_up(e, 1);  // the sum of e before a token, that of f from it on (scanned mirrored)
+    before = wave_scan(lane == 0 ? 0.f : before);
+    f = __shfl(wave_scan(__shfl(f, 63 - lane)), 63 - lane);
     if (lane < n) {
       const int64_t token = seg.start + at + lane;
       const float r = (f + before) + x;
@@ -168,10 +151,10 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
     const int n = (int)min((int64_t)C, seg.end - at);
     __syncthreads();  // the chunk behind has been read
     if (wave == 0 && c + 1 < chunks) decay_gradient(at + C);
-    ql.store(qs);
-    kl.store(ks);
-    vl.store(vs);
-    dl.store(ds);
+    ql.store(qs, n, K);
+    kl.store(ks, n, K);
+    vl.store(vs, n, nv);
+    dl.store(ds, n, nv);
     if (wave == 0) scan_decays<C>(gl, dec);
     // the state before the chunk: rows v = 16 a + 4 g + r, own key columns
     f32x4 h[NV][OK];
@@ -217,11 +200,11 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          cols[r] = group_sum(cols[r]);
+          cols[r] = row16_sum(cols[r]);
           if (l == 0) wcol[wave][jt * 16 + 4 * g + r] = cols[r];
         }
       }
-      rows = across_groups(rows);
+      rows = across_rows(rows);
 #pragma unroll
       for (int x = 0; x < NI; ++x)
         if (g == 0) wrow[wave][x * 16 + l] = x == it ? rows : 0.f;
@@ -298,8 +281,8 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
       }
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
-      fsum[x] = across_groups(fsum[x]);
-      esum[x] = across_groups(esum[x]);
+      fsum[x] = across_rows(fsum[x]);
+      esum[x] = across_rows(esum[x]);
       if (g == 0) {
         fs[wave][x * 16 + l] = fsum[x];
         es[wave][x * 16 + l] = esum[x];

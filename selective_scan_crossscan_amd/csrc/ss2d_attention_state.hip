@@ -81,8 +81,9 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
       if (c + 1 == chunks) break;  // the state behind the last chunk is not needed
     }
     __syncthreads();  // the previous chunk has been read
-    kl.store(ks);
-    vl.store(vs);
+    const int n = (int)min((int64_t)C, seg.end - start_of(c));
+    kl.store(ks, n, K);
+    vl.store(vs, n, nv);
     if (wave == 0) scan_decays<C>(gl, dec);
     __syncthreads();
     if (c + 1 < chunks) fetch(start_of(c + 1));

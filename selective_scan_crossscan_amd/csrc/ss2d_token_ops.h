@@ -10,6 +10,7 @@ namespace ss2d {
 
 constexpr int kMaxKeyDim = 256;
 constexpr int kMaxValueDim = 1024;
+constexpr int64_t kMaxTokenStride = 1 << 24;  // 64 tokens' offsets fit 32 bits
 constexpr int kMaxNormDim = 16384;
 constexpr int kScaleBlock = 128;  // channels per scale of the 8-bit values
 
@@ -162,11 +163,45 @@ __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_bits_to_
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, 0.f); }
 
+// v moved across lanes by a DPP pattern; lanes without a source, and rows outside
+// ROWS, get 0.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, true));
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, ROWS, 0xf, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROWS, 0xf, true);
+  return __hiloint2double(hi, lo);
+}
+constexpr int kRowShr = 0x110, kRowRor = 0x120;  // + 1 .. 15: lanes of a row of 16 shifted up, rotated
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143;  // a row's (half's) last lane to the next row (half)
+
+// Sum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp<kRowRor + 8>(v);
+  v += dpp<kRowRor + 4>(v);
+  v += dpp<kRowRor + 2>(v);
+  return v + dpp<kRowRor + 1>(v);
+}
+// Sum over the lanes 16 apart, in every lane.
+__device__ __forceinline__ float across_rows(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
 // Sum over the 64 lanes of a wave, in every lane.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+__device__ __forceinline__ float wave_sum(float v) { return across_rows(row16_sum(v)); }
+
+// Inclusive sum over the lanes up to this one.
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+  v += dpp<kRowShr + 1>(v);
+  v += dpp<kRowShr + 2>(v);
+  v += dpp<kRowShr + 4>(v);
+  v += dpp<kRowShr + 8>(v);
+  v += dpp<kBcast15, 0xa>(v);  // rows 1 and 3
+  return v + dpp<kBcast31, 0xc>(v);  // rows 2 and 3
 }
 
 }  // namespace tok

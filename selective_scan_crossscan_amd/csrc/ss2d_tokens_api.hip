@@ -73,7 +73,7 @@ int64_t extent(const int64_t* stride, int64_t sequences, int64_t tokens, int64_t
   for (int i = 0; i < 3; ++i) {
     int64_t part;
     if (n[i] == 1) continue;
-    if (stride[i] < 0 || __builtin_mul_overflow(n[i] - 1, stride[i], &part) ||
+    if (stride[i] < 0 || (i == 1 && stride[i] > ss2d::kMaxTokenStride) || __builtin_mul_overflow(n[i] - 1, stride[i], &part) ||
         __builtin_add_overflow(last, part, &last))
       return -1;
   }
