@@ -60,6 +60,7 @@ struct AttentionPlan {
   int64_t chunks;   // chunks, an upper bound for packed sequences
   int nseg;         // per sequence of equal lengths
   bool split;       // some sequence may have more than one segment
+  bool tiny;        // rows of keys or values under 16 bytes: kp 256, vt 64, loaded value by value
 };
 AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
                              bool packed, int dtype);
@@ -108,6 +109,9 @@ hipError_t launch_state_pass(StatePass pass, const StateParams& p, const Attenti
 hipError_t launch_state_carry(bool reverse, const StateParams& p, const float* from, hipStream_t st);
 
 namespace tok {
+
+// This wave's number, in a scalar register.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
 // Where a segment lies: sequence s, its first token and length, and the
 // segment's range [begin, end) inside the sequence.
@@ -279,10 +283,11 @@ __device__ __forceinline__ Frag<float> frag_col_split(const Tile<float, R, C>& m
 // A tile on its way from global memory to LDS, in registers, by THREADS threads
 // with 16 bytes a piece.  Every piece is loaded, with no branch around it, so all
 // are in flight together: rows behind the last read the last one, pieces behind
-// the row's end and the piece across it read the row's last 16 bytes, and store()
-// puts zeros or the piece's own part in their place.  Rows shorter than 16 bytes
-// are loaded value by value.
-template <typename E, int ROWS, int COLS, int THREADS = 256>
+// the row's end and the piece across it read the 16 bytes that end there, and
+// store() puts zeros or the piece's own part in their place.  `first` columns of
+// the row lie before the tile's (the 16 bytes may begin there); a row of fewer
+// than 16 bytes in all takes TINY, which loads value by value.
+template <typename E, int ROWS, int COLS, int THREADS, bool TINY>
 struct TileLoad {
   static constexpr int kPer = 16 / (int)sizeof(E);  // elements per piece
   static constexpr int kRowPieces = COLS / kPer;
@@ -291,27 +296,24 @@ struct TileLoad {
 
   // nrows >= 1 rows of `base`, stride elements apart, of ncols >= 1 columns.
   __device__ __forceinline__ void load(const E* base, int64_t stride, int nrows, int ncols) {
-    if (ncols >= kPer) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int idx = threadIdx.x + i * THREADS;
-        const int row = min(idx / kRowPieces, nrows - 1), c = min((idx % kRowPieces) * kPer, ncols - kPer);
-        // 32-bit offsets: a chunk's rows span less than 2^31 elements (the strides are checked)
-        r[i] = *reinterpret_cast<const Bytes16*>(base + ((uint32_t)row * (uint32_t)stride + (uint32_t)c));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int idx = threadIdx.x + i * THREADS, row = min(idx / kRowPieces, nrows - 1);
+    for (int i = 0; i < kPieces; ++i) {
+      const int idx = threadIdx.x + i * THREADS;
+      const int row = min(idx / kRowPieces, nrows - 1), c = (idx % kRowPieces) * kPer;
+      // 32-bit offsets: a chunk's rows span less than 2^31 elements (the strides are checked)
+      if (TINY) {
         E e[kPer];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) e[j] = base[(uint32_t)row * (uint32_t)stride + (uint32_t)min(j, ncols - 1)];
+        for (int j = 0; j < kPer; ++j) e[j] = base[row * (int)stride + min(c + j, ncols - 1)];
         __builtin_memcpy(&r[i], e, 16);
+      } else {
+        r[i] = *reinterpret_cast<const Bytes16*>(base + (row * (int)stride + min(c, ncols - kPer)));
       }
     }
   }
   // The same nrows and ncols.
   __device__ __forceinline__ void store(Tile<E, ROWS, COLS>& m, int nrows, int ncols) const {
+    const bool ragged = TINY || ncols % kPer != 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int idx = threadIdx.x + i * THREADS;
@@ -323,10 +325,10 @@ struct TileLoad {
 #pragma unroll
       for (int j = 0; j < 4; ++j) x.w[j] = n > 0 ? x.w[j] : 0;
       __builtin_memcpy(__builtin_assume_aligned(to, 16), &x, 16);
-      if (n > 0 && n < kPer) {  // across the end: the loaded bytes end where the row does
+      if (ragged && n > 0 && n < kPer) {  // across the end: the loaded bytes end where the row does
         E e[kPer];
         __builtin_memcpy(e, &r[i], 16);
-        const int shift = ncols >= kPer ? kPer - n : 0;
+        const int shift = TINY ? 0 : kPer - n;
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
           if (j >= shift && j - shift < n) to[j - shift] = e[j];
@@ -345,9 +347,26 @@ struct TileLoad {
 // the chunk decays as a whole.
 template <int C>
 struct Decays {
-  float whole[C], frac[C];
+  __attribute__((aligned(16))) float whole[C], frac[C];
   __device__ __forceinline__ float between(int i, int j) const {  // exp(G_i - G_j)
     return __builtin_amdgcn_exp2f((whole[i] - whole[j]) + (frac[i] - frac[j]));
+  }
+  // exp(G_i - G_j) for j .. j + 3
+  __device__ __forceinline__ f32x4 between4(int i, int j) const {
+    const f32x4 w = *reinterpret_cast<const f32x4*>(&whole[j]), f = *reinterpret_cast<const f32x4*>(&frac[j]);
+    const float wi = whole[i], fi = frac[i];
+    f32x4 e;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) e[r] = __builtin_amdgcn_exp2f((wi - w[r]) + (fi - f[r]));
+    return e;
+  }
+  // exp(G_j) for j .. j + 3
+  __device__ __forceinline__ f32x4 since4(int j) const {
+    const f32x4 w = *reinterpret_cast<const f32x4*>(&whole[j]), f = *reinterpret_cast<const f32x4*>(&frac[j]);
+    f32x4 e;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) e[r] = __builtin_amdgcn_exp2f(w[r] + f[r]);
+    return e;
   }
 };
 

@@ -40,7 +40,7 @@ struct AttentionParams {
   bool split;  // segments behind a sequence's first start from seg_state
 };
 
-template <typename E, int C, int KP, int VT>
+template <typename E, int C, int KP, int VT, bool TINY>
 __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
   constexpr int NW = VT / 16, THREADS = NW * 64;
   constexpr int NI = C / 16;                            // token tiles
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
   __shared__ Tile<E, C, C> ps;
   __shared__ Decays<C> dec;
 
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+  const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const int vt = blockIdx.x % p.vtiles;
   const int head = (blockIdx.x / p.vtiles) % p.heads;
   const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
@@ -72,16 +72,20 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
   f32x4 h[NK];
   const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
   const float* from = p.split && seg.begin > 0 ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
+  if (from) {
+    const float* c = from + v0 + min(vw + l, nv - 1);
+#pragma unroll
+    for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) h[kt][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
+  }
 #pragma unroll
   for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int k = kt * 16 + 4 * g + r;
-      h[kt][r] = from && k < K && vw + l < nv ? from[(int64_t)k * p.V + v0 + vw + l] : 0.f;
-    }
+    for (int r = 0; r < 4; ++r) h[kt][r] = from && kt * 16 + 4 * g + r < K && vw + l < nv ? h[kt][r] : 0.f;
 
-  TileLoad<E, C, KP, THREADS> ql, kl;
-  TileLoad<E, C, VT, THREADS> vl;
+  TileLoad<E, C, KP, THREADS, TINY> ql, kl;
+  TileLoad<E, C, VT, THREADS, TINY> vl;
   float gl = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
@@ -99,7 +103,7 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
     vl.store(vs, n, nv);
     if (wave == 0) scan_decays<C>(gl, dec);
     __syncthreads();
-    if (at + C < seg.end) fetch(at + C);
+    fetch(at + C < seg.end ? at + C : at);  // always: a load under a condition would be waited for where the paths meet
 
     // scores, transposed (rows j, columns i): 16 tokens i per JS waves, which take every JS-th tile of keys j
     {
@@ -111,10 +115,11 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
           if (jt <= it)
 #pragma unroll
             for (int c = 0; c < KP; c += 32) s = mma(frag_row(ks, jt * 16 + l, c), frag_row(qs, i, c), s);
+          const f32x4 e = dec.between4(i, jt * 16 + 4 * g);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int j = jt * 16 + 4 * g + r;
-            s[r] = j <= i ? s[r] * (p.scale * dec.between(i, j)) : 0.f;
+            const float w = s[r] * (p.scale * e[r]);
+            s[r] = jt * 16 + 4 * g + r <= i ? w : 0.f;
           }
           put4(&ps.e[i * ps.stride + jt * 16 + 4 * g], s);
         }
@@ -158,10 +163,11 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
         Frag<E> b[PF];
         float u[8];
         frag_values(a, u);
+        const f32x4 w0 = dec.between4(C - 1, j * 16 + 4 * g), w1 = dec.between4(C - 1, j * 16 + 16 + 4 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          u[r] *= dec.between(C - 1, j * 16 + 4 * g + r);
-          u[4 + r] *= dec.between(C - 1, j * 16 + 16 + 4 * g + r);
+          u[r] *= w0[r];
+          u[4 + r] *= w1[r];
         }
         split_parts(u, b);
 #pragma unroll
@@ -194,11 +200,15 @@ namespace {
 template <typename E, int C, int VT>
 hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
   const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(VT * 4);
+  if (pl.tiny) {
+    attention_kernel<E, C, 256, 64, true><<<grid, dim3(256), 0, st>>>(p);
+    return hipGetLastError();
+  }
   switch (pl.kp) {
-    case 32: attention_kernel<E, C, 32, VT><<<grid, block, 0, st>>>(p); break;
-    case 64: attention_kernel<E, C, 64, VT><<<grid, block, 0, st>>>(p); break;
-    case 128: attention_kernel<E, C, 128, VT><<<grid, block, 0, st>>>(p); break;
-    default: attention_kernel<E, C, 256, VT><<<grid, block, 0, st>>>(p);
+    case 32: attention_kernel<E, C, 32, VT, false><<<grid, block, 0, st>>>(p); break;
+    case 64: attention_kernel<E, C, 64, VT, false><<<grid, block, 0, st>>>(p); break;
+    case 128: attention_kernel<E, C, 128, VT, false><<<grid, block, 0, st>>>(p); break;
+    default: attention_kernel<E, C, 256, VT, false><<<grid, block, 0, st>>>(p);
   }
   return hipGetLastError();
 }
@@ -208,7 +218,10 @@ hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream
 AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
                         bool packed, int dtype, int vt, int64_t want) {
   AttentionPlan pl;
-  pl.kp = key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
+  const int64_t least = dtype == 1 ? 8 : 4;  // values in 16 bytes
+  pl.tiny = key_dim < least || value_dim < least;
+  if (pl.tiny) vt = 64;
+  pl.kp = pl.tiny ? 256 : key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
   pl.vt = vt;
   pl.vtiles = (int)((value_dim + vt - 1) / vt);
   const int64_t chunk = pl.chunk = dtype == 1 ? 64 : 32;

@@ -52,7 +52,7 @@ struct BackwardParams {
   bool split;
 };
 
-template <typename E, int C, int KP, int VT, int NW>
+template <typename E, int C, int KP, int VT, int NW, bool TINY>
 __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardParams p) {
   constexpr int THREADS = NW * 64;
   constexpr int NI = C / 16, NK = KP / 16, NV = VT / 16;
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
   __shared__ Decays<C> dec;
   __shared__ float wrow[NW][C], wcol[NW][C], fs[NW][C], es[NW][C], xs[NW];
 
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+  const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const int vt = blockIdx.x % p.vtiles;
   const int head = (blockIdx.x / p.vtiles) % p.heads;
   const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
@@ -99,8 +99,8 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 #pragma unroll
       for (int r = 0; r < 4; ++r) dvk[a][b][r] = entry((wave + b * NW) * 16 + l, a * 16 + 4 * g + r);
 
-  TileLoad<E, C, KP, THREADS> ql, kl;
-  TileLoad<E, C, VT, THREADS> vl, dl;
+  TileLoad<E, C, KP, THREADS, TINY> ql, kl;
+  TileLoad<E, C, VT, THREADS, TINY> vl, dl;
   float gl = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
             h[a][b] = *reinterpret_cast<const f32x4*>(hb + ((a * NK + wave + b * NW) * 64 + lane) * 4);
     }
     __syncthreads();
-    if (c > 0) fetch(at - C);
+    fetch(c > 0 ? at - C : at);  // always: a load under a condition would be waited for where the paths meet
 
     // ---- S and D, transposed (rows j, columns i): 16 tokens i per JS waves, which take every JS-th tile of j
     {
@@ -185,15 +185,15 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 #pragma unroll
             for (int x = 0; x < VT; x += 32) d = mma(frag_row(vs, jt * 16 + l, x), frag_row(ds, i, x), d);
           }
+          const f32x4 e = dec.between4(i, jt * 16 + 4 * g) * p.scale;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = jt * 16 + 4 * g + r;
-            const float m = j <= i ? p.scale * dec.between(i, j) : 0.f;
-            const float w = j < i ? s[r] * d[r] * m : 0.f;
-            rows += w;
-            cols[r] = w;
-            s[r] = j <= i ? s[r] * m : 0.f;
-            d[r] = j <= i ? d[r] * m : 0.f;
+            const float smv = s[r] * e[r], dmv = d[r] * e[r], w = smv * d[r];
+            cols[r] = j < i ? w : 0.f;
+            rows += cols[r];
+            s[r] = j <= i ? smv : 0.f;
+            d[r] = j <= i ? dmv : 0.f;
           }
           put4(&sm.e[i * sm.stride + jt * 16 + 4 * g], s);
           put4(&dm.e[i * dm.stride + jt * 16 + 4 * g], d);
@@ -342,19 +342,17 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
       for (int b = 0; b < OK; ++b) dvk[a][b] *= all;
 #pragma unroll
     for (int j = 0; j < NI; j += 2) {
-      float f[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int i = j * 16 + 4 * g + (r & 3) + (r & 4) * 4;
-        f[r] = p.scale * __builtin_amdgcn_exp2f(dec.whole[i] + dec.frac[i]);
-      }
+      const f32x4 f0 = dec.since4(j * 16 + 4 * g) * p.scale, f1 = dec.since4(j * 16 + 16 + 4 * g) * p.scale;
       Frag<E> fd[OV][PF];
 #pragma unroll
       for (int b = 0; b < OV; ++b) {
         float u[8];
         frag_values(frag_col_split(ds, j * 16, (wave + b * NW) * 16), u);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) u[r] *= f[r];
+        for (int r = 0; r < 4; ++r) {
+          u[r] *= f0[r];
+          u[4 + r] *= f1[r];
+        }
         split_parts(u, fd[b]);
       }
 #pragma unroll
@@ -372,7 +370,10 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
           Frag<E> fq[PF];
           frag_values(frag_col_split(qs, j * 16, (wave + b * NW) * 16), u);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) u[r] *= f[r];
+          for (int r = 0; r < 4; ++r) {
+            u[r] *= f0[r];
+            u[4 + r] *= f1[r];
+          }
           split_parts(u, fq);
 #pragma unroll
           for (int a = 0; a < NV; ++a) {
@@ -436,11 +437,15 @@ Regions regions(const AttentionPlan& pl, int64_t tokens, int64_t groups, int64_t
 template <typename E, int C, int VT, int NW>
 hipError_t launch_k(const BackwardParams& p, const AttentionPlan& pl, hipStream_t st) {
   const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(NW * 64);
+  if (pl.tiny) {
+    attention_backward_kernel<E, C, 256, 64, 4, true><<<grid, dim3(256), 0, st>>>(p);
+    return hipGetLastError();
+  }
   switch (pl.kp) {
-    case 32: attention_backward_kernel<E, C, 32, VT, NW><<<grid, block, 0, st>>>(p); break;
-    case 64: attention_backward_kernel<E, C, 64, VT, NW><<<grid, block, 0, st>>>(p); break;
-    case 128: attention_backward_kernel<E, C, 128, VT, NW><<<grid, block, 0, st>>>(p); break;
-    default: attention_backward_kernel<E, C, 256, VT, NW><<<grid, block, 0, st>>>(p);
+    case 32: attention_backward_kernel<E, C, 32, VT, NW, false><<<grid, block, 0, st>>>(p); break;
+    case 64: attention_backward_kernel<E, C, 64, VT, NW, false><<<grid, block, 0, st>>>(p); break;
+    case 128: attention_backward_kernel<E, C, 128, VT, NW, false><<<grid, block, 0, st>>>(p); break;
+    default: attention_backward_kernel<E, C, 256, VT, NW, false><<<grid, block, 0, st>>>(p);
   }
   return hipGetLastError();
 }

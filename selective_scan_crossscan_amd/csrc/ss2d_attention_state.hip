@@ -18,14 +18,14 @@ namespace {
 
 using namespace tok;
 
-template <typename E, int C, int KP, int VT, StatePass PASS>
+template <typename E, int C, int KP, int VT, StatePass PASS, bool TINY>
 __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
   constexpr bool REVERSE = PASS == kSegmentGradients;
   constexpr int NI = C / 16, NK = KP / 16, NV = VT / 64, PF = kFullParts<E>;
   __shared__ Tile<E, C, KP> ks;
   __shared__ Tile<E, C, VT> vs;
   __shared__ Decays<C> dec;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+  const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const int vt = blockIdx.x % p.vtiles;
   const int head = (blockIdx.x / p.vtiles) % p.heads;
   const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
@@ -57,8 +57,8 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
         h[t][kt][r] = from && k < K && v < nv ? from[(int64_t)k * p.V + v0 + v] : 0.f;
       }
 
-  TileLoad<E, C, KP> kl;
-  TileLoad<E, C, VT> vl;
+  TileLoad<E, C, KP, 256, TINY> kl;
+  TileLoad<E, C, VT, 256, TINY> vl;
   float gl = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
     vl.store(vs, n, nv);
     if (wave == 0) scan_decays<C>(gl, dec);
     __syncthreads();
-    if (c + 1 < chunks) fetch(start_of(c + 1));
+    fetch(start_of(c + 1 < chunks ? c + 1 : c));  // always: a load under a condition would be waited for where the paths meet
     const float a = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
     whole += dec.whole[C - 1];
     frac += dec.frac[C - 1];
@@ -98,18 +98,18 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
         Frag<E> b[NV][PF];
-        float w[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int i = j * 16 + 4 * g + (r & 3) + (r & 4) * 4;
-          w[r] = REVERSE ? p.scale * __builtin_amdgcn_exp2f(dec.whole[i] + dec.frac[i]) : dec.between(C - 1, i);
-        }
+        const int i0 = j * 16 + 4 * g;
+        const f32x4 w0 = REVERSE ? dec.since4(i0) * p.scale : dec.between4(C - 1, i0);
+        const f32x4 w1 = REVERSE ? dec.since4(i0 + 16) * p.scale : dec.between4(C - 1, i0 + 16);
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
           float x[8];
           frag_values(frag_col_split(vs, j * 16, vw + t * 16), x);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) x[r] *= w[r];
+          for (int r = 0; r < 4; ++r) {
+            x[r] *= w0[r];
+            x[4 + r] *= w1[r];
+          }
           split_parts(x, b[t]);
         }
 #pragma unroll
@@ -171,11 +171,15 @@ __global__ __launch_bounds__(256) void state_carry(StateParams p, const float* f
 template <typename E, int C, int VT, StatePass PASS>
 hipError_t launch_k(const StateParams& p, const AttentionPlan& pl, hipStream_t st) {
   const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(256);
+  if (pl.tiny) {
+    state_kernel<E, C, 256, 64, PASS, true><<<grid, block, 0, st>>>(p);
+    return hipGetLastError();
+  }
   switch (pl.kp) {
-    case 32: state_kernel<E, C, 32, VT, PASS><<<grid, block, 0, st>>>(p); break;
-    case 64: state_kernel<E, C, 64, VT, PASS><<<grid, block, 0, st>>>(p); break;
-    case 128: state_kernel<E, C, 128, VT, PASS><<<grid, block, 0, st>>>(p); break;
-    default: state_kernel<E, C, 256, VT, PASS><<<grid, block, 0, st>>>(p);
+    case 32: state_kernel<E, C, 32, VT, PASS, false><<<grid, block, 0, st>>>(p); break;
+    case 64: state_kernel<E, C, 64, VT, PASS, false><<<grid, block, 0, st>>>(p); break;
+    case 128: state_kernel<E, C, 128, VT, PASS, false><<<grid, block, 0, st>>>(p); break;
+    default: state_kernel<E, C, 256, VT, PASS, false><<<grid, block, 0, st>>>(p);
   }
   return hipGetLastError();
 }
