@@ -227,25 +227,26 @@ __device__ __forceinline__ void frag_values(const Frag<float>& f, float (&x)[8])
 }
 
 // ---------------------------------------------------------------- LDS tiles
-// A ROWS x COLS tile, row major; 16 bytes of padding per row spread sixteen
-// rows' 16-byte reads over the banks.
-template <typename E, int ROWS, int COLS>
+// A ROWS x COLS tile, row major, with PAD bytes behind each row: 16 spread
+// sixteen rows' reads of 8 or 16 bytes over the banks (frag_row, frag_row_split),
+// 32 the transposing reads of four rows by four 8-byte pieces (frag_col_split).
+template <typename E, int ROWS, int COLS, int PAD = 16>
 struct Tile {
-  static constexpr int stride = COLS + 16 / (int)sizeof(E);
+  static constexpr int stride = COLS + PAD / (int)sizeof(E);
   E e[ROWS * stride];
 };
 
 // Fragment of row `row` (inner index along the row from c0), plain order.
-template <typename E, int R, int C>
-__device__ __forceinline__ Frag<E> frag_row(const Tile<E, R, C>& m, int row, int c0) {
+template <typename E, int R, int C, int PAD>
+__device__ __forceinline__ Frag<E> frag_row(const Tile<E, R, C, PAD>& m, int row, int c0) {
   const int g = (threadIdx.x & 63) >> 4;
   Frag<E> f;
   __builtin_memcpy(&f, __builtin_assume_aligned(&m.e[row * m.stride + c0 + 8 * g], 16), sizeof(f));
   return f;
 }
 // The same in split order.
-template <typename E, int R, int C>
-__device__ __forceinline__ Frag<E> frag_row_split(const Tile<E, R, C>& m, int row, int c0) {
+template <typename E, int R, int C, int PAD>
+__device__ __forceinline__ Frag<E> frag_row_split(const Tile<E, R, C, PAD>& m, int row, int c0) {
   const int g = (threadIdx.x & 63) >> 4;
   Frag<E> f;
   const E* p = &m.e[row * m.stride + c0 + 4 * g];
@@ -257,8 +258,8 @@ __device__ __forceinline__ Frag<E> frag_row_split(const Tile<E, R, C>& m, int ro
 // Fragment of column c0 + lane % 16 (inner index down the rows from r0), split
 // order.  bf16: the transposing LDS read, in which the sixteen lanes of a group
 // each read four columns of one of four rows and get four rows of one column.
-template <int R, int C>
-__device__ __forceinline__ Frag<uint16_t> frag_col_split(const Tile<uint16_t, R, C>& m, int r0, int c0) {
+template <int R, int C, int PAD>
+__device__ __forceinline__ Frag<uint16_t> frag_col_split(const Tile<uint16_t, R, C, PAD>& m, int r0, int c0) {
   typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
   const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const uint16_t* p = &m.e[(r0 + 4 * g + (l >> 2)) * m.stride + c0 + 4 * (l & 3)];
@@ -268,8 +269,8 @@ __device__ __forceinline__ Frag<uint16_t> frag_col_split(const Tile<uint16_t, R,
   f.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   return f;
 }
-template <int R, int C>
-__device__ __forceinline__ Frag<float> frag_col_split(const Tile<float, R, C>& m, int r0, int c0) {
+template <int R, int C, int PAD>
+__device__ __forceinline__ Frag<float> frag_col_split(const Tile<float, R, C, PAD>& m, int r0, int c0) {
   const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   Frag<float> f;
 #pragma unroll
@@ -312,7 +313,8 @@ struct TileLoad {
     }
   }
   // The same nrows and ncols.
-  __device__ __forceinline__ void store(Tile<E, ROWS, COLS>& m, int nrows, int ncols) const {
+  template <int PAD>
+  __device__ __forceinline__ void store(Tile<E, ROWS, COLS, PAD>& m, int nrows, int ncols) const {
     const bool ragged = TINY || ncols % kPer != 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {

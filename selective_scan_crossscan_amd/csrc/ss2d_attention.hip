@@ -40,15 +40,16 @@ struct AttentionParams {
   bool split;  // segments behind a sequence's first start from seg_state
 };
 
-template <typename E, int C, int KP, int VT, bool TINY>
-__global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
-  constexpr int NW = VT / 16, THREADS = NW * 64;
+template <typename E, int C, int KP, int VT, int NV, bool TINY>
+__global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionParams p) {
+  constexpr int NW = VT / 16 / NV, THREADS = NW * 64;   // a wave owns NV tiles of 16 value columns
   constexpr int NI = C / 16;                            // token tiles
   constexpr int NK = KP / 16;                           // key tiles
   constexpr int JS = NW / NI < NI ? NW / NI : NI;       // waves that share 16 tokens' scores
   constexpr int PF = kFullParts<E>, PH = kHalfParts<E>;
-  __shared__ Tile<E, C, KP> qs, ks;
-  __shared__ Tile<E, C, VT> vs;
+  __shared__ Tile<E, C, KP> qs;
+  __shared__ Tile<E, C, KP, 32> ks;
+  __shared__ Tile<E, C, VT, 32> vs;
   __shared__ Tile<E, C, C> ps;
   __shared__ Decays<C> dec;
 
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
   if (!find_segment(p.map, slot, seg)) return;
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
-  const int vw = wave * 16;        // this wave's first column in the tile
+  const int vw = wave * 16 * NV;   // this wave's first column in the tile
   const bool active = vw < nv;     // it has columns at all
   const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
   const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + first * p.q_stride[1] + group * p.q_stride[2];
@@ -68,42 +69,58 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
   const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + first * p.v_stride[1] + head * p.v_stride[2] + v0;
   const float* gb = p.g + sq * p.g_stride[0] + first * p.g_stride[1] + head * p.g_stride[2];
 
-  // the state: rows 16 kt + 4 g + r, column vw + l
-  f32x4 h[NK];
+  // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
+  f32x4 h[NK][NV];
   const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
   const float* from = p.split && seg.begin > 0 ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
-  if (from) {
-    const float* c = from + v0 + min(vw + l, nv - 1);
+#pragma unroll
+  for (int t = 0; t < NV; ++t) {
+    const int v = vw + t * 16 + l;
+    if (from) {
+      const float* c = from + v0 + min(v, nv - 1);
+#pragma unroll
+      for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[kt][t][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
+    }
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) h[kt][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
+      for (int r = 0; r < 4; ++r) h[kt][t][r] = from && kt * 16 + 4 * g + r < K && v < nv ? h[kt][t][r] : 0.f;
   }
-#pragma unroll
-  for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) h[kt][r] = from && kt * 16 + 4 * g + r < K && vw + l < nv ? h[kt][r] : 0.f;
 
-  TileLoad<E, C, KP, THREADS, TINY> ql, kl;
-  TileLoad<E, C, VT, THREADS, TINY> vl;
-  float gl = 0.f;
-  auto fetch = [&](int64_t at) {
-    const int n = (int)min((int64_t)C, seg.end - at);
-    ql.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
-    kl.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
-    vl.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
-    if (wave == 0) gl = lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
+  struct Chunk {
+    TileLoad<E, C, KP, THREADS, TINY> q, k;
+    TileLoad<E, C, VT, THREADS, TINY> v;
+    float g;
   };
-  if (seg.begin < seg.end) fetch(seg.begin);
+  auto fetch = [&](Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+    x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
+    x.g = wave == 0 && lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
+  };
+  auto land = [&](const Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+    x.q.store(qs, n, K);
+    x.k.store(ks, n, K);
+    x.v.store(vs, n, nv);
+    if (wave == 0) scan_decays<C>(x.g, dec);
+  };
+  if (seg.begin < seg.end) {
+    Chunk x;
+    fetch(x, seg.begin);
+    land(x, seg.begin);
+  }
   for (int64_t at = seg.begin; at < seg.end; at += C) {
     const int n = (int)min((int64_t)C, seg.end - at);
-    __syncthreads();  // the previous chunk has been read
-    ql.store(qs, n, K);
-    kl.store(ks, n, K);
-    vl.store(vs, n, nv);
-    if (wave == 0) scan_decays<C>(gl, dec);
-    __syncthreads();
-    fetch(at + C < seg.end ? at + C : at);  // always: a load under a condition would be waited for where the paths meet
+    __syncthreads();  // the chunk has landed
+    // the next chunk's loads run beside this one's products; always, the last one's again: a load under a condition
+    // would be waited for where the paths meet
+    Chunk next;
+    const int64_t ahead = at + C < seg.end ? at + C : at;
+    fetch(next, ahead);
 
     // scores, transposed (rows j, columns i): 16 tokens i per JS waves, which take every JS-th tile of keys j
     {
@@ -127,94 +144,137 @@ __global__ __launch_bounds__(VT * 4) void attention_kernel(AttentionParams p) {
     __syncthreads();
 
     if (active) {
-      f32x4 o[NI];
+      f32x4 o[NV][NI];
 #pragma unroll
-      for (int x = 0; x < NI; ++x) o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < NV; ++t)
+#pragma unroll
+        for (int x = 0; x < NI; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
       // h' q'
 #pragma unroll
       for (int c = 0; c < NK; c += 2) {
-        Frag<E> a[PH];
-        float u[8];
+        Frag<E> a[NV][PH];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          u[r] = h[c][r];
-          u[4 + r] = h[c + 1][r];
+        for (int t = 0; t < NV; ++t) {
+          float u[8];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            u[r] = h[c][t][r];
+            u[4 + r] = h[c + 1][t][r];
+          }
+          split_parts(u, a[t]);
         }
-        split_parts(u, a);
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const Frag<E> b = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-          for (int q = 0; q < PH; ++q) o[x] = mma(a[q], b, o[x]);
+          for (int q = 0; q < PH; ++q)
+#pragma unroll
+            for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], b, o[t][x]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int x = 0; x < NI; ++x)
-        o[x] *= p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
-      // v' scores' for the output, k' (decayed v) for the state
-      const float all = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
+      for (int x = 0; x < NI; ++x) {
+        const float f = p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
 #pragma unroll
-      for (int kt = 0; kt < NK; ++kt) h[kt] *= all;
+        for (int t = 0; t < NV; ++t) o[t][x] *= f;
+      }
+      // v' scores'
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        const Frag<E> a = frag_col_split(vs, j * 16, vw);
+        Frag<E> a[NV];
 #pragma unroll
-        for (int x = j; x < NI; ++x) o[x] = mma(a, frag_row_split(ps, x * 16 + l, j * 16), o[x]);
-        Frag<E> b[PF];
-        float u[8];
-        frag_values(a, u);
+        for (int t = 0; t < NV; ++t) a[t] = frag_col_split(vs, j * 16, vw + t * 16);
+#pragma unroll
+        for (int x = j; x < NI; ++x) {
+          const Frag<E> s = frag_row_split(ps, x * 16 + l, j * 16);
+#pragma unroll
+          for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t], s, o[t][x]);
+        }
+      }
+      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
+#pragma unroll
+      for (int x = 0; x < NI; ++x)
+        if (x * 16 + l < n)
+#pragma unroll
+          for (int t = 0; t < NV; ++t) {
+            const int v = vw + t * 16 + 4 * g;
+            store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[t][x]);
+          }
+      __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
+
+      // k' (decayed v)
+      const float all = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
+#pragma unroll
+      for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+        for (int t = 0; t < NV; ++t) h[kt][t] *= all;
+#pragma unroll
+      for (int j = 0; j < NI; j += 2) {
+        Frag<E> b[NV][PF];
         const f32x4 w0 = dec.between4(C - 1, j * 16 + 4 * g), w1 = dec.between4(C - 1, j * 16 + 16 + 4 * g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          u[r] *= w0[r];
-          u[4 + r] *= w1[r];
+        for (int t = 0; t < NV; ++t) {
+          float u[8];
+          frag_values(frag_col_split(vs, j * 16, vw + t * 16), u);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            u[r] *= w0[r];
+            u[4 + r] *= w1[r];
+          }
+          split_parts(u, b[t]);
         }
-        split_parts(u, b);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
           const Frag<E> k = frag_col_split(ks, j * 16, kt * 16);
 #pragma unroll
-          for (int q = 0; q < PF; ++q) h[kt] = mma(k, b[q], h[kt]);
-        }
-      }
-      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-      const int v = vw + 4 * g;
+          for (int q = 0; q < PF; ++q)
 #pragma unroll
-      for (int x = 0; x < NI; ++x)
-        if (x * 16 + l < n) store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[x]);
+            for (int t = 0; t < NV; ++t) h[kt][t] = mma(k, b[t][q], h[kt][t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    __syncthreads();  // the chunk has been read
+    land(next, ahead);
   }
 
   if (seg.last && p.state_out)
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = kt * 16 + 4 * g + r;
-        if (k < K && vw + l < nv) p.state_out[qh + (int64_t)k * p.V + v0 + vw + l] = h[kt][r];
-      }
+      for (int t = 0; t < NV; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
+          if (k < K && v < nv) p.state_out[qh + (int64_t)k * p.V + v0 + v] = h[kt][t][r];
+        }
 }
 
 namespace {
 
 template <typename E, int C, int VT>
 hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(VT * 4);
+  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles));
+  constexpr int NV = VT / 64;
   if (pl.tiny) {
-    attention_kernel<E, C, 256, 64, true><<<grid, dim3(256), 0, st>>>(p);
+    attention_kernel<E, C, 256, 64, 1, true><<<grid, dim3(256), 0, st>>>(p);
     return hipGetLastError();
   }
   switch (pl.kp) {
-    case 32: attention_kernel<E, C, 32, VT, false><<<grid, block, 0, st>>>(p); break;
-    case 64: attention_kernel<E, C, 64, VT, false><<<grid, block, 0, st>>>(p); break;
-    case 128: attention_kernel<E, C, 128, VT, false><<<grid, block, 0, st>>>(p); break;
-    default: attention_kernel<E, C, 256, VT, false><<<grid, block, 0, st>>>(p);
+    case 32: attention_kernel<E, C, 32, VT, NV, false><<<grid, dim3(256), 0, st>>>(p); break;
+    case 64: attention_kernel<E, C, 64, VT, NV, false><<<grid, dim3(256), 0, st>>>(p); break;
+    case 128: attention_kernel<E, C, 128, VT, NV, false><<<grid, dim3(256), 0, st>>>(p); break;
+    default: attention_kernel<E, C, 256, VT, 1, false><<<grid, dim3(VT * 4), 0, st>>>(p);
   }
   return hipGetLastError();
 }
 
-// The plan for tiles of vt value columns and segments of about tokens x heads x
-// tiles / want tokens: `want` workgroups, of four chunks each at least.
+// The plan for tiles of vt value columns.  Sequences are cut so that there are
+// about `want` workgroups and no more: a few over a whole number per CU would
+// cost as long as a full round.  Equal lengths are cut evenly; packed ones every
+// tokens / (want per head and tile, less one ragged end per sequence) tokens.
+// Segments have four chunks at least.
 AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
                         bool packed, int dtype, int vt, int64_t want) {
   AttentionPlan pl;
@@ -225,10 +285,13 @@ AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_
   pl.vt = vt;
   pl.vtiles = (int)((value_dim + vt - 1) / vt);
   const int64_t chunk = pl.chunk = dtype == 1 ? 64 : 32;
-  int64_t seg = (tokens * heads * pl.vtiles + want - 1) / want;
+  const int64_t longest = packed ? tokens : tokens / sequences;
+  const int64_t each = want / (heads * pl.vtiles);  // segments of all sequences together
+  int64_t parts = packed ? (each - sequences > each / 2 ? each - sequences : each / 2) : each / sequences;
+  if (parts < 1) parts = 1;
+  int64_t seg = (longest + parts - 1) / parts;
   if (seg < 4 * chunk) seg = 4 * chunk;
   seg = (seg + chunk - 1) / chunk * chunk;
-  const int64_t longest = packed ? tokens : tokens / sequences;
   pl.split = longest > seg;
   if (!pl.split) seg = (longest + chunk - 1) / chunk * chunk;
   pl.seg_len = seg;

@@ -22,8 +22,8 @@ template <typename E, int C, int KP, int VT, StatePass PASS, bool TINY>
 __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
   constexpr bool REVERSE = PASS == kSegmentGradients;
   constexpr int NI = C / 16, NK = KP / 16, NV = VT / 64, PF = kFullParts<E>;
-  __shared__ Tile<E, C, KP> ks;
-  __shared__ Tile<E, C, VT> vs;
+  __shared__ Tile<E, C, KP, 32> ks;
+  __shared__ Tile<E, C, VT, 32> vs;
   __shared__ Decays<C> dec;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const int vt = blockIdx.x % p.vtiles;
