@@ -70,9 +70,9 @@ typedef struct {
  *   state_out  [sequences, heads, key_dim, value_dim] fp32, out, or NULL; may be
  *              state_in itself
  * Outputs must not overlap inputs otherwise (SS2D_ERR_ALIAS).  States, decays and
- * sums are fp32 (decays summed in fp64).  For bf16 the masked scores q.k are rounded
- * to bf16 for their product with v, as the output is; what the state is made of is
- * carried in three bf16 parts (24 bits of mantissa), the state read for o in two.  NaN and Inf
+ * sums are fp32 (decays summed in fp64).  For bf16 the masked scores
+ * and the state are rounded to bf16 for their products into o, whose own rounding is
+ * as large; what the state itself is made of keeps all its bits.  NaN and Inf
  * propagate: from a token to its sequence's outputs from up to 63 tokens before it on
  * (tokens are taken in chunks as matrix products).  Results do not depend on the
  * workspace, other sequences or streams: no atomics, sums in a fixed order.

@@ -14,9 +14,10 @@
 //
 // Parts.  An fp32 value that enters a bf16 product as a state or a decayed
 // operand is split into bf16 parts that add up to it, each the rounding of what
-// the parts before left: three give all 24 bits and two give 16.  What becomes an
-// fp32 result (states, gradients of the decay) takes three, what ends in a bf16
-// output two.  The fp32 product takes the value itself.
+// the parts before left: three give all 24 bits.  What becomes an fp32 result
+// (states, gradients of the decay) takes three.  What only ends in a bf16 output
+// takes one, as the masked scores do: its rounding, 2^-9 of its share of the output
+// at most, is that of the output itself.  The fp32 product takes the value itself.
 #pragma once
 
 #include "ss2d_token_ops.h"
@@ -176,11 +177,9 @@ struct Frag<float> {
   float v[8];
 };
 
-// Parts an fp32 value is split into (see above): for fp32 results, for others.
+// Parts an fp32 value is split into for fp32 results (see above).
 template <typename E>
 constexpr int kFullParts = sizeof(E) == 2 ? 3 : 1;
-template <typename E>
-constexpr int kHalfParts = sizeof(E) == 2 ? 2 : 1;
 
 __device__ __forceinline__ f32x4 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
@@ -288,7 +287,7 @@ __device__ __forceinline__ Frag<float> frag_col_split(const Tile<float, R, C, PA
 // store() puts zeros or the piece's own part in their place.  `first` columns of
 // the row lie before the tile's (the 16 bytes may begin there); a row of fewer
 // than 16 bytes in all takes TINY, which loads value by value.
-template <typename E, int ROWS, int COLS, int THREADS, bool TINY>
+template <typename E, int ROWS, int COLS, int PAD, int THREADS, bool TINY>
 struct TileLoad {
   static constexpr int kPer = 16 / (int)sizeof(E);  // elements per piece
   static constexpr int kRowPieces = COLS / kPer;
@@ -301,20 +300,31 @@ struct TileLoad {
     for (int i = 0; i < kPieces; ++i) {
       const int idx = threadIdx.x + i * THREADS;
       const int row = min(idx / kRowPieces, nrows - 1), c = (idx % kRowPieces) * kPer;
-      // 32-bit offsets: a chunk's rows span less than 2^31 elements (the strides are checked)
+      // 24-bit factors: the strides are checked, a chunk's rows span less than 2^31 elements.  Signed sums: the 16
+      // bytes of a narrow tile may begin before its first column
+      const int at = (int)__umul24((uint32_t)row, (uint32_t)stride);
       if (TINY) {
         E e[kPer];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) e[j] = base[row * (int)stride + min(c + j, ncols - 1)];
+        for (int j = 0; j < kPer; ++j) e[j] = base[at + min(c + j, ncols - 1)];
         __builtin_memcpy(&r[i], e, 16);
       } else {
-        r[i] = *reinterpret_cast<const Bytes16*>(base + (row * (int)stride + min(c, ncols - kPer)));
+        r[i] = *reinterpret_cast<const Bytes16*>(base + (at + min(c, ncols - kPer)));
       }
     }
   }
   // The same nrows and ncols.
-  template <int PAD>
   __device__ __forceinline__ void store(Tile<E, ROWS, COLS, PAD>& m, int nrows, int ncols) const {
+    if (!TINY && nrows == ROWS && ncols == COLS) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int idx = threadIdx.x + i * THREADS;
+        if (ROWS * kRowPieces % THREADS == 0 || idx < ROWS * kRowPieces)
+          __builtin_memcpy(__builtin_assume_aligned(&m.e[idx / kRowPieces * m.stride + (idx % kRowPieces) * kPer], 16),
+                           &r[i], 16);
+      }
+      return;
+    }
     const bool ragged = TINY || ncols % kPer != 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -407,6 +417,30 @@ __device__ __forceinline__ void store4(uint16_t* p, int n, f32x4 v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < n) p[i] = (uint16_t)(i & 1 ? b.w[i / 2] >> 16 : b.w[i / 2]);
+  }
+}
+// Transposed result tiles to memory: tile [t][x] holds, for token 16 x + l, the
+// four columns from c0 + t * step on; `tokens` rows and `cols` columns exist.
+template <int NI, int NV, typename O>
+__device__ __forceinline__ void put_rows(O* base, int64_t stride, int tokens, int cols, int c0, int step, int l,
+                                         const f32x4 (&x)[NV][NI]) {
+  if (tokens == NI * 16 && cols % 4 == 0) {  // whole tokens, whole pieces or none
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      O* row = base + (i * 16 + l) * stride;
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+        if (c0 + t * step < cols) store4(row + c0 + t * step, 4, x[t][i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (i * 16 + l < tokens)
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          const int c = c0 + t * step;
+          store4(base + (i * 16 + l) * stride + c, cols - c, x[t][i]);
+        }
   }
 }
 // Four elements into an LDS row (aligned to four elements).

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
   constexpr int NI = C / 16;                            // token tiles
   constexpr int NK = KP / 16;                           // key tiles
   constexpr int JS = NW / NI < NI ? NW / NI : NI;       // waves that share 16 tokens' scores
-  constexpr int PF = kFullParts<E>, PH = kHalfParts<E>;
+  constexpr int PF = kFullParts<E>;
   __shared__ Tile<E, C, KP> qs;
   __shared__ Tile<E, C, KP, 32> ks;
   __shared__ Tile<E, C, VT, 32> vs;
@@ -90,8 +90,9 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
   }
 
   struct Chunk {
-    TileLoad<E, C, KP, THREADS, TINY> q, k;
-    TileLoad<E, C, VT, THREADS, TINY> v;
+    TileLoad<E, C, KP, 16, THREADS, TINY> q;
+    TileLoad<E, C, KP, 32, THREADS, TINY> k;
+    TileLoad<E, C, VT, 32, THREADS, TINY> v;
     float g;
   };
   auto fetch = [&](Chunk& x, int64_t at) {
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
       // h' q'
 #pragma unroll
       for (int c = 0; c < NK; c += 2) {
-        Frag<E> a[NV][PH];
+        Frag<E> a[NV][1];
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
           float u[8];
@@ -167,9 +168,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
         for (int x = 0; x < NI; ++x) {
           const Frag<E> b = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-          for (int q = 0; q < PH; ++q)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], b, o[t][x]);
+          for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][0], b, o[t][x]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -193,14 +192,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
         }
       }
       E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-#pragma unroll
-      for (int x = 0; x < NI; ++x)
-        if (x * 16 + l < n)
-#pragma unroll
-          for (int t = 0; t < NV; ++t) {
-            const int v = vw + t * 16 + 4 * g;
-            store4(ob + (int64_t)(x * 16 + l) * p.heads * p.V + v, nv - v, o[t][x]);
-          }
+      put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
       __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
 
       // k' (decayed v)

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
   constexpr int NI = C / 16, NK = KP / 16, NV = VT / 16;
   constexpr int OK = (NK + NW - 1) / NW, OV = NV / NW;  // key and value tiles a wave owns: wave, wave + NW, ...
   constexpr int JS = NW / NI < NI ? NW / NI : NI;       // waves that share 16 tokens' scores
-  constexpr int PF = kFullParts<E>, PH = kHalfParts<E>;
+  constexpr int PF = kFullParts<E>;
   static_assert(NV % NW == 0 && NW >= NI, "value tiles and token tiles are dealt evenly");
   __shared__ Tile<E, C, KP> qs, ks;
   __shared__ Tile<E, C, VT> vs, ds;
@@ -99,8 +99,8 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 #pragma unroll
       for (int r = 0; r < 4; ++r) dvk[a][b][r] = entry((wave + b * NW) * 16 + l, a * 16 + 4 * g + r);
 
-  TileLoad<E, C, KP, THREADS, TINY> ql, kl;
-  TileLoad<E, C, VT, THREADS, TINY> vl, dl;
+  TileLoad<E, C, KP, 16, THREADS, TINY> ql, kl;
+  TileLoad<E, C, VT, 16, THREADS, TINY> vl, dl;
   float gl = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 #pragma unroll
       for (int a = 0; a < NK; a += 2) {
         float u[8];
-        Frag<E> dp[PH];
+        Frag<E> dp[1];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           u[r] = dkv[a][b][r];
@@ -311,8 +311,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const Frag<E> fk = frag_row_split(ks, x * 16 + l, a * 16);
-#pragma unroll
-          for (int q = 0; q < PH; ++q) dv[x] = mma(dp[q], fk, dv[x]);
+          dv[x] = mma(dp[0], fk, dv[x]);
         }
       }
 #pragma unroll

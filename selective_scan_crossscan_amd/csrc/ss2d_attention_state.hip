@@ -19,7 +19,7 @@ namespace {
 using namespace tok;
 
 template <typename E, int C, int KP, int VT, StatePass PASS, bool TINY>
-__global__ __launch_bounds__(256) void state_kernel(StateParams p) {
+__global__ __launch_bounds__(256, 2) void state_kernel(StateParams p) {
   constexpr bool REVERSE = PASS == kSegmentGradients;
   constexpr int NI = C / 16, NK = KP / 16, NV = VT / 64, PF = kFullParts<E>;
   __shared__ Tile<E, C, KP, 32> ks;
@@ -47,29 +47,47 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
                       : p.split && seg.begin > 0        ? p.seg_state + sh
                       : p.state_in                      ? p.state_in + ((int64_t)seg.s * p.heads + head) * K * p.V
                                                         : nullptr;
+  if (from)
+#pragma unroll
+    for (int t = 0; t < NV; ++t)
+#pragma unroll
+      for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          h[t][kt][r] = from[(int64_t)min(kt * 16 + l, K - 1) * p.V + v0 + min(vw + t * 16 + 4 * g + r, nv - 1)];
 #pragma unroll
   for (int t = 0; t < NV; ++t)
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = kt * 16 + l, v = vw + t * 16 + 4 * g + r;
-        h[t][kt][r] = from && k < K && v < nv ? from[(int64_t)k * p.V + v0 + v] : 0.f;
-      }
+      for (int r = 0; r < 4; ++r)
+        h[t][kt][r] = from && kt * 16 + l < K && vw + t * 16 + 4 * g + r < nv ? h[t][kt][r] : 0.f;
 
-  TileLoad<E, C, KP, 256, TINY> kl;
-  TileLoad<E, C, VT, 256, TINY> vl;
-  float gl = 0.f;
-  auto fetch = [&](int64_t at) {
+  struct Chunk {
+    TileLoad<E, C, KP, 32, 256, TINY> k;
+    TileLoad<E, C, VT, 32, 256, TINY> v;
+    float g;
+  };
+  auto fetch = [&](Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-    kl.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
-    vl.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
-    if (wave == 0) gl = lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
+    x.g = wave == 0 && lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
+  };
+  auto land = [&](const Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+    x.k.store(ks, n, K);
+    x.v.store(vs, n, nv);
+    if (wave == 0) scan_decays<C>(x.g, dec);
   };
   const int64_t chunks = (seg.end - seg.begin + C - 1) / C;
   auto start_of = [&](int64_t c) { return seg.begin + (REVERSE ? chunks - 1 - c : c) * C; };
   float whole = 0.f, frac = 0.f;  // the segment's log2 decay so far
-  if (chunks > 0) fetch(start_of(0));
+  if (chunks > 0) {
+    Chunk x;
+    fetch(x, start_of(0));
+    land(x, start_of(0));
+  }
   for (int64_t c = 0; c < chunks; ++c) {
     if (PASS == kChunkStates) {  // before the chunk, as it lies in registers: 1 KiB per tile and wave
       float* to = p.chunk_state + ((chunk_number<C>(p.map, seg, start_of(c)) * p.heads + head) * p.vtiles + vt) * (KP * VT);
@@ -80,13 +98,12 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
           *reinterpret_cast<f32x4*>(to + (((wave * NV + t) * NK + kt) * 64 + lane) * 4) = h[t][kt];
       if (c + 1 == chunks) break;  // the state behind the last chunk is not needed
     }
-    __syncthreads();  // the previous chunk has been read
-    const int n = (int)min((int64_t)C, seg.end - start_of(c));
-    kl.store(ks, n, K);
-    vl.store(vs, n, nv);
-    if (wave == 0) scan_decays<C>(gl, dec);
-    __syncthreads();
-    fetch(start_of(c + 1 < chunks ? c + 1 : c));  // always: a load under a condition would be waited for where the paths meet
+    __syncthreads();  // the chunk has landed
+    // the next chunk's loads run beside this one's products; always, the last one's again: a load under a condition
+    // would be waited for where the paths meet
+    Chunk next;
+    const int64_t ahead = start_of(c + 1 < chunks ? c + 1 : c);
+    fetch(next, ahead);
     const float a = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
     whole += dec.whole[C - 1];
     frac += dec.frac[C - 1];
@@ -116,12 +133,15 @@ __global__ __launch_bounds__(256) void state_kernel(StateParams p) {
         for (int kt = 0; kt < NK; ++kt) {
           const Frag<E> k = frag_col_split(ks, j * 16, kt * 16);
 #pragma unroll
-          for (int t = 0; t < NV; ++t)
+          for (int q = 0; q < PF; ++q)
 #pragma unroll
-            for (int q = 0; q < PF; ++q) h[t][kt] = mma(b[t][q], k, h[t][kt]);
+            for (int t = 0; t < NV; ++t) h[t][kt] = mma(b[t][q], k, h[t][kt]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    __syncthreads();  // the chunk has been read
+    land(next, ahead);
   }
   if (PASS != kChunkStates) {
 #pragma unroll
