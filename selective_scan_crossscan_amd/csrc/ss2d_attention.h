@@ -420,27 +420,25 @@ __device__ __forceinline__ void store4(uint16_t* p, int n, f32x4 v) {
   }
 }
 // Transposed result tiles to memory: tile [t][x] holds, for token 16 x + l, the
-// four columns from c0 + t * step on; `tokens` rows and `cols` columns exist.
+// four columns from c0 + t * step on; `tokens` rows, stride elements apart (64 of
+// them under 2^32), and `cols` columns exist.
 template <int NI, int NV, typename O>
 __device__ __forceinline__ void put_rows(O* base, int64_t stride, int tokens, int cols, int c0, int step, int l,
                                          const f32x4 (&x)[NV][NI]) {
+  const uint32_t at = (uint32_t)l * (uint32_t)stride + (uint32_t)c0;
   if (tokens == NI * 16 && cols % 4 == 0) {  // whole tokens, whole pieces or none
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      O* row = base + (i * 16 + l) * stride;
+    for (int t = 0; t < NV; ++t)
+      if (c0 + t * step < cols)
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-        if (c0 + t * step < cols) store4(row + c0 + t * step, 4, x[t][i]);
-    }
+        for (int i = 0; i < NI; ++i) store4(base + i * 16 * stride + (at + (uint32_t)(t * step)), 4, x[t][i]);
   } else {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       if (i * 16 + l < tokens)
 #pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          const int c = c0 + t * step;
-          store4(base + (i * 16 + l) * stride + c, cols - c, x[t][i]);
-        }
+        for (int t = 0; t < NV; ++t)
+          store4(base + i * 16 * stride + (at + (uint32_t)(t * step)), cols - c0 - t * step, x[t][i]);
   }
 }
 // Four elements into an LDS row (aligned to four elements).

@@ -85,7 +85,10 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
   f32x4 dkv[NK][OV], dvk[NV][OK];
   const int64_t kv = (int64_t)K * p.V, qh = ((int64_t)seg.s * p.heads + head) * kv;
   const float* from = !seg.last ? p.seg_dstate + (slot * p.heads + head) * kv : p.dstate_out ? p.dstate_out + qh : nullptr;
-  auto entry = [&](int k, int v) { return from && k < K && v < nv ? from[(int64_t)k * p.V + v0 + v] : 0.f; };
+  auto entry = [&](int k, int v) {  // loaded at a place inside, dropped outside: no branch around the load
+    const float x = from ? from[(int64_t)min(k, K - 1) * p.V + v0 + min(v, nv - 1)] : 0.f;
+    return k < K && v < nv ? x : 0.f;
+  };
 #pragma unroll
   for (int a = 0; a < NK; ++a)
 #pragma unroll
@@ -99,16 +102,26 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 #pragma unroll
       for (int r = 0; r < 4; ++r) dvk[a][b][r] = entry((wave + b * NW) * 16 + l, a * 16 + 4 * g + r);
 
-  TileLoad<E, C, KP, 16, THREADS, TINY> ql, kl;
-  TileLoad<E, C, VT, 16, THREADS, TINY> vl, dl;
-  float gl = 0.f;
-  auto fetch = [&](int64_t at) {
+  struct Chunk {
+    TileLoad<E, C, KP, 16, THREADS, TINY> q, k;
+    TileLoad<E, C, VT, 16, THREADS, TINY> v, d;
+    float g;
+  };
+  auto fetch = [&](Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-    ql.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
-    kl.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
-    vl.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
-    dl.load(db + at * p.do_stride[1], p.do_stride[1], n, nv);
-    if (wave == 0) gl = lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
+    x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
+    x.d.load(db + at * p.do_stride[1], p.do_stride[1], n, nv);
+    x.g = wave == 0 && lane < n ? gb[(at + lane) * p.g_stride[1]] : 0.f;
+  };
+  auto land = [&](const Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+    x.q.store(qs, n, K);
+    x.k.store(ks, n, K);
+    x.v.store(vs, n, nv);
+    x.d.store(ds, n, nv);
+    if (wave == 0) scan_decays<C>(x.g, dec);
   };
   // wave 0, behind a barrier: the chunk's decay gradients from the waves' sums
   auto decay_gradient = [&](int64_t at) {
@@ -135,27 +148,26 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
         p.dg[token * p.heads + head] = r;
     }
   };
-  // four values of row `token` of a gradient of q or k
+  // a chunk's rows of a gradient of q or k: the gradient itself or this head's and tile's part
   const int part = (head % rep) * p.vtiles + vt;
-  auto put_qk = [&](void* whole, float* parts, int64_t token, int k, f32x4 x) {
+  auto put_qk = [&](void* whole, float* parts, int64_t token, int n, int k, const f32x4 (&x)[1][NI]) {
+    const int64_t stride = (int64_t)p.groups * K;
     if (parts)
-      store4(parts + ((part * p.map.tokens + token) * p.groups + group) * K + k, K - k, x);
+      put_rows<NI, 1>(parts + ((part * p.map.tokens + token) * p.groups + group) * K, stride, n, K, k, 0, l, x);
     else
-      store4(static_cast<E*>(whole) + (token * p.groups + group) * K + k, K - k, x);
+      put_rows<NI, 1>(static_cast<E*>(whole) + (token * p.groups + group) * K, stride, n, K, k, 0, l, x);
   };
 
   const int64_t chunks = (seg.end - seg.begin + C - 1) / C;
-  if (chunks > 0) fetch(seg.begin + (chunks - 1) * C);
+  if (chunks > 0) {
+    Chunk x;
+    fetch(x, seg.begin + (chunks - 1) * C);
+    land(x, seg.begin + (chunks - 1) * C);
+  }
   for (int64_t c = chunks - 1; c >= 0; --c) {
     const int64_t at = seg.begin + c * C;
     const int n = (int)min((int64_t)C, seg.end - at);
-    __syncthreads();  // the chunk behind has been read
-    if (wave == 0 && c + 1 < chunks) decay_gradient(at + C);
-    ql.store(qs, n, K);
-    kl.store(ks, n, K);
-    vl.store(vs, n, nv);
-    dl.store(ds, n, nv);
-    if (wave == 0) scan_decays<C>(gl, dec);
+    __syncthreads();  // the chunk has landed
     // the state before the chunk: rows v = 16 a + 4 g + r, own key columns
     f32x4 h[NV][OK];
     {
@@ -167,8 +179,12 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
           for (int a = 0; a < NV; ++a)
             h[a][b] = *reinterpret_cast<const f32x4*>(hb + ((a * NK + wave + b * NW) * 64 + lane) * 4);
     }
-    __syncthreads();
-    fetch(c > 0 ? at - C : at);  // always: a load under a condition would be waited for where the paths meet
+    // the loads of the chunk before run beside this one's products; always: a load under a condition would be waited
+    // for where the paths meet
+    Chunk next;
+    const int64_t ahead = c > 0 ? at - C : at;
+    fetch(next, ahead);
+    __builtin_amdgcn_sched_barrier(0);  // here and below: phases in order, or their registers add up and spill
 
     // ---- S and D, transposed (rows j, columns i): 16 tokens i per JS waves, which take every JS-th tile of j
     {
@@ -210,6 +226,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
         if (g == 0) wrow[wave][x * 16 + l] = x == it ? rows : 0.f;
     }
     __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
 
     // ---- own keys: dq, dk, and the flows F, E, X
     const float all = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
@@ -220,7 +237,9 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
     for (int b = 0; b < OK; ++b)
       if (wave + b * NW < NK) {
         const int k0 = (wave + b * NW) * 16;
-        f32x4 dq[NI], dk[NI];
+        f32x4 dq_[1][NI], dk_[1][NI];
+        auto& dq = dq_[0];
+        auto& dk = dk_[0];
 #pragma unroll
         for (int x = 0; x < NI; ++x) dq[x] = dk[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -250,6 +269,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
               dk[x] = mma(dp[q], fv, dk[x]);
             }
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
@@ -271,13 +291,8 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
             if (x < j + 2) dk[x] = mma(fq, frag_col_split(dm, j * 16, x * 16), dk[x]);   // tokens i = j .. j + 31
           }
         }
-#pragma unroll
-        for (int x = 0; x < NI; ++x)
-          if (x * 16 + l < n) {
-            const int64_t token = seg.start + at + x * 16 + l;
-            put_qk(p.dq, p.dq_part, token, k0 + 4 * g, dq[x]);
-            put_qk(p.dk, p.dk_part, token, k0 + 4 * g, dk[x]);
-          }
+        put_qk(p.dq, p.dq_part, seg.start + at, n, k0 + 4 * g, dq_);
+        put_qk(p.dk, p.dk_part, seg.start + at, n, k0 + 4 * g, dk_);
       }
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
@@ -291,11 +306,14 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
     xsum = wave_sum(xsum);
     if (lane == 0) xs[wave] = xsum * all;
 
+    __builtin_amdgcn_sched_barrier(0);
+
     // ---- own values: dv
 #pragma unroll
     for (int b = 0; b < OV; ++b) {
       const int w0 = (wave + b * NW) * 16;
-      f32x4 dv[NI];
+      f32x4 dv_[1][NI];
+      auto& dv = dv_[0];
 #pragma unroll
       for (int x = 0; x < NI; ++x) dv[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -323,12 +341,11 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
         for (int x = 0; x < NI; ++x)
           if (x < j + 2) dv[x] = mma(fd, frag_col_split(sm, j * 16, x * 16), dv[x]);
       }
-#pragma unroll
-      for (int x = 0; x < NI; ++x)
-        if (x * 16 + l < n)
-          store4(static_cast<E*>(p.dv) + ((seg.start + at + x * 16 + l) * p.heads + head) * p.V + v0 + w0 + 4 * g,
-                 nv - (w0 + 4 * g), dv[x]);
+      put_rows<NI, 1>(static_cast<E*>(p.dv) + ((seg.start + at) * p.heads + head) * p.V + v0, (int64_t)p.heads * p.V, n,
+                      nv, w0 + 4 * g, 0, l, dv_);
     }
+
+    __builtin_amdgcn_sched_barrier(0);
 
     // ---- d for the chunk before
 #pragma unroll
@@ -381,10 +398,12 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
             for (int q = 0; q < PF; ++q) dvk[a][b] = mma(fv, fq[q], dvk[a][b]);
           }
         }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    __syncthreads();  // the chunk has been read, the waves' sums are there
+    if (wave == 0) decay_gradient(at);
+    land(next, ahead);
   }
-  __syncthreads();
-  if (wave == 0 && chunks > 0) decay_gradient(seg.begin);
 
   if (seg.begin == 0 && p.dstate_in)
 #pragma unroll
