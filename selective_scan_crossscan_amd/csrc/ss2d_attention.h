@@ -84,30 +84,32 @@ size_t attention_backward_workspace_bytes(const AttentionPlan& pl, int64_t token
                                           int64_t key_dim, int64_t value_dim);
 hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const AttentionPlan& pl);
 
-// The state's passes over keys and values alone (ss2d_attention_state.hip).
+// The state's passes over keys and values alone (ss2d_attention_state.hip), in tiles
+// of 64 value columns whatever the plan's.
 enum StatePass {
-  kSegmentStates,   // what each segment (but a sequence's last) adds to the state, from 0, and its whole decay
-  kChunkStates,     // the state before every chunk
-  kSegmentGradients // what each segment (but the first) adds to the state's gradient, from 0, walking backwards
+  kSegmentStates,    // what each segment (but a sequence's last) adds to the state, from 0, and its whole decay
+  kChunkStates,      // the state before every chunk
+  kSegmentGradients  // what each segment (but the first) adds to the state's gradient, from 0, walking backwards
 };
 struct StateParams {
-  const void *k, *v;  // kSegmentGradients: q and d_o
+  const void *k, *v;      // gradients: q and d_o
   const float* g;
-  const float* state_in;     // or null
-  float* seg_state;          // (slot, head, K, V)
-  float* seg_decay;          // (slot, head)
-  float* chunk_state;        // kChunkStates: (chunk, head, value tile, KP x VT as the kernel lays it out)
+  const float* state_in;  // the sequences' initial states (gradients: of their final states), or null
+  float* seg_state;       // (slot, head, K, V)
+  float* seg_decay;       // (slot, head)
+  float* chunk_state;     // chunk states: (chunk, head, tile, KP x 64 as the kernel lays it out)
   SequenceMap map;
   int64_t k_stride[3], v_stride[3], g_stride[3];
-  int groups, heads, K, V, vtiles;
+  int groups, heads, K, V, tiles;  // tiles of 64 value columns
   float scale;
-  bool split;                // segments start from seg_state
+  bool split;             // segments start from seg_state
 };
-hipError_t launch_state_pass(StatePass pass, const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
-// seg_state: from what each segment adds to the state before it (forward) or the
-// gradient of the state behind it (reverse); `from` is the sequences' initial
-// state or final gradient, or null.
-hipError_t launch_state_carry(bool reverse, const StateParams& p, const float* from, hipStream_t st);
+// seg_state: the state before every segment but a sequence's first.
+hipError_t launch_segment_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
+// The same, and r's seg_state: the gradient of the state behind every segment but a sequence's last.
+hipError_t launch_segment_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, int dtype,
+                               hipStream_t st);
+hipError_t launch_chunk_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
 
 namespace tok {
 

@@ -355,10 +355,10 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& pl) {
     s.heads = p.heads;
     s.K = p.K;
     s.V = p.V;
-    s.vtiles = pl.vtiles;
+    s.tiles = (int)((a.value_dim + 63) / 64);
+    s.state_in = a.state_in;
     p.seg_state = s.seg_state;
-    hipError_t e = launch_state_pass(kSegmentStates, s, pl, a.dtype, a.stream);
-    if (e == hipSuccess) e = launch_state_carry(false, s, a.state_in, a.stream);
+    const hipError_t e = launch_segment_states(s, pl, a.dtype, a.stream);
     if (e != hipSuccess) return e;
   }
   if (a.dtype == 1)

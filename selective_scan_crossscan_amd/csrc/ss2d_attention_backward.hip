@@ -429,7 +429,7 @@ __global__ __launch_bounds__(256) void sum_parts(const float* __restrict__ parts
 
 // Byte offsets of the workspace's regions.
 struct Regions {
-  size_t chunk_state, seg_state, seg_dstate, seg_decay, dq_part, dk_part, dg_part, end;
+  size_t chunk_state, seg_state, seg_dstate, seg_decay, seg_decay_back, dq_part, dk_part, dg_part, end;
   int parts;
 };
 Regions regions(const AttentionPlan& pl, int64_t tokens, int64_t groups, int64_t heads, int64_t K, int64_t V) {
@@ -445,6 +445,7 @@ Regions regions(const AttentionPlan& pl, int64_t tokens, int64_t groups, int64_t
   r.seg_state = take(pl.split ? pl.slots * heads * K * V : 0);
   r.seg_dstate = take(pl.split ? pl.slots * heads * K * V : 0);
   r.seg_decay = take(pl.split ? pl.slots * heads : 0);
+  r.seg_decay_back = take(pl.split ? pl.slots * heads : 0);
   r.dq_part = take(r.parts > 1 ? r.parts * tokens * groups * K : 0);
   r.dk_part = take(r.parts > 1 ? r.parts * tokens * groups * K : 0);
   r.dg_part = take(pl.vtiles > 1 ? pl.vtiles * tokens * heads : 0);
@@ -497,23 +498,10 @@ hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const Atten
   s.heads = (int)f.heads;
   s.K = (int)f.key_dim;
   s.V = (int)f.value_dim;
-  s.vtiles = pl.vtiles;
+  s.tiles = pl.vtiles * (pl.vt / 64);
   s.scale = f.scale;
   s.split = pl.split;
   for (int i = 0; i < 3; ++i) s.g_stride[i] = f.g_stride[i];
-  hipError_t e = hipSuccess;
-  if (pl.split) {  // the gradients of the states behind the segments
-    s.k = f.q;
-    s.v = a.d_o;
-    s.seg_state = at(rg.seg_dstate);
-    for (int i = 0; i < 3; ++i) {
-      s.k_stride[i] = f.q_stride[i];
-      s.v_stride[i] = a.do_stride[i];
-    }
-    e = launch_state_pass(kSegmentGradients, s, pl, f.dtype, f.stream);
-    if (e == hipSuccess) e = launch_state_carry(true, s, a.dstate_out, f.stream);
-    if (e != hipSuccess) return e;
-  }
   s.k = f.k;
   s.v = f.v;
   s.state_in = f.state_in;
@@ -522,12 +510,22 @@ hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const Atten
     s.k_stride[i] = f.k_stride[i];
     s.v_stride[i] = f.v_stride[i];
   }
-  if (pl.split) {  // the states before them
-    e = launch_state_pass(kSegmentStates, s, pl, f.dtype, f.stream);
-    if (e == hipSuccess) e = launch_state_carry(false, s, f.state_in, f.stream);
+  hipError_t e = hipSuccess;
+  if (pl.split) {  // the states before the segments and the gradients of those behind them
+    StateParams r = s;
+    r.k = f.q;
+    r.v = a.d_o;
+    r.state_in = a.dstate_out;
+    r.seg_state = at(rg.seg_dstate);
+    r.seg_decay = at(rg.seg_decay_back);
+    for (int i = 0; i < 3; ++i) {
+      r.k_stride[i] = f.q_stride[i];
+      r.v_stride[i] = a.do_stride[i];
+    }
+    e = launch_segment_pair(s, r, pl, f.dtype, f.stream);
     if (e != hipSuccess) return e;
   }
-  e = launch_state_pass(kChunkStates, s, pl, f.dtype, f.stream);
+  e = launch_chunk_states(s, pl, f.dtype, f.stream);
   if (e != hipSuccess) return e;
 
   BackwardParams p{};

@@ -5,12 +5,15 @@
 // d <- exp(G_last) d + sum_i scale exp(G_i) q_i do_i': the same sum with q, do
 // and other weights, chunks in reverse.
 //
-// One workgroup of four waves owns a head's VT value columns of one segment; a
-// wave owns VT / 4 of them.  The state is kept transposed (result tiles with
+// One workgroup of four waves owns 64 value columns of a head and one segment; a
+// wave owns 16 of them.  (128 columns would read the keys half as often, but took
+// as long: more and smaller workgroups per CU hide more of the latency.)  The state is kept transposed (result tiles with
 // rows v and columns k): a lane then holds four consecutive values of one key
 // row for 16-byte accesses, and a pair of tiles is, as it lies in registers, an
 // operand whose inner index is v.  The decayed v (do) goes into the product in
 // parts that keep all of its bits.
+#include <type_traits>
+
 #include "ss2d_attention.h"
 
 namespace ss2d {
@@ -18,30 +21,38 @@ namespace {
 
 using namespace tok;
 
-template <typename E, int C, int KP, int VT, StatePass PASS, bool TINY>
-__global__ __launch_bounds__(256, 2) void state_kernel(StateParams p) {
+template <typename E, int C, int KP>
+struct StateTiles {
+  Tile<E, C, KP, 32> ks;
+  Tile<E, C, 64, 32> vs;
+  Decays<C> dec;
+};
+
+// One segment's tile of 64 value columns; block: its number among the pass's.
+template <typename E, int C, int KP, StatePass PASS, bool TINY>
+__device__ __forceinline__ void state_walk(const StateParams& p, int block, StateTiles<E, C, KP>& lds) {
   constexpr bool REVERSE = PASS == kSegmentGradients;
-  constexpr int NI = C / 16, NK = KP / 16, NV = VT / 64, PF = kFullParts<E>;
-  __shared__ Tile<E, C, KP, 32> ks;
-  __shared__ Tile<E, C, VT, 32> vs;
-  __shared__ Decays<C> dec;
+  constexpr int VT = 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
+  auto& ks = lds.ks;
+  auto& vs = lds.vs;
+  auto& dec = lds.dec;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const int vt = blockIdx.x % p.vtiles;
-  const int head = (blockIdx.x / p.vtiles) % p.heads;
-  const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
+  const int vt = block % p.tiles;
+  const int head = (block / p.tiles) % p.heads;
+  const int64_t slot = block / (p.tiles * p.heads);
   Segment seg;
   if (!find_segment(p.map, slot, seg)) return;
   if (PASS == kSegmentStates ? seg.last : PASS == kSegmentGradients ? seg.begin == 0 : false) return;  // of no use
   const int group = head / (p.heads / p.groups);
-  const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), vw = wave * (VT / 4);
+  const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), vw = wave * 16;
   const bool active = vw < nv;
   const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
   const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + first * p.k_stride[1] + group * p.k_stride[2];
   const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + first * p.v_stride[1] + head * p.v_stride[2] + v0;
   const float* gb = p.g + sq * p.g_stride[0] + first * p.g_stride[1] + head * p.g_stride[2];
 
-  // rows v = vw + 16 t + 4 g + r, column k = 16 kt + l
-  f32x4 h[NV][NK];
+  // rows v = vw + 4 g + r, column k = 16 kt + l
+  f32x4 h[NK];
   const int64_t sh = (slot * p.heads + head) * K * p.V;
   const float* from = PASS != kChunkStates              ? nullptr
                       : p.split && seg.begin > 0        ? p.seg_state + sh
@@ -49,19 +60,14 @@ __global__ __launch_bounds__(256, 2) void state_kernel(StateParams p) {
                                                         : nullptr;
   if (from)
 #pragma unroll
-    for (int t = 0; t < NV; ++t)
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          h[t][kt][r] = from[(int64_t)min(kt * 16 + l, K - 1) * p.V + v0 + min(vw + t * 16 + 4 * g + r, nv - 1)];
-#pragma unroll
-  for (int t = 0; t < NV; ++t)
-#pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        h[t][kt][r] = from && kt * 16 + l < K && vw + t * 16 + 4 * g + r < nv ? h[t][kt][r] : 0.f;
+        h[kt][r] = from[(int64_t)min(kt * 16 + l, K - 1) * p.V + v0 + min(vw + 4 * g + r, nv - 1)];
+#pragma unroll
+  for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[kt][r] = from && kt * 16 + l < K && vw + 4 * g + r < nv ? h[kt][r] : 0.f;
 
   struct Chunk {
     TileLoad<E, C, KP, 32, 256, TINY> k;
@@ -90,12 +96,10 @@ __global__ __launch_bounds__(256, 2) void state_kernel(StateParams p) {
   }
   for (int64_t c = 0; c < chunks; ++c) {
     if (PASS == kChunkStates) {  // before the chunk, as it lies in registers: 1 KiB per tile and wave
-      float* to = p.chunk_state + ((chunk_number<C>(p.map, seg, start_of(c)) * p.heads + head) * p.vtiles + vt) * (KP * VT);
+      const int64_t chunk = chunk_number<C>(p.map, seg, start_of(c));
+      float* to = p.chunk_state + ((chunk * p.heads + head) * p.tiles + vt) * (KP * VT);
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int kt = 0; kt < NK; ++kt)
-          *reinterpret_cast<f32x4*>(to + (((wave * NV + t) * NK + kt) * 64 + lane) * 4) = h[t][kt];
+      for (int kt = 0; kt < NK; ++kt) *reinterpret_cast<f32x4*>(to + ((wave * NK + kt) * 64 + lane) * 4) = h[kt];
       if (c + 1 == chunks) break;  // the state behind the last chunk is not needed
     }
     __syncthreads();  // the chunk has landed
@@ -109,58 +113,69 @@ __global__ __launch_bounds__(256, 2) void state_kernel(StateParams p) {
     frac += dec.frac[C - 1];
     if (active) {
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int kt = 0; kt < NK; ++kt) h[t][kt] *= a;
+      for (int kt = 0; kt < NK; ++kt) h[kt] *= a;
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        Frag<E> b[NV][PF];
         const int i0 = j * 16 + 4 * g;
         const f32x4 w0 = REVERSE ? dec.since4(i0) * p.scale : dec.between4(C - 1, i0);
         const f32x4 w1 = REVERSE ? dec.since4(i0 + 16) * p.scale : dec.between4(C - 1, i0 + 16);
+        Frag<E> b[PF];
+        float x[8];
+        frag_values(frag_col_split(vs, j * 16, vw), x);
 #pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float x[8];
-          frag_values(frag_col_split(vs, j * 16, vw + t * 16), x);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] *= w0[r];
-            x[4 + r] *= w1[r];
-          }
-          split_parts(x, b[t]);
+        for (int r = 0; r < 4; ++r) {
+          x[r] *= w0[r];
+          x[4 + r] *= w1[r];
         }
+        split_parts(x, b);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt) {
           const Frag<E> k = frag_col_split(ks, j * 16, kt * 16);
 #pragma unroll
-          for (int q = 0; q < PF; ++q)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) h[t][kt] = mma(b[t][q], k, h[t][kt]);
+          for (int q = 0; q < PF; ++q) h[kt] = mma(b[q], k, h[kt]);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
     }
     __syncthreads();  // the chunk has been read
     land(next, ahead);
   }
   if (PASS != kChunkStates) {
+    const int v = vw + 4 * g;
 #pragma unroll
-    for (int t = 0; t < NV; ++t)
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt) {
-        const int k = kt * 16 + l, v = vw + t * 16 + 4 * g;
-        if (k < K) store4(p.seg_state + sh + (int64_t)k * p.V + v0 + v, nv - v, h[t][kt]);
-      }
+    for (int kt = 0; kt < NK; ++kt) {
+      const int k = kt * 16 + l;
+      if (k < K) store4(p.seg_state + sh + (int64_t)k * p.V + v0 + v, nv - v, h[kt]);
+    }
     if (vt == 0 && threadIdx.x == 0) p.seg_decay[slot * p.heads + head] = __builtin_amdgcn_exp2f(whole + frac);
   }
 }
 
-// One thread per state entry walks its sequence's segments.
-__global__ __launch_bounds__(256) void state_carry(StateParams p, const float* from, bool reverse) {
+template <typename E, int C, int KP, StatePass PASS, bool TINY>
+__global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_kernel(StateParams p) {
+  __shared__ StateTiles<E, C, KP> lds;
+  state_walk<E, C, KP, PASS, TINY>(p, blockIdx.x, lds);
+}
+
+// What the segments add to the state and to its gradient, one after the other in
+// one grid: each alone leaves CUs idle where sequences had to be cut.
+template <typename E, int C, int KP, bool TINY>
+__global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_pair_kernel(StateParams p, StateParams r) {
+  __shared__ StateTiles<E, C, KP> lds;
+  const int n = gridDim.x / 2;
+  if ((int)blockIdx.x < n)
+    state_walk<E, C, KP, kSegmentStates, TINY>(p, blockIdx.x, lds);
+  else
+    state_walk<E, C, KP, kSegmentGradients, TINY>(r, blockIdx.x - n, lds);
+}
+
+// seg_state: from what each segment adds to the state before it, or, in reverse, to
+// the gradient of the state behind it.  One thread per state entry walks its
+// sequence's segments, eight sums read at a time.
+__device__ __forceinline__ void carry_walk(const StateParams& p, const float* from, bool reverse, int64_t block) {
   const int64_t kv = (int64_t)p.K * p.V;
   const int64_t blocks = (kv + 255) / 256;
-  const int64_t e = blockIdx.x % blocks * 256 + threadIdx.x;
-  const int head = (int)(blockIdx.x / blocks % p.heads), s = (int)(blockIdx.x / blocks / p.heads);
+  const int64_t e = block % blocks * 256 + threadIdx.x;
+  const int head = (int)(block / blocks % p.heads), s = (int)(block / blocks / p.heads);
   if (e >= kv) return;
   int64_t slot, len;
   if (p.map.cu) {
@@ -173,55 +188,102 @@ __global__ __launch_bounds__(256) void state_carry(StateParams p, const float* f
   }
   const int64_t n = (len + p.map.seg_len - 1) / p.map.seg_len;  // segments
   if (n < 2) return;
-  // along the walk: the first segment's sum moves the state on, and what lies before (behind) the next one replaces its sum
+  // along the walk: a segment's sum moves the state on, and what lies before (behind) the next one replaces its sum
   if (reverse) slot += n - 1;
   const int dir = reverse ? -1 : 1;
   const int64_t step = dir * p.heads * kv;
   float* u = p.seg_state + (slot * p.heads + head) * kv + e;
+  const float* a = p.seg_decay + slot * p.heads + head;
   float h = from ? from[((int64_t)s * p.heads + head) * kv + e] : 0.f;
-  float add = *u;
-  for (int64_t i = 0; i + 1 < n; ++i, slot += dir) {
-    h = fmaf(p.seg_decay[slot * p.heads + head], h, add);
-    u += step;
-    if (i + 2 < n) add = *u;
-    *u = h;
+  constexpr int N = 8;
+  float first = *u;  // the sum of segment i, kept: its place is overwritten
+  for (int64_t i = 0; i + 1 < n; i += N) {
+    float add[N], decay[N];
+    add[0] = first;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t at = i + j < n - 1 ? i + j : n - 1;  // a place inside, no branch around the load
+      if (j > 0) add[j] = u[at * step];
+      decay[j] = a[at * dir * p.heads];
+    }
+    first = u[(i + N < n - 1 ? i + N : n - 1) * step];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (i + j + 1 < n) {
+        h = fmaf(decay[j], h, add[j]);
+        u[(i + j + 1) * step] = h;
+      }
   }
 }
 
-template <typename E, int C, int VT, StatePass PASS>
-hipError_t launch_k(const StateParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(256);
-  if (pl.tiny) {
-    state_kernel<E, C, 256, 64, PASS, true><<<grid, block, 0, st>>>(p);
-    return hipGetLastError();
-  }
-  switch (pl.kp) {
-    case 32: state_kernel<E, C, 32, VT, PASS, false><<<grid, block, 0, st>>>(p); break;
-    case 64: state_kernel<E, C, 64, VT, PASS, false><<<grid, block, 0, st>>>(p); break;
-    case 128: state_kernel<E, C, 128, VT, PASS, false><<<grid, block, 0, st>>>(p); break;
-    default: state_kernel<E, C, 256, VT, PASS, false><<<grid, block, 0, st>>>(p);
-  }
-  return hipGetLastError();
+__global__ __launch_bounds__(256) void state_carry(StateParams p, const float* from) {
+  carry_walk(p, from, false, blockIdx.x);
 }
 
-template <typename E, int C, int VT>
-hipError_t launch_p(StatePass pass, const StateParams& p, const AttentionPlan& pl, hipStream_t st) {
-  if (pass == kSegmentStates) return launch_k<E, C, VT, kSegmentStates>(p, pl, st);
-  if (pass == kChunkStates) return launch_k<E, C, VT, kChunkStates>(p, pl, st);
-  return launch_k<E, C, VT, kSegmentGradients>(p, pl, st);
+__global__ __launch_bounds__(256) void state_carry_pair(StateParams p, const float* from, StateParams r,
+                                                        const float* behind) {
+  const int n = gridDim.x / 2;
+  if ((int)blockIdx.x < n)
+    carry_walk(p, from, false, blockIdx.x);
+  else
+    carry_walk(r, behind, true, blockIdx.x - n);
+}
+
+// Calls f with the padded key size and whether rows are tiny as constants.
+template <typename F>
+void with_keys(const AttentionPlan& pl, F f) {
+  using std::integral_constant;
+  if (pl.tiny)
+    f(integral_constant<int, 256>(), integral_constant<bool, true>());
+  else if (pl.kp == 32)
+    f(integral_constant<int, 32>(), integral_constant<bool, false>());
+  else if (pl.kp == 64)
+    f(integral_constant<int, 64>(), integral_constant<bool, false>());
+  else if (pl.kp == 128)
+    f(integral_constant<int, 128>(), integral_constant<bool, false>());
+  else
+    f(integral_constant<int, 256>(), integral_constant<bool, false>());
+}
+
+unsigned grid_of(const StateParams& p, const AttentionPlan& pl) { return (unsigned)(pl.slots * p.heads * p.tiles); }
+unsigned carry_grid_of(const StateParams& p) {
+  return (unsigned)(((int64_t)p.K * p.V + 255) / 256 * p.heads * p.map.sequences);
+}
+
+template <typename E, int C>
+void launch_single(StatePass pass, const StateParams& p, const AttentionPlan& pl, hipStream_t st) {
+  with_keys(pl, [&](auto kp, auto tiny) {
+    if (pass == kSegmentStates)
+      state_kernel<E, C, kp(), kSegmentStates, tiny()><<<dim3(grid_of(p, pl)), dim3(256), 0, st>>>(p);
+    else
+      state_kernel<E, C, kp(), kChunkStates, tiny()><<<dim3(grid_of(p, pl)), dim3(256), 0, st>>>(p);
+  });
+}
+
+template <typename E, int C>
+void launch_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, hipStream_t st) {
+  with_keys(pl, [&](auto kp, auto tiny) {
+    state_pair_kernel<E, C, kp(), tiny()><<<dim3(2 * grid_of(p, pl)), dim3(256), 0, st>>>(p, r);
+  });
 }
 
 }  // namespace
 
-hipError_t launch_state_pass(StatePass pass, const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st) {
-  if (dtype == 1)
-    return pl.vt == 64 ? launch_p<uint16_t, 64, 64>(pass, p, pl, st) : launch_p<uint16_t, 64, 128>(pass, p, pl, st);
-  return pl.vt == 64 ? launch_p<float, 32, 64>(pass, p, pl, st) : launch_p<float, 32, 128>(pass, p, pl, st);
+hipError_t launch_segment_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st) {
+  dtype == 1 ? launch_single<uint16_t, 64>(kSegmentStates, p, pl, st) : launch_single<float, 32>(kSegmentStates, p, pl, st);
+  state_carry<<<dim3(carry_grid_of(p)), dim3(256), 0, st>>>(p, p.state_in);
+  return hipGetLastError();
 }
 
-hipError_t launch_state_carry(bool reverse, const StateParams& p, const float* from, hipStream_t st) {
-  const int64_t blocks = ((int64_t)p.K * p.V + 255) / 256;
-  state_carry<<<dim3((unsigned)(blocks * p.heads * p.map.sequences)), dim3(256), 0, st>>>(p, from, reverse);
+hipError_t launch_segment_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, int dtype,
+                               hipStream_t st) {
+  dtype == 1 ? launch_pair<uint16_t, 64>(p, r, pl, st) : launch_pair<float, 32>(p, r, pl, st);
+  state_carry_pair<<<dim3(2 * carry_grid_of(p)), dim3(256), 0, st>>>(p, p.state_in, r, r.state_in);
+  return hipGetLastError();
+}
+
+hipError_t launch_chunk_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st) {
+  dtype == 1 ? launch_single<uint16_t, 64>(kChunkStates, p, pl, st) : launch_single<float, 32>(kChunkStates, p, pl, st);
   return hipGetLastError();
 }
 
