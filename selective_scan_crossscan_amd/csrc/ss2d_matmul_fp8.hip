@@ -124,18 +124,33 @@ __device__ __forceinline__ void store_out(uint16_t* p, int64_t n, f32x4 v) {
 
 // ------------------------------------------------------------------ tiles of 128 x 128
 constexpr int kTile = 128;
+constexpr int kScaleStep = 16;  // blocks of a's scales in LDS at a time
 
-// Four waves, 64 x 64 outputs each.  An operand's 128 rows of one block lie in LDS
-// as 128-byte rows of eight 16-byte pieces, piece q of row r in place q ^ (r % 8):
-// eight rows' reads of one piece then fall into different banks.  DMA: rows are 16-byte
-// aligned and whole pieces long; pieces go from memory to LDS without registers,
-// and those outside the operand read as 0 by the buffer's bounds.  Otherwise they
-// go through registers, byte by byte at a row's end.
+// Four waves, 64 x 64 outputs each; two workgroups share a CU.  An operand's 128
+// rows of one block lie in LDS, double buffered, as 128-byte rows of eight 16-byte
+// pieces, piece q of row r in place q ^ (r / 2 % 8): sixteen rows' reads of one piece
+// then fall into different banks (two rows to the 64 banks, eight places each).  (Fragments straight from memory would spare half of
+// LDS's traffic, but a wave's 16 rows by four pieces 32 bytes apart are 64 separate
+// addresses: 232 us where this takes 136, 5001 x 4096 x 4096.)  a's scales, one
+// per row and block, come through LDS as well, sixteen blocks at a time: read from
+// memory where they are used, sixteen rows' lines for four bytes each, they cost a
+// quarter of the time.
+// DMA: rows are 16-byte aligned and whole pieces long; pieces go from memory to LDS
+// without registers, and those outside the operand read as 0 by the buffer's bounds.
+// Otherwise they go through registers, byte by byte at a row's end.
 template <typename O, bool DMA>
-__global__ __launch_bounds__(256) void matmul_fp8_tiles(MatmulParams p) {
+__global__ __launch_bounds__(256, 2) void matmul_fp8_tiles(MatmulParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t sm[2][kTile * kScaleBlock], sn[2][kTile * kScaleBlock];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const int64_t m0 = (int64_t)(blockIdx.x % p.mtiles) * kTile, n0 = (int64_t)(blockIdx.x / p.mtiles) * kTile;
+  __shared__ float scale[kTile * (kScaleStep + 1)];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, g = lane >> 4,
+            l = lane & 15;
+  // Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets a band of columns of tiles and walks
+  // down it row by row, so that a row of a is read once for the whole band and the band's rows of b stay in its L2.
+  const int total = p.mtiles * p.ntiles, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
+  const int at = xcd * each + min(xcd, more) + (blockIdx.x >> 3);
+  const int width = (p.ntiles + 7) >> 3, band = at / (width * p.mtiles), rest = at - band * width * p.mtiles;
+  const int here = min(width, p.ntiles - band * width);  // the last band may be narrower
+  const int64_t m0 = (int64_t)(rest / here) * kTile, n0 = (int64_t)(band * width + rest % here) * kTile;
   const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
   const int rows_m = (int)min((int64_t)kTile, p.M - m0), rows_n = (int)min((int64_t)kTile, p.N - n0);
   const uint8_t *a = p.a + m0 * p.K, *b = p.b + n0 * p.K;
@@ -149,7 +164,7 @@ __global__ __launch_bounds__(256) void matmul_fp8_tiles(MatmulParams p) {
   auto fetch = [&](int kb, int buf) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int place = (wave * 4 + i) * 64 + lane, row = place >> 3, c = kb * kScaleBlock + ((place & 7) ^ (row & 7)) * 16;
+      const int place = (wave * 4 + i) * 64 + lane, row = place >> 3, c = kb * kScaleBlock + ((place & 7) ^ ((row >> 1) & 7)) * 16;
       if (DMA) {
         const uint32_t at = c < p.K ? (uint32_t)row * (uint32_t)p.K + c : 1u << 30;  // past any operand's rows: 128 x 2^20 bytes
         __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(sm[buf] + (wave * 4 + i) * 1024), 16, at, 0, 0, 0);
@@ -169,16 +184,21 @@ __global__ __launch_bounds__(256) void matmul_fp8_tiles(MatmulParams p) {
         *reinterpret_cast<i32x4*>(sn[buf] + place * 16) = stage_n[i];
       }
   };
+  // scales of blocks kb .. kb + 15: a row's sixteen by sixteen lanes
+  auto fetch_scales = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < kTile * kScaleStep / 256; ++i) {
+      const int idx = threadIdx.x + i * 256, row = idx / kScaleStep, c = idx % kScaleStep;
+      scale[row * (kScaleStep + 1) + c] = p.sa[(m0 + min(row, rows_m - 1)) * p.blocks + min(kb + c, p.blocks - 1)];
+    }
+  };
   auto fragment = [&](const uint8_t* s, int row) {
     const uint8_t* r = s + row * kScaleBlock;
-    const i32x4 x = *reinterpret_cast<const i32x4*>(r + ((2 * g) ^ (row & 7)) * 16);
-    const i32x4 y = *reinterpret_cast<const i32x4*>(r + ((2 * g + 1) ^ (row & 7)) * 16);
+    const i32x4 x = *reinterpret_cast<const i32x4*>(r + ((2 * g) ^ ((row >> 1) & 7)) * 16);
+    const i32x4 y = *reinterpret_cast<const i32x4*>(r + ((2 * g + 1) ^ ((row >> 1) & 7)) * 16);
     return Operand<O>(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   const float* sbp = p.sb + (n0 / kScaleBlock) * p.blocks;
-  const float* sap[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) sap[t] = p.sa + min(m0 + wm + t * 16 + l, p.M - 1) * p.blocks;
 
   f32x4 acc[4][4];
 #pragma unroll
@@ -189,6 +209,10 @@ __global__ __launch_bounds__(256) void matmul_fp8_tiles(MatmulParams p) {
   land(0);
   for (int kb = 0; kb < p.blocks; ++kb) {
     const int buf = kb & 1;
+    if (kb % kScaleStep == 0) {
+      if (kb > 0) __syncthreads();  // the scales before have been read
+      fetch_scales(kb);
+    }
     if (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's pieces have landed
     __syncthreads();  // the block is whole, the other buffer has been read
     if (kb + 1 < p.blocks) fetch(kb + 1, buf ^ 1);
@@ -197,7 +221,7 @@ __global__ __launch_bounds__(256) void matmul_fp8_tiles(MatmulParams p) {
     Operand<O> fm[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      s[t] = sap[t][kb] * sb;
+      s[t] = scale[(wm + t * 16 + l) * (kScaleStep + 1) + kb % kScaleStep] * sb;
       fm[t] = fragment(sm[buf], wm + t * 16 + l);
     }
 #pragma unroll
