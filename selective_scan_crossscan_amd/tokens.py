@@ -29,24 +29,30 @@ def _code(x) -> int:
     return code
 
 
-def _require(name, x, device, dtype, shape=None, dense=True):
-    """x is a tensor of this device, dtype and shape (None: not checked)."""
-    if not x.is_cuda:
-        raise ValueError("all tensors must be on the GPU (no CPU fallback)")
-    if x.device != device:
-        raise ValueError("all tensors must be on the same device")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and x.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}")
-    if dense and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _require(first, *items):
+    """Each item (name, tensor, dtype, shape, dense) is a GPU tensor on `first`'s device of that dtype and shape (None: not
+    checked), contiguous if dense.  One cheap condition per tensor: a single token's call has six of them."""
+    index = first.get_device()
+    for name, x, dtype, shape, dense in items:
+        if (x.dtype is not dtype or x.get_device() != index or (shape is not None and x.shape != shape)
+                or (dense and not x.is_contiguous()) or index < 0):
+            if not x.is_cuda or not first.is_cuda:
+                raise ValueError("all tensors must be on the GPU (no CPU fallback)")
+            if x.device != first.device:
+                raise ValueError("all tensors must be on the same device")
+            if x.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}")
+            if shape is not None and x.shape != shape:
+                raise ValueError(f"{name} must be {tuple(shape)}")
+            raise ValueError(f"{name} must be contiguous")
 
 
 def _call(fn, device, *args):
     """fn(*args, current stream) with `device` current; raises on a status code."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    index = device.index
+    # the raw handle: torch.cuda.current_stream builds a Stream object around it, 2 us of a call's 10
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -64,6 +70,11 @@ def _on_stream(stream, device, fn, *args, **kwargs):
 
 def _ptr(x):
     return None if x is None else x.data_ptr()
+
+
+def _empty(x):
+    """A contiguous tensor of x's shape and dtype beside it."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _workspace(bytes_, device):
@@ -91,18 +102,16 @@ def _attention_sizes(q, k, v, log_decay, cu_seqlens, do=None):
     n = 3 if packed else 4
     if v.dim() != n or q.dim() != n or k.dim() != n:
         raise ValueError("q, k, v must be (T, heads, dim) with cu_seqlens, else (S, L, heads, dim)")
-    code, device = _code(v), v.device
-    lead = tuple(v.shape[:-2])
-    H, V = v.shape[-2:]
+    code, dtype = _code(v), v.dtype
+    shape = v.shape
+    lead, (H, V) = shape[:-2], shape[-2:]
     G, K = q.shape[-2:]
-    _require("v", v, device, v.dtype, dense=False)
-    _require("q", q, device, v.dtype, lead + (G, K), dense=False)
-    _require("k", k, device, v.dtype, lead + (G, K), dense=False)
-    _require("log_decay", log_decay, device, torch.float32, lead + (H,), dense=False)
+    _require(v, ("v", v, dtype, None, False), ("q", q, dtype, lead + (G, K), False),
+             ("k", k, dtype, lead + (G, K), False), ("log_decay", log_decay, torch.float32, lead + (H,), False))
     if G < 1 or H % G != 0:
         raise ValueError("the heads of v must be a multiple of those of q and k")
     if packed:
-        _require("cu_seqlens", cu_seqlens, device, torch.int32)
+        _require(v, ("cu_seqlens", cu_seqlens, torch.int32, None, True))
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
             raise ValueError("cu_seqlens must be (sequences + 1,)")
         S, T = cu_seqlens.shape[0] - 1, lead[0]
@@ -111,7 +120,7 @@ def _attention_sizes(q, k, v, log_decay, cu_seqlens, do=None):
     sizes = [S, T, G, H, K, V, *_token_strides("q", q, lead), *_token_strides("k", k, lead),
              *_token_strides("v", v, lead), *_token_strides("log_decay", log_decay, lead)]
     if do is not None:
-        _require("do", do, device, v.dtype, v.shape, dense=False)
+        _require(v, ("do", do, dtype, shape, False))
         sizes += _token_strides("do", do, lead)
     return _SIZES(*sizes), lead, S, G, H, K, V, code
 
@@ -134,11 +143,11 @@ def linear_attention(q, k, v, log_decay, state=None, cu_seqlens=None, scale: flo
     sizes, lead, S, G, H, K, V, code = _attention_sizes(q, k, v, log_decay, cu_seqlens)
     device = v.device
     if state is not None:
-        _require("state", state, device, torch.float32, (S, H, K, V))
+        _require(v, ("state", state, torch.float32, (S, H, K, V), True))
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=device)
+        out = _empty(v)
     else:
-        _require("out", out, device, v.dtype, v.shape)
+        _require(v, ("out", out, v.dtype, v.shape, True))
     last = torch.empty((S, H, K, V), dtype=torch.float32, device=device) if final_state else None
     L = lib()
     nbytes = L.ss2d_linear_attention_workspace(sizes, 0 if cu_seqlens is None else 1, code)
@@ -161,13 +170,11 @@ def linear_attention_backward(q, k, v, log_decay, do, state=None, dfinal_state=N
                           cu_seqlens, scale)
     sizes, lead, S, G, H, K, V, code = _attention_sizes(q, k, v, log_decay, cu_seqlens, do)
     device = v.device
-    out = {"dq": torch.empty(q.shape, dtype=v.dtype, device=device),
-           "dk": torch.empty(q.shape, dtype=v.dtype, device=device),
-           "dv": torch.empty(v.shape, dtype=v.dtype, device=device),
+    out = {"dq": _empty(q), "dk": _empty(q), "dv": _empty(v),
            "dlog_decay": torch.empty(lead + (H,), dtype=torch.float32, device=device)}
     for name, t in (("state", state), ("dfinal_state", dfinal_state)):
         if t is not None:
-            _require(name, t, device, torch.float32, (S, H, K, V))
+            _require(v, (name, t, torch.float32, (S, H, K, V), True))
     if state is not None:
         out["dstate"] = torch.empty((S, H, K, V), dtype=torch.float32, device=device)
     L = lib()
@@ -192,30 +199,28 @@ def linear_attention_step(q, k, v, log_decay, state, state_index=None, scale: fl
         return _on_stream(stream, v.device, linear_attention_step, q, k, v, log_decay, state, state_index, scale, out)
     if v.dim() != 3 or q.dim() != 3 or state.dim() != 4:
         raise ValueError("q, k must be (B,G,K), v (B,H,V), state (slots,H,K,V)")
-    code, device = _code(v), v.device
+    code, dtype = _code(v), v.dtype
     B, H, V = v.shape
-    G, K = q.shape[1:]
-    slots = state.shape[0]
-    _require("v", v, device, v.dtype, dense=False)
-    _require("q", q, device, v.dtype, (B, G, K), dense=False)
-    _require("k", k, device, v.dtype, (B, G, K), dense=False)
-    _require("log_decay", log_decay, device, torch.float32, (B, H))
-    _require("state", state, device, torch.float32, (slots, H, K, V))
+    qshape, cache = q.shape, state.shape
+    G, K = qshape[1:]
+    _require(v, ("v", v, dtype, None, False), ("q", q, dtype, (B, G, K), False), ("k", k, dtype, qshape, False),
+             ("log_decay", log_decay, torch.float32, (B, H), True),
+             ("state", state, torch.float32, (cache[0], H, K, V), True))
     if G < 1 or H % G != 0:
         raise ValueError("the heads of v must be a multiple of those of q and k")
     if state_index is not None:
-        _require("state_index", state_index, device, torch.int32, (B,))
-    for name, x, d in (("q", q, K), ("k", k, K), ("v", v, V)):
-        st = x.stride()
-        if (x.shape[1] > 1 and st[1] != d) or (d > 1 and st[2] != 1):
+        _require(v, ("state_index", state_index, torch.int32, (B,), True))
+    rows = [x.stride() for x in (q, k, v)]
+    for name, st, n, d in (("q", rows[0], G, K), ("k", rows[1], G, K), ("v", rows[2], H, V)):
+        if (n > 1 and st[1] != d) or (d > 1 and st[2] != 1):
             raise ValueError(f"{name} must be dense inside a row")
     if out is None:
-        out = torch.empty((B, H, V), dtype=v.dtype, device=device)
+        out = _empty(v)
     else:
-        _require("out", out, device, v.dtype, (B, H, V))
-    _call(lib().ss2d_linear_attention_step, device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-          state.data_ptr(), _ptr(state_index), out.data_ptr(), B, slots, G, H, K, V, q.stride(0), k.stride(0),
-          v.stride(0), scale, code)
+        _require(v, ("out", out, dtype, (B, H, V), True))
+    _call(lib().ss2d_linear_attention_step, v.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          state.data_ptr(), _ptr(state_index), out.data_ptr(), B, cache[0], G, H, K, V, rows[0][0], rows[1][0],
+          rows[2][0], scale, code)
     return out
 
 
@@ -224,13 +229,11 @@ def _norm_inputs(x, weight, others):
     code, device = _code(x), x.device
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be (..., dim)")
-    dim = x.shape[-1]
-    _require("x", x, device, x.dtype)
+    shape = x.shape
+    dim = shape[-1]
+    _require(x, ("x", x, x.dtype, None, True), *[(name, t, x.dtype, shape, True) for name, t in others if t is not None])
     if weight is not None:
-        _require("weight", weight, device, torch.float32, (dim,))
-    for name, t in others:
-        if t is not None:
-            _require(name, t, device, x.dtype, x.shape)
+        _require(x, ("weight", weight, torch.float32, (dim,), True))
     return code, device, x.numel() // dim, dim
 
 
@@ -246,9 +249,9 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out=None, residua
     code, device, rows, dim = _norm_inputs(x, weight, (("residual", residual), ("out", out),
                                                        ("residual_out", residual_out)))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out = torch.empty_like(x)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        residual_out = torch.empty_like(x)
     _call(lib().ss2d_rms_norm, device, x.data_ptr(), _ptr(residual), _ptr(weight), eps, _ptr(residual_out),
           out.data_ptr(), None, rows, dim, code)
     return out if residual is None else (out, residual_out)
@@ -260,10 +263,10 @@ def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, residual_out=
     if stream is not None:
         return _on_stream(stream, x.device, rms_norm_fp8, x, weight, residual, eps, residual_out)
     code, device, rows, dim = _norm_inputs(x, weight, (("residual", residual), ("residual_out", residual_out)))
-    y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=device)
+    y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     scales = torch.empty(x.shape[:-1] + ((dim + 127) // 128,), dtype=torch.float32, device=device)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        residual_out = torch.empty_like(x)
     _call(lib().ss2d_rms_norm, device, x.data_ptr(), _ptr(residual), _ptr(weight), eps, _ptr(residual_out),
           y.data_ptr(), scales.data_ptr(), rows, dim, code)
     return (y, scales) if residual is None else (y, scales, residual_out)
@@ -276,7 +279,7 @@ def rms_norm_backward(r, weight, dy, dresidual=None, eps: float = 1e-6, stream=N
     if stream is not None:
         return _on_stream(stream, r.device, rms_norm_backward, r, weight, dy, dresidual, eps)
     code, device, rows, dim = _norm_inputs(r, weight, (("dy", dy), ("dresidual", dresidual)))
-    dx = torch.empty(r.shape, dtype=r.dtype, device=device)
+    dx = torch.empty_like(r)
     L = lib()
     dweight = ws = at = None
     nbytes = 0
@@ -298,23 +301,21 @@ def matmul_fp8(a, a_scales, b, b_scales, out_dtype=torch.bfloat16, out=None, str
     """
     if stream is not None:
         return _on_stream(stream, a.device, matmul_fp8, a, a_scales, b, b_scales, out_dtype, out)
-    device = a.device
     if a.dim() < 1 or b.dim() != 2:
         raise ValueError("a must be (...,K) and b (N,K)")
     N, K = b.shape
-    lead = tuple(a.shape[:-1])
+    lead = a.shape[:-1]
     blocks = (K + 127) // 128
-    _require("a", a, device, torch.float8_e4m3fn, lead + (K,))
-    _require("b", b, device, torch.float8_e4m3fn)
-    _require("a_scales", a_scales, device, torch.float32, lead + (blocks,))
-    _require("b_scales", b_scales, device, torch.float32, ((N + 127) // 128, blocks))
+    _require(a, ("a", a, torch.float8_e4m3fn, lead + (K,), True), ("b", b, torch.float8_e4m3fn, None, True),
+             ("a_scales", a_scales, torch.float32, lead + (blocks,), True),
+             ("b_scales", b_scales, torch.float32, ((N + 127) // 128, blocks), True))
     if out is None:
-        out = torch.empty(lead + (N,), dtype=out_dtype, device=device)
+        out = torch.empty(lead + (N,), dtype=out_dtype, device=a.device)
     else:
-        _require("out", out, device, out.dtype, lead + (N,))
+        _require(a, ("out", out, out.dtype, lead + (N,), True))
     M = 1
     for n in lead:
         M *= n
-    _call(lib().ss2d_matmul_fp8, device, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
+    _call(lib().ss2d_matmul_fp8, a.device, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
           out.data_ptr(), M, N, K, _code(out))
     return out
