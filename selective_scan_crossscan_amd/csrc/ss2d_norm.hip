@@ -170,20 +170,31 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(
   }
 }
 
-// dweight[c] = sum over the workgroups' parts: 64 channels by 16 ranges of parts
-// per workgroup, the ranges' sums added in order.
-__global__ __launch_bounds__(1024) void norm_sum_partials(const float* __restrict__ partial, float* __restrict__ dw,
-                                                          int parts, int dim) {
-  __shared__ float sums[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), range = threadIdx.x >> 6;
+// dweight[c] = sum over the workgroups' parts: 32 channels by 32 ranges of parts
+// per workgroup, eight loads in flight per thread, the ranges' sums added in order.
+constexpr int kSumCols = 32, kSumRanges = 32;
+__global__ __launch_bounds__(kSumCols * kSumRanges) void norm_sum_partials(const float* __restrict__ partial,
+                                                                           float* __restrict__ dw, int parts, int dim) {
+  __shared__ float sums[kSumRanges][kSumCols + 1];
+  const int col = threadIdx.x % kSumCols, range = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + col;
   float s = 0.f;
   if (c < dim)
-    for (int p = range; p < parts; p += 16) s += partial[(int64_t)p * dim + c];
-  sums[range][threadIdx.x & 63] = s;
+    for (int p = range; p < parts; p += 8 * kSumRanges) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = p + i * kSumRanges;
+        v[i] = q < parts ? partial[(int64_t)q * dim + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+  sums[range][col] = s;
   __syncthreads();
   if (range == 0 && c < dim) {
+    s = 0.f;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += sums[i][threadIdx.x];
+    for (int i = 0; i < kSumRanges; ++i) s += sums[i][col];
     dw[c] = s;
   }
 }
@@ -236,7 +247,7 @@ hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
   else
     launch_norm_backward_t<S, 1024, 2>(a);
   if (a.dweight)
-    norm_sum_partials<<<dim3((unsigned)((a.dim + 63) / 64)), dim3(1024), 0, a.stream>>>(
+    norm_sum_partials<<<dim3((unsigned)((a.dim + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumRanges), 0, a.stream>>>(
         a.partial, a.dweight, (int)norm_backward_blocks(a.rows, a.dim), (int)a.dim);
   return hipGetLastError();
 }
