@@ -71,23 +71,27 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[j][i] *= rstd;
+      if (!FP8) v[j][i] *= rstd;
       if (weight) v[j][i] *= w[i];
       if (FP8) amax = fmaxf(amax, fabsf(v[j][i]));  // a NaN is passed over here and stays one below
     }
     if (!FP8) {
       store8(static_cast<S*>(yv) + at + c, dim - c, v[j]);
     } else {
-      // 16 consecutive threads hold one block of 128 channels
+      // 16 consecutive threads hold one block of 128 channels.  v is r weight still without rstd, which cancels in
+      // y / s = v 448 / max|v|: fewer roundings before the one to 8 bits, and one division per block
 #pragma unroll
       for (int m = 1; m < 16; m <<= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
-      const float s = fmaxf(amax / 448.0f, 1.17549435e-38f);
+      constexpr float kLeast = 1.17549435e-38f;  // 2^-126
+      const float t = amax * rstd / 448.0f;
+      const bool least = !(t > kLeast);  // nearly nothing, or NaN
+      const float s = least ? kLeast : t, k = least ? rstd : 448.0f / amax, k2 = least ? 1.0f / kLeast : 1.0f;
       const int blocks = (dim + kScaleBlock - 1) / kScaleBlock;
-      if ((t & 15) == 0 && c < dim) scales[row * blocks + c / kScaleBlock] = s;
+      if ((threadIdx.x & 15) == 0 && c < dim) scales[row * blocks + c / kScaleBlock] = s;
       float u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float z = v[j][i] / s;
+        const float z = v[j][i] * k * k2;
         u[i] = z > 448.f ? 448.f : z < -448.f ? -448.f : z;  // keeps NaN
       }
       uint32_t q[2];
