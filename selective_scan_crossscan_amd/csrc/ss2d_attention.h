@@ -104,9 +104,9 @@ struct StateParams {
   float scale;
   bool split;             // segments start from seg_state
 };
-// seg_state: the state before every segment but a sequence's first.
+// seg_state: the state before every segment of a sequence of several.
 hipError_t launch_segment_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
-// The same, and r's seg_state: the gradient of the state behind every segment but a sequence's last.
+// The same, and r's seg_state: the gradient of the state behind every segment of a sequence of several.
 hipError_t launch_segment_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, int dtype,
                                hipStream_t st);
 hipError_t launch_chunk_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
@@ -122,6 +122,7 @@ struct Segment {
   int s;
   int64_t start, len, begin, end;
   bool last;  // the sequence's last segment
+  __device__ __forceinline__ bool several() const { return begin > 0 || !last; }  // the sequence has other segments
 };
 
 __device__ __forceinline__ int64_t cu_at(const SequenceMap& m, int s) {

@@ -37,7 +37,7 @@ struct AttentionParams {
   int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3];
   int groups, heads, K, V, vtiles;
   float scale;
-  bool split;  // segments behind a sequence's first start from seg_state
+  bool split;  // segments of a sequence of several start from seg_state
 };
 
 template <typename E, int C, int KP, int VT, int NV, bool TINY>
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
   // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
   f32x4 h[NK][NV];
   const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
-  const float* from = p.split && seg.begin > 0 ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
+  const float* from = p.split && seg.several() ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
 #pragma unroll
   for (int t = 0; t < NV; ++t) {
     const int v = vw + t * 16 + l;

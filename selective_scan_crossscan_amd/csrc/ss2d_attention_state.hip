@@ -55,7 +55,7 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
   f32x4 h[NK];
   const int64_t sh = (slot * p.heads + head) * K * p.V;
   const float* from = PASS != kChunkStates              ? nullptr
-                      : p.split && seg.begin > 0        ? p.seg_state + sh
+                      : p.split && seg.several()        ? p.seg_state + sh
                       : p.state_in                      ? p.state_in + ((int64_t)seg.s * p.heads + head) * K * p.V
                                                         : nullptr;
   if (from)
@@ -169,8 +169,10 @@ __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_pair_kernel(State
 }
 
 // seg_state: from what each segment adds to the state before it, or, in reverse, to
-// the gradient of the state behind it.  One thread per state entry walks its
-// sequence's segments, eight sums read at a time.
+// the gradient of the state behind it, for every segment of a sequence of several
+// (the first one's is a copy of the initial state: the last segment's workgroup may
+// write the final state over that one before the first has begun).  One thread per
+// state entry walks its sequence's segments, eight sums read at a time.
 __device__ __forceinline__ void carry_walk(const StateParams& p, const float* from, bool reverse, int64_t block) {
   const int64_t kv = (int64_t)p.K * p.V;
   const int64_t blocks = (kv + 255) / 256;
@@ -197,6 +199,7 @@ __device__ __forceinline__ void carry_walk(const StateParams& p, const float* fr
   float h = from ? from[((int64_t)s * p.heads + head) * kv + e] : 0.f;
   constexpr int N = 8;
   float first = *u;  // the sum of segment i, kept: its place is overwritten
+  *u = h;
   for (int64_t i = 0; i + 1 < n; i += N) {
     float add[N], decay[N];
     add[0] = first;

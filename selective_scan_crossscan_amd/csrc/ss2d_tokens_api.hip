@@ -132,10 +132,11 @@ ss2d::AttentionArgs attention_args(const void* q, const void* k, const void* v, 
   return a;
 }
 
-// Whether a plan's launches fit a grid.
+// Whether a plan's launches fit a grid: two passes' segments in tiles of 64 value
+// columns, two passes' state entries.
 bool grid_ok(const ss2d::AttentionPlan& pl, const ss2d_attention_sizes& z) {
-  return pl.slots * z.heads * pl.vtiles <= INT32_MAX &&
-         z.sequences * z.heads * ((z.key_dim * z.value_dim + 255) / 256) <= INT32_MAX;
+  return pl.slots * z.heads * pl.vtiles * (pl.vt / 64) <= INT32_MAX / 2 &&
+         z.sequences * z.heads * ((z.key_dim * z.value_dim + 255) / 256) <= INT32_MAX / 2;
 }
 
 }  // namespace
