@@ -146,14 +146,16 @@ __device__ __forceinline__ bool find_segment(const SequenceMap& m, int64_t slot,
     g.start = (int64_t)g.s * m.len;
     g.len = m.len;
   } else {
-    int lo = 0, hi = m.sequences - 1;  // the last sequence whose first slot is at most `slot`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu_at(m, mid) / m.seg_len + mid <= slot)
-        lo = mid;
-      else
-        hi = mid - 1;
+    // the last sequence whose first slot is at most `slot`: the lanes look at 64 sequences at a time (first slots
+    // ascend, so counting finds it), one load's latency where a search would take one per halving
+    const uint32_t seg_len = (uint32_t)m.seg_len;
+    int lo = -1;
+    for (int s0 = 0; s0 < m.sequences; s0 += 64) {
+      const int s = s0 + (int)(threadIdx.x & 63);
+      const bool before = s < m.sequences && (int64_t)((uint32_t)cu_at(m, min(s, m.sequences - 1)) / seg_len) + s <= slot;
+      lo += __popcll(__ballot(before));
     }
+    lo = max(lo, 0);  // offsets that do not ascend may leave none
     g.s = lo;
     g.start = cu_at(m, lo);
     const int64_t end = cu_at(m, lo + 1);

@@ -63,31 +63,11 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
   const int vw = wave * 16 * NV;   // this wave's first column in the tile
   const bool active = vw < nv;     // it has columns at all
-  const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
-  const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + first * p.q_stride[1] + group * p.q_stride[2];
-  const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + first * p.k_stride[1] + group * p.k_stride[2];
-  const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + first * p.v_stride[1] + head * p.v_stride[2] + v0;
-  const float* gb = p.g + sq * p.g_stride[0] + first * p.g_stride[1] + head * p.g_stride[2];
-
-  // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
-  f32x4 h[NK][NV];
-  const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
-  const float* from = p.split && seg.several() ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
-#pragma unroll
-  for (int t = 0; t < NV; ++t) {
-    const int v = vw + t * 16 + l;
-    if (from) {
-      const float* c = from + v0 + min(v, nv - 1);
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h[kt][t][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
-    }
-#pragma unroll
-    for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) h[kt][t][r] = from && kt * 16 + 4 * g + r < K && v < nv ? h[kt][t][r] : 0.f;
-  }
+  const int64_t token0 = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
+  const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + token0 * p.q_stride[1] + group * p.q_stride[2];
+  const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + token0 * p.k_stride[1] + group * p.k_stride[2];
+  const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + token0 * p.v_stride[1] + head * p.v_stride[2] + v0;
+  const float* gb = p.g + sq * p.g_stride[0] + token0 * p.g_stride[1] + head * p.g_stride[2];
 
   struct Chunk {
     TileLoad<E, C, KP, 16, THREADS, TINY> q;
@@ -109,11 +89,29 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
     x.v.store(vs, n, nv);
     if (wave == 0) scan_decays<C>(x.g, dec);
   };
-  if (seg.begin < seg.end) {
-    Chunk x;
-    fetch(x, seg.begin);
-    land(x, seg.begin);
+  Chunk first;  // on its way while the state is read
+  if (seg.begin < seg.end) fetch(first, seg.begin);
+
+  // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
+  f32x4 h[NK][NV];
+  const int64_t sh = ((int64_t)slot * p.heads + head) * K * p.V, qh = ((int64_t)seg.s * p.heads + head) * K * p.V;
+  const float* from = p.split && seg.several() ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
+#pragma unroll
+  for (int t = 0; t < NV; ++t) {
+    const int v = vw + t * 16 + l;
+    if (from) {
+      const float* c = from + v0 + min(v, nv - 1);
+#pragma unroll
+      for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[kt][t][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
+    }
+#pragma unroll
+    for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) h[kt][t][r] = from && kt * 16 + 4 * g + r < K && v < nv ? h[kt][t][r] : 0.f;
   }
+  if (seg.begin < seg.end) land(first, seg.begin);
   for (int64_t at = seg.begin; at < seg.end; at += C) {
     const int n = (int)min((int64_t)C, seg.end - at);
     __syncthreads();  // the chunk has landed

@@ -46,28 +46,10 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), vw = wave * 16;
   const bool active = vw < nv;
-  const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
-  const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + first * p.k_stride[1] + group * p.k_stride[2];
-  const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + first * p.v_stride[1] + head * p.v_stride[2] + v0;
-  const float* gb = p.g + sq * p.g_stride[0] + first * p.g_stride[1] + head * p.g_stride[2];
-
-  // rows v = vw + 4 g + r, column k = 16 kt + l
-  f32x4 h[NK];
-  const int64_t sh = (slot * p.heads + head) * K * p.V;
-  const float* from = PASS != kChunkStates              ? nullptr
-                      : p.split && seg.several()        ? p.seg_state + sh
-                      : p.state_in                      ? p.state_in + ((int64_t)seg.s * p.heads + head) * K * p.V
-                                                        : nullptr;
-  if (from)
-#pragma unroll
-    for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        h[kt][r] = from[(int64_t)min(kt * 16 + l, K - 1) * p.V + v0 + min(vw + 4 * g + r, nv - 1)];
-#pragma unroll
-  for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) h[kt][r] = from && kt * 16 + l < K && vw + 4 * g + r < nv ? h[kt][r] : 0.f;
+  const int64_t token0 = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
+  const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + token0 * p.k_stride[1] + group * p.k_stride[2];
+  const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + token0 * p.v_stride[1] + head * p.v_stride[2] + v0;
+  const float* gb = p.g + sq * p.g_stride[0] + token0 * p.g_stride[1] + head * p.g_stride[2];
 
   struct Chunk {
     TileLoad<E, C, KP, 32, 256, TINY> k;
@@ -89,11 +71,27 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
   const int64_t chunks = (seg.end - seg.begin + C - 1) / C;
   auto start_of = [&](int64_t c) { return seg.begin + (REVERSE ? chunks - 1 - c : c) * C; };
   float whole = 0.f, frac = 0.f;  // the segment's log2 decay so far
-  if (chunks > 0) {
-    Chunk x;
-    fetch(x, start_of(0));
-    land(x, start_of(0));
-  }
+  Chunk first;  // on its way while the state is read
+  if (chunks > 0) fetch(first, start_of(0));
+
+  // rows v = vw + 4 g + r, column k = 16 kt + l
+  f32x4 h[NK];
+  const int64_t sh = (slot * p.heads + head) * K * p.V;
+  const float* from = PASS != kChunkStates              ? nullptr
+                      : p.split && seg.several()        ? p.seg_state + sh
+                      : p.state_in                      ? p.state_in + ((int64_t)seg.s * p.heads + head) * K * p.V
+                                                        : nullptr;
+  if (from)
+#pragma unroll
+    for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        h[kt][r] = from[(int64_t)min(kt * 16 + l, K - 1) * p.V + v0 + min(vw + 4 * g + r, nv - 1)];
+#pragma unroll
+  for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[kt][r] = from && kt * 16 + l < K && vw + 4 * g + r < nv ? h[kt][r] : 0.f;
+  if (chunks > 0) land(first, start_of(0));
   for (int64_t c = 0; c < chunks; ++c) {
     if (PASS == kChunkStates) {  // before the chunk, as it lies in registers: 1 KiB per tile and wave
       const int64_t chunk = chunk_number<C>(p.map, seg, start_of(c));
