@@ -131,16 +131,20 @@ constexpr int kScaleStep = 16;  // blocks of a's scales in LDS at a time
 // pieces, piece q of row r in place q ^ (r / 2 % 8): sixteen rows' reads of one piece
 // then fall into different banks (two rows to the 64 banks, eight places each).  (Fragments straight from memory would spare half of
 // LDS's traffic, but a wave's 16 rows by four pieces 32 bytes apart are 64 separate
-// addresses: 232 us where this takes 136, 5001 x 4096 x 4096.)  a's scales, one
-// per row and block, come through LDS as well, sixteen blocks at a time: read from
-// memory where they are used, sixteen rows' lines for four bytes each, they cost a
-// quarter of the time.
+// addresses: 232 us where this takes 108, 5001 x 4096 x 4096.)  The scales,
+// one product per row and block, come through LDS as well, sixteen blocks at a time:
+// read from memory where they are used, sixteen rows' lines for four bytes each, they
+// cost a quarter of the time, and even b's alone made every step wait for the pieces
+// on their way (loads are waited for in order).
 // DMA: rows are 16-byte aligned and whole pieces long; pieces go from memory to LDS
 // without registers, and those outside the operand read as 0 by the buffer's bounds.
 // Otherwise they go through registers, byte by byte at a row's end.
 template <typename O, bool DMA>
 __global__ __launch_bounds__(256, 2) void matmul_fp8_tiles(MatmulParams p) {
-  __shared__ __attribute__((aligned(16))) uint8_t sm[2][kTile * kScaleBlock], sn[2][kTile * kScaleBlock];
+  // Two buffers each, as variables of their own and with the steps written out for either: only so does the compiler see
+  // that a step's reads are not of the pieces on their way, and not wait for those (136 us where this takes 108)
+  __shared__ __attribute__((aligned(16))) uint8_t sm0[kTile * kScaleBlock], sm1[kTile * kScaleBlock];
+  __shared__ __attribute__((aligned(16))) uint8_t sn0[kTile * kScaleBlock], sn1[kTile * kScaleBlock];
   __shared__ float scale[kTile * (kScaleStep + 1)];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, g = lane >> 4,
             l = lane & 15;
@@ -161,72 +165,69 @@ __global__ __launch_bounds__(256, 2) void matmul_fp8_tiles(MatmulParams p) {
       __builtin_amdgcn_make_buffer_rsrc((void*)a, 0, (uint32_t)rows_m * (uint32_t)p.K, 0x00020000);
   const __amdgpu_buffer_rsrc_t rb =
       __builtin_amdgcn_make_buffer_rsrc((void*)b, 0, (uint32_t)rows_n * (uint32_t)p.K, 0x00020000);
-  auto fetch = [&](int kb, int buf) {
+  auto fetch = [&](int kb, uint8_t* sm, uint8_t* sn) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int place = (wave * 4 + i) * 64 + lane, row = place >> 3, c = kb * kScaleBlock + ((place & 7) ^ ((row >> 1) & 7)) * 16;
       if (DMA) {
         const uint32_t at = c < p.K ? (uint32_t)row * (uint32_t)p.K + c : 1u << 30;  // past any operand's rows: 128 x 2^20 bytes
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(sm[buf] + (wave * 4 + i) * 1024), 16, at, 0, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(sn[buf] + (wave * 4 + i) * 1024), 16, at, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(sm + (wave * 4 + i) * 1024), 16, at, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(sn + (wave * 4 + i) * 1024), 16, at, 0, 0, 0);
       } else {
         stage_m[i] = load_bytes16(a + (int64_t)row * p.K + c, row < rows_m ? p.K - c : 0);
         stage_n[i] = load_bytes16(b + (int64_t)row * p.K + c, row < rows_n ? p.K - c : 0);
       }
     }
   };
-  auto land = [&](int buf) {
+  auto land = [&](uint8_t* sm, uint8_t* sn) __attribute__((always_inline)) {
     if (!DMA)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int place = (wave * 4 + i) * 64 + lane;
-        *reinterpret_cast<i32x4*>(sm[buf] + place * 16) = stage_m[i];
-        *reinterpret_cast<i32x4*>(sn[buf] + place * 16) = stage_n[i];
+        *reinterpret_cast<i32x4*>(sm + place * 16) = stage_m[i];
+        *reinterpret_cast<i32x4*>(sn + place * 16) = stage_n[i];
       }
   };
-  // scales of blocks kb .. kb + 15: a row's sixteen by sixteen lanes
+  const float* sbp = p.sb + (n0 / kScaleBlock) * p.blocks;
+  // both scales' products for blocks kb .. kb + 15: a row's sixteen by sixteen lanes
   auto fetch_scales = [&](int kb) {
 #pragma unroll
     for (int i = 0; i < kTile * kScaleStep / 256; ++i) {
       const int idx = threadIdx.x + i * 256, row = idx / kScaleStep, c = idx % kScaleStep;
-      scale[row * (kScaleStep + 1) + c] = p.sa[(m0 + min(row, rows_m - 1)) * p.blocks + min(kb + c, p.blocks - 1)];
+      const int block = min(kb + c, p.blocks - 1);
+      scale[row * (kScaleStep + 1) + c] = p.sa[(m0 + min(row, rows_m - 1)) * p.blocks + block] * sbp[block];
     }
   };
-  auto fragment = [&](const uint8_t* s, int row) {
+  auto fragment = [&](const uint8_t* s, int row) __attribute__((always_inline)) {
     const uint8_t* r = s + row * kScaleBlock;
     const i32x4 x = *reinterpret_cast<const i32x4*>(r + ((2 * g) ^ ((row >> 1) & 7)) * 16);
     const i32x4 y = *reinterpret_cast<const i32x4*>(r + ((2 * g + 1) ^ ((row >> 1) & 7)) * 16);
     return Operand<O>(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  const float* sbp = p.sb + (n0 / kScaleBlock) * p.blocks;
-
   f32x4 acc[4][4];
 #pragma unroll
   for (int x = 0; x < 4; ++x)
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[x][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  fetch(0, 0);
-  land(0);
-  for (int kb = 0; kb < p.blocks; ++kb) {
-    const int buf = kb & 1;
+  // block kb from (sm, sn), the next one on its way into (tm, tn)
+  auto step = [&](int kb, const uint8_t* sm, const uint8_t* sn, uint8_t* tm, uint8_t* tn) __attribute__((always_inline)) {
     if (kb % kScaleStep == 0) {
       if (kb > 0) __syncthreads();  // the scales before have been read
       fetch_scales(kb);
     }
     if (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's pieces have landed
     __syncthreads();  // the block is whole, the other buffer has been read
-    if (kb + 1 < p.blocks) fetch(kb + 1, buf ^ 1);
-    const float sb = sbp[kb];
+    if (kb + 1 < p.blocks) fetch(kb + 1, tm, tn);
     float s[4];
     Operand<O> fm[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      s[t] = scale[(wm + t * 16 + l) * (kScaleStep + 1) + kb % kScaleStep] * sb;
-      fm[t] = fragment(sm[buf], wm + t * 16 + l);
+      s[t] = scale[(wm + t * 16 + l) * (kScaleStep + 1) + kb % kScaleStep];
+      fm[t] = fragment(sm, wm + t * 16 + l);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const Operand<O> fn = fragment(sn[buf], wn + x * 16 + l);
+      const Operand<O> fn = fragment(sn, wn + x * 16 + l);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f32x4 d = mfma_block(fn, fm[t]);
@@ -234,7 +235,13 @@ __global__ __launch_bounds__(256, 2) void matmul_fp8_tiles(MatmulParams p) {
         for (int r = 0; r < 4; ++r) acc[x][t][r] = fmaf(d[r], s[t], acc[x][t][r]);
       }
     }
-    if (kb + 1 < p.blocks) land(buf ^ 1);
+    if (kb + 1 < p.blocks) land(tm, tn);
+  };
+  fetch(0, sm0, sn0);
+  land(sm0, sn0);
+  for (int kb = 0; kb < p.blocks; kb += 2) {
+    step(kb, sm0, sn0, sm1, sn1);
+    if (kb + 1 < p.blocks) step(kb + 1, sm1, sn1, sm0, sn0);
   }
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
