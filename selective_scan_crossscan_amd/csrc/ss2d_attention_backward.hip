@@ -179,11 +179,6 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
           for (int a = 0; a < NV; ++a)
             h[a][b] = *reinterpret_cast<const f32x4*>(hb + ((a * NK + wave + b * NW) * 64 + lane) * 4);
     }
-    // the loads of the chunk before run beside this one's products; always: a load under a condition would be waited
-    // for where the paths meet
-    Chunk next;
-    const int64_t ahead = c > 0 ? at - C : at;
-    fetch(next, ahead);
     __builtin_amdgcn_sched_barrier(0);  // here and below: phases in order, or their registers add up and spill
 
     // ---- S and D, transposed (rows j, columns i): 16 tokens i per JS waves, which take every JS-th tile of j
@@ -306,6 +301,12 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
     xsum = wave_sum(xsum);
     if (lane == 0) xs[wave] = xsum * all;
 
+    __builtin_amdgcn_sched_barrier(0);
+    // the loads of the chunk before run beside the rest of this one's products (from its start on they would cost the
+    // keys' phase its registers); always: a load under a condition would be waited for where the paths meet
+    Chunk next;
+    const int64_t ahead = c > 0 ? at - C : at;
+    fetch(next, ahead);
     __builtin_amdgcn_sched_barrier(0);
 
     // ---- own values: dv
