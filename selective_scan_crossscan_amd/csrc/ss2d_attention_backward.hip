@@ -60,9 +60,11 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
   constexpr int JS = NW / NI < NI ? NW / NI : NI;       // waves that share 16 tokens' scores
   constexpr int PF = kFullParts<E>;
   static_assert(NV % NW == 0 && NW >= NI, "value tiles and token tiles are dealt evenly");
-  __shared__ Tile<E, C, KP> qs, ks;
+  __shared__ Tile<E, C, KP, 32> qs;
+  __shared__ Tile<E, C, KP> ks;
   __shared__ Tile<E, C, VT> vs, ds;
-  __shared__ Tile<E, C, C> sm, dm;  // S M and D M, rows i
+  __shared__ Tile<E, C, C, 32> sm;  // S M, rows i
+  __shared__ Tile<E, C, C> dm;      // D M
   __shared__ Decays<C> dec;
   __shared__ float wrow[NW][C], wcol[NW][C], fs[NW][C], es[NW][C], xs[NW];
 
@@ -103,7 +105,8 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
       for (int r = 0; r < 4; ++r) dvk[a][b][r] = entry((wave + b * NW) * 16 + l, a * 16 + 4 * g + r);
 
   struct Chunk {
-    TileLoad<E, C, KP, 16, THREADS, TINY> q, k;
+    TileLoad<E, C, KP, 32, THREADS, TINY> q;
+    TileLoad<E, C, KP, 16, THREADS, TINY> k;
     TileLoad<E, C, VT, 16, THREADS, TINY> v, d;
     float g;
   };
