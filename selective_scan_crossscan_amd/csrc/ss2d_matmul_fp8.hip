@@ -16,11 +16,12 @@
 // for its stores.  A fragment is 32 consecutive bytes of a row per lane, 16 rows
 // by four quarters of a block, in both operands alike.
 //
-// Two kernels.  Products with enough rows for tiles of 128x128 stage both
-// operands through LDS, double buffered.  Fewer rows are bound by reading b
-// once: there a workgroup's waves split the inner dimension over one strip of 16
-// n, each streaming its part of b from global memory straight into fragments,
-// and add their sums through LDS in a fixed order.
+// Two kernels.  Products with enough outputs for tiles of 128x128 stage both
+// operands through LDS, double buffered (5001 x 4096 x 4096: 105 us, 1591
+// TFLOP/s).  Fewer are bound by reading b once: there a workgroup's waves split
+// the inner dimension over one strip of 16 n, each streaming its part of b from
+// global memory straight into fragments, and add their sums through LDS in a
+// fixed order (3 x 6144 x 4096: 8.6 us, 2.9 TB/s).
 #include "ss2d_token_ops.h"
 
 namespace ss2d {
@@ -327,14 +328,20 @@ hipError_t launch_o(const MatmulArgs& x) {
                  x.m, x.n, (int)x.k, (int)((x.k + kScaleBlock - 1) / kScaleBlock), 0, 0};
   p.mtiles = (int)((x.m + kTile - 1) / kTile);
   p.ntiles = (int)((x.n + kTile - 1) / kTile);
-  // tiles of 128 x 128 where they give half the CUs a workgroup
-  if (x.m > 64 && (int64_t)p.mtiles * p.ntiles >= 128) {
+  // Strips cost a step for every 16 x 16 outputs that a CU gets, tiles a walk over k at least, however few they are.
+  // K = 4096, us of strips against tiles: 64 x 4096 15.9 (25.6), 80 x 4096 20.6 (25.7), 128 x 4096 28.5 (26.7),
+  // 256 x 1024 15.6 (26.4), 512 x 1024 28.2 (26.3), 16 x 16384 22.9 (31.4), 48 x 16384 43.9 (32.4); fp32 outputs,
+  // whose tiles take longer: 128 x 4096 29.1 (38.6), 256 x 4096 54.4 (38.8), 48 x 16384 46.6 (38.7).
+  if (x.m * x.n >= (sizeof(O) == 2 ? 1 << 19 : 3 << 18)) {
     const dim3 grid((unsigned)((int64_t)p.mtiles * p.ntiles)), block(256);
+    // 16-byte copies into LDS; odd rows through registers (4096 cubed: 84 us against 118)
     if (x.k % 16 == 0 && (((uintptr_t)x.a | (uintptr_t)x.b) & 15) == 0)
       matmul_fp8_tiles<O, true><<<grid, block, 0, x.stream>>>(p);
     else
       matmul_fp8_tiles<O, false><<<grid, block, 0, x.stream>>>(p);
   } else if (x.m <= 16) {
+    // Strips of 16, 32 or 64 rows at once; 4096 x 4096, us of the three: 16 rows 7.5, 9.2, 9.9; 32 rows 12.2, 10.2,
+    // 11.7; 64 rows 20.9, 17.2, 15.6.
     launch_rows<O, 1>(p, x.stream);
   } else if (x.m <= 32) {
     launch_rows<O, 2>(p, x.stream);

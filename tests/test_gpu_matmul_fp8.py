@@ -87,6 +87,16 @@ def test_product_matches_oracle(shape, dtype):
     _check(out, case, dtype, f"{shape} {dtype}")
 
 
+# tiles with a few rows of very many columns, strips with many rows of a few
+LONG = [(5, 170000, 130), (20, 40000, 256), (6000, 20, 128), (300, 1500, 200), (600, 1500, 272)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_long_products_match_oracle(shape, dtype):
+    test_product_matches_oracle(shape, dtype)
+
+
 @pytest.mark.parametrize("shape", [(5, 70, 160), (1100, 1900, 160)], ids=lambda s: "x".join(map(str, s)))
 def test_unaligned_operands(shape):
     """Operands one byte into their storage, the output next to guard values that stay."""
