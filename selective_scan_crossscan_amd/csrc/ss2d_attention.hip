@@ -260,29 +260,38 @@ hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream
   return hipGetLastError();
 }
 
+int64_t chunk_of(int dtype) { return dtype == 1 ? 64 : 32; }
+bool tiny_rows(int64_t key_dim, int64_t value_dim, int dtype) {
+  const int64_t least = dtype == 1 ? 8 : 4;  // values in 16 bytes
+  return key_dim < least || value_dim < least;
+}
+
 // The plan for tiles of vt value columns.  Sequences are cut so that there are
 // about `want` workgroups and no more: a few over a whole number per CU would
 // cost as long as a full round.  Equal lengths are cut evenly; packed ones every
-// tokens / (want per head and tile, less one ragged end per sequence) tokens.
-// Segments have four chunks at least.
+// tokens / (want per head and tile, less one ragged end per sequence) tokens,
+// and where those ends would take a quarter of them, for twice as many (gradients
+// of 38144 tokens in 6 sequences, 16 heads of 128: 1203 us against 1428; 8192 in
+// one, whose ends take less, 333 against 282).  Segments have four chunks at least,
+// and there are `least` of them or the sequences stay whole.
 AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
-                        bool packed, int dtype, int vt, int64_t want) {
+                        bool packed, int dtype, int vt, int64_t want, int least) {
   AttentionPlan pl;
-  const int64_t least = dtype == 1 ? 8 : 4;  // values in 16 bytes
-  pl.tiny = key_dim < least || value_dim < least;
+  pl.tiny = tiny_rows(key_dim, value_dim, dtype);
   if (pl.tiny) vt = 64;
   pl.kp = pl.tiny ? 256 : key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
   pl.vt = vt;
   pl.vtiles = (int)((value_dim + vt - 1) / vt);
-  const int64_t chunk = pl.chunk = dtype == 1 ? 64 : 32;
+  const int64_t chunk = pl.chunk = chunk_of(dtype);
   const int64_t longest = packed ? tokens : tokens / sequences;
-  const int64_t each = want / (heads * pl.vtiles);  // segments of all sequences together
+  int64_t each = want / (heads * pl.vtiles);  // segments of all sequences together
+  for (; packed && 4 * sequences >= each && want < 1024; want *= 2) each = 2 * want / (heads * pl.vtiles);
   int64_t parts = packed ? (each - sequences > each / 2 ? each - sequences : each / 2) : each / sequences;
   if (parts < 1) parts = 1;
   int64_t seg = (longest + parts - 1) / parts;
   if (seg < 4 * chunk) seg = 4 * chunk;
   seg = (seg + chunk - 1) / chunk * chunk;
-  pl.split = longest > seg;
+  pl.split = longest > (least - 1) * seg;
   if (!pl.split) seg = (longest + chunk - 1) / chunk * chunk;
   pl.seg_len = seg;
   pl.nseg = (int)((longest + seg - 1) / seg);
@@ -295,14 +304,23 @@ AttentionPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_
 
 AttentionPlan plan_attention(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
                              bool packed, int dtype) {
-  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, value_dim <= 64 ? 64 : 128, 512);
+  // Tiles of 64 value columns for the wide heads of few tokens, which leave CUs idle; they read the keys twice.  16
+  // heads of 128, us of tiles of 64 against 128: 256 tokens 21 (28), 2048 tokens 45 (54), 2 x 4096 92 (94), 38144
+  // tokens 460 (314).  Two workgroups per CU: 38144 tokens for 256, 512 and 1024 workgroups 502, 327 and 336 us.
+  // Three segments at least: 16 x 4096 tokens in two each 464 us, whole 371; 9 x 4096 in three 290, whole 364.
+  const bool narrow = tokens / (4 * chunk_of(dtype)) * heads * ((value_dim + 63) / 64) <= 512;
+  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, value_dim <= 64 || narrow ? 64 : 128,
+                   512, 3);
 }
 
 AttentionPlan plan_attention_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim,
                                       int64_t value_dim, bool packed, int dtype) {
-  // one tile of value columns where they fit: a second one would make dq and dk sums of two parts in memory
-  const int vt = value_dim <= 64 ? 64 : 128;
-  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, vt, vt == 64 ? 512 : 256);
+  // One tile of value columns where they fit: a second one would make dq and dk sums of two parts in memory.  A
+  // workgroup fills a CU's LDS unless the keys are narrow: 2 x 4096 tokens, 16 heads of 128, for 256 and 512
+  // workgroups 270 and 309 us, 8192 tokens of 16 x 64 x 64 131 and 152, of 16 x 32 x 64 100 and 85.  Two segments pay
+  // here, where the states are formed in any case: 8 x 8192 tokens 1669 us, whole 2316.
+  return make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, value_dim <= 64 ? 64 : 128,
+                   key_dim <= 32 ? 512 : 256, 2);
 }
 
 SequenceMap sequence_map(const AttentionArgs& a, const AttentionPlan& pl) {

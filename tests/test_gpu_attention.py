@@ -104,6 +104,21 @@ def test_prompts_match_oracle(case, dtype):
     check("state", _host(last), ref_s, ts)
 
 
+# heads enough for tiles of 128 value columns: in several segments, of packed sequences too, and in one each
+WIDE = [
+    ([2560], 1, 64, 16, 128),
+    ([2000, 0, 700], 2, 64, 16, 100),
+    ([512, 512], 1, 160, 8, 128),
+    ([150, 600], 1, 80, 200, 90),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_wide_tiles_match_oracle(case, dtype):
+    test_prompts_match_oracle(case, dtype)
+
+
 @pytest.mark.parametrize("decay", ["none", "strong", "far"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_decays(decay, dtype):
