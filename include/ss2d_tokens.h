@@ -35,9 +35,9 @@ extern "C" {
 /*
  * Sizes and strides of linear attention.  Strides are in elements, for each of
  * sequence, token and head, at least 0 (0 repeats one value along that axis) and
- * for tokens at most 2^24;
- * the innermost axis (key_dim or value_dim) is dense.  With packed sequences the
- * sequence stride is unused.  do_stride is used by the backward only.
+ * for tokens below 2^24; the innermost axis (key_dim or value_dim) is dense.  With
+ * packed sequences the sequence stride is unused.  do_stride is used by the backward
+ * only.
  */
 typedef struct {
   int64_t sequences;  /* >= 1                                                        */
@@ -70,10 +70,9 @@ typedef struct {
  *   state_out  [sequences, heads, key_dim, value_dim] fp32, out, or NULL; may be
  *              state_in itself
  * Outputs must not overlap inputs otherwise (SS2D_ERR_ALIAS).  States, decays and
- * sums are fp32 (decays summed in fp64).  For bf16 the masked scores
- * and the state are rounded to bf16 for their products into o, whose own rounding is
- * as large; what the state itself is made of keeps all its bits.  NaN and Inf
- * propagate: from a token to its sequence's outputs from up to 63 tokens before it on
+ * sums are fp32 (decays summed in fp64).  For bf16 the masked scores and the state
+ * are rounded to bf16 for their products into o, whose own rounding is as large; what
+ * the state itself is made of keeps all its bits.  NaN and Inf propagate: from a token to its sequence's outputs from up to 63 tokens before it on
  * (tokens are taken in chunks as matrix products).  Results do not depend on the
  * workspace, other sequences or streams: no atomics, sums in a fixed order.
  */
@@ -177,9 +176,10 @@ int64_t ss2d_rms_norm_backward_workspace(int64_t rows, int64_t dim, int dtype);
  * All dense; out must not overlap an input.  Sums are fp32 on the matrix cores, in a
  * fixed order.  For a bf16 output the products run in 8 bits, where the instruction
  * drops, in each group of eight inner indices, what lies below 2^-13 of the group's
- * largest product; for an fp32 output they run in bf16 (exact values), all bits kept.  m, n >= 1 and at most 2^30, k 1..2^20 (SS2D_ERR_SHAPE
- * otherwise).  One kernel, no workspace; any k and any addresses, fastest with k a
- * multiple of 16 and a and b aligned to 16 bytes.
+ * largest product; for an fp32 output they run in bf16 (exact values), all bits kept.
+ * m, n >= 1 and at most 2^30, k 1..2^20 (SS2D_ERR_SHAPE otherwise).  One kernel, no
+ * workspace; any k and any addresses, fastest with k a multiple of 16 and a and b
+ * aligned to 16 bytes.
  */
 int ss2d_matmul_fp8(const void* a, const float* a_scales, const void* b, const float* b_scales, void* out, int64_t m,
                     int64_t n, int64_t k, int dtype, void* stream);

@@ -25,6 +25,10 @@
 // parts through LDS at every chunk.  S, D and W are split over the waves, S M
 // and D M go through LDS.
 //
+// 2 x 4096 tokens, 16 heads of 128 in bf16: 174 us of 284 in all (123 TFLOP/s).
+// One workgroup of eight waves per CU (97 KiB of LDS, 256 registers), bound by the
+// latency of a chunk's phases, of which the registers leave no more to overlap.
+//
 // Where several heads share keys and queries or the values take several tiles,
 // dq, dk (and dg) are written as fp32 parts and added in order by sum_parts.
 #include "ss2d_attention.h"

@@ -7,11 +7,16 @@
 //
 // One workgroup of four waves owns 64 value columns of a head and one segment; a
 // wave owns 16 of them.  (128 columns would read the keys half as often, but took
-// as long: more and smaller workgroups per CU hide more of the latency.)  The state is kept transposed (result tiles with
-// rows v and columns k): a lane then holds four consecutive values of one key
-// row for 16-byte accesses, and a pair of tiles is, as it lies in registers, an
-// operand whose inner index is v.  The decayed v (do) goes into the product in
-// parts that keep all of its bits.
+// as long: more and smaller workgroups per CU hide more of the latency.)  The state
+// is kept transposed (result tiles with rows v and columns k): a lane then holds four
+// consecutive values of one key row for 16-byte accesses, and a pair of tiles is, as
+// it lies in registers, an operand whose inner index is v.  The decayed v (do) goes
+// into the product in parts that keep all of its bits.
+//
+// 38144 packed tokens, 16 heads of 128 in bf16: segment states 111 us, bound as the
+// walk that follows, their carry 18 us for 30 segments' 31 MB read and written in
+// order.  2 x 4096 tokens: states before all chunks 52 us (268 MB written, 5.1 TB/s),
+// both ways' segments 44 us, their carries 20 us.
 #include <type_traits>
 
 #include "ss2d_attention.h"

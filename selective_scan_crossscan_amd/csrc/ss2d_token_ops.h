@@ -10,7 +10,7 @@ namespace ss2d {
 
 constexpr int kMaxKeyDim = 256;
 constexpr int kMaxValueDim = 1024;
-constexpr int64_t kMaxTokenStride = 1 << 24;  // 64 tokens' offsets fit 32 bits
+constexpr int64_t kMaxTokenStride = (1 << 24) - 1;  // a factor of 24 bits; 64 tokens' offsets fit 32
 constexpr int kMaxNormDim = 16384;
 constexpr int kScaleBlock = 128;  // channels per scale of the 8-bit values
 

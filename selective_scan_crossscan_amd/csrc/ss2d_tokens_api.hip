@@ -138,6 +138,10 @@ bool grid_ok(const ss2d::AttentionPlan& pl, const ss2d_attention_sizes& z) {
   return pl.slots * z.heads * pl.vtiles * (pl.vt / 64) <= INT32_MAX / 2 &&
          z.sequences * z.heads * ((z.key_dim * z.value_dim + 255) / 256) <= INT32_MAX / 2;
 }
+// The same with the sums of dq's, dk's and the decay's parts.
+bool backward_grid_ok(const ss2d::AttentionPlan& pl, const ss2d_attention_sizes& z) {
+  return grid_ok(pl, z) && z.tokens * z.groups * z.key_dim / 256 < INT32_MAX && z.tokens * z.heads / 256 < INT32_MAX;
+}
 
 }  // namespace
 
@@ -147,6 +151,7 @@ int64_t ss2d_linear_attention_backward_workspace(const ss2d_attention_sizes* siz
   const int rc = check_attention_sizes(sizes, packed != 0, dtype);
   if (rc != SS2D_OK) return rc;
   const ss2d::AttentionPlan pl = backward_plan_of(sizes, packed != 0, dtype);
+  if (!backward_grid_ok(pl, *sizes)) return SS2D_ERR_SHAPE;
   return (int64_t)ss2d::attention_backward_workspace_bytes(pl, sizes->tokens, sizes->groups, sizes->heads,
                                                            sizes->key_dim, sizes->value_dim);
 }
@@ -173,8 +178,9 @@ int ss2d_linear_attention_backward(const void* q, const void* k, const void* v, 
   for (const Range& r : in)
     if (r.bytes < 0) return SS2D_ERR_SHAPE;
   const ss2d::AttentionPlan pl = backward_plan_of(sizes, packed, dtype);
-  const int64_t need = ss2d_linear_attention_backward_workspace(sizes, packed ? 1 : 0, dtype);
-  if (!grid_ok(pl, z) || z.tokens * z.groups * z.key_dim / 256 >= INT32_MAX) return SS2D_ERR_SHAPE;
+  if (!backward_grid_ok(pl, z)) return SS2D_ERR_SHAPE;
+  const int64_t need = (int64_t)ss2d::attention_backward_workspace_bytes(pl, z.tokens, z.groups, z.heads, z.key_dim,
+                                                                         z.value_dim);
   const Range out[6] = {{dq, z.tokens * z.groups * z.key_dim * e},   {dk, z.tokens * z.groups * z.key_dim * e},
                         {dv, z.tokens * z.heads * z.value_dim * e},  {dlog_decay, z.tokens * z.heads * 4},
                         {dstate_in, st},                             {need > 0 ? workspace : nullptr, need}};
@@ -209,6 +215,7 @@ int64_t ss2d_linear_attention_workspace(const ss2d_attention_sizes* sizes, int p
   const int rc = check_attention_sizes(sizes, packed != 0, dtype);
   if (rc != SS2D_OK) return rc;
   const ss2d::AttentionPlan pl = plan_of(sizes, packed != 0, dtype);
+  if (!grid_ok(pl, *sizes)) return SS2D_ERR_SHAPE;
   return (int64_t)ss2d::attention_workspace_bytes(pl, sizes->heads, sizes->key_dim, sizes->value_dim);
 }
 
@@ -231,8 +238,8 @@ int ss2d_linear_attention(const void* q, const void* k, const void* v, const flo
     if (r.bytes < 0) return SS2D_ERR_SHAPE;
   const Range ro{o, z.tokens * z.heads * z.value_dim * e}, rs{state_out, in[5].bytes};
   const ss2d::AttentionPlan pl = plan_of(sizes, packed, dtype);
-  const int64_t need = (int64_t)ss2d::attention_workspace_bytes(pl, z.heads, z.key_dim, z.value_dim);
   if (!grid_ok(pl, z)) return SS2D_ERR_SHAPE;
+  const int64_t need = (int64_t)ss2d::attention_workspace_bytes(pl, z.heads, z.key_dim, z.value_dim);
   const Range rw{need > 0 ? workspace : nullptr, need};
   for (int i = 0; i < 6; ++i)
     if (overlap(ro, in[i]) || overlap(rw, in[i]) || (i < 5 ? overlap(rs, in[i]) : partly(rs, in[i])))

@@ -102,6 +102,8 @@ def test_attention_refusals(call):
         assert call(z=resized(**bad)) == SHAPE, bad
     assert call(z=sizes(q=(-1, 32, 16))) == SHAPE
     assert call(z=sizes(v=(1 << 62, 1 << 62, 24))) == SHAPE
+    assert call(z=sizes(v=(1 << 40, 1 << 24, 24))) == SHAPE  # the device multiplies strides of 24 bits
+    assert call(z=sizes(q=(1 << 40, 1 << 24, 16))) == SHAPE
     assert call(dtype=2) == DTYPE
     assert call(q=at(1) + 2) == ALIGN
     assert call(g=at(4) + 1) == ALIGN
@@ -132,6 +134,9 @@ def test_attention_workspace_rules():
     assert lib.ss2d_linear_attention_workspace(sizes(K=300), 0, 0) == SHAPE
     assert lib.ss2d_linear_attention_workspace(sizes(), 0, 5) == DTYPE
     assert lib.ss2d_linear_attention_workspace(None, 0, 0) == NULL
+    for name in ("ss2d_linear_attention_workspace", "ss2d_linear_attention_backward_workspace"):  # no such grid
+        assert getattr(lib, name)(sizes(S=1 << 20, T=1 << 30, G=1, H=65536, K=256, V=1024), 1, 1) == SHAPE
+        assert getattr(lib, name)(sizes(S=1 << 24, T=1 << 24, G=1, H=65536, K=256, V=1024), 0, 0) == SHAPE
     need = lib.ss2d_linear_attention_backward_workspace(sizes(), 0, 0)
     assert need > 0
     assert backward(nbytes=need - 1) == WORKSPACE and backward(ws=None) == WORKSPACE

@@ -174,6 +174,20 @@ def test_tokens_outside_the_sequences_are_left_alone(dtype):
     check("o", got[lead:-tail], ref, to)
 
 
+def test_tokens_far_apart():
+    """Values 2^24 - 1 elements apart, the largest stride taken: offsets beyond 2^31 elements and 2^32 bytes."""
+    T, H, K, V, far = 150, 2, 16, 40, 2 ** 24 - 1
+    q, k, v, g, _ = make([T], 1, H, K, V, "bf16", seed=20)
+    room = torch.empty((T - 1) * far + H * V, dtype=torch.bfloat16, device="cuda")
+    vd = room.as_strided((1, T, H, V), (0, far, V, 1))
+    vd.copy_(_dev(v, "bf16")[None])
+    o = _lib().linear_attention(_dev(q, "bf16")[None], _dev(k, "bf16")[None], vd, _dev(g)[None])
+    torch.cuda.synchronize()
+    ref, _ = tokens.linear_attention(q, k, v, g, [T])
+    to, _ = bounds(q, k, v, g, None, [T], 1.0, "bf16", ref)
+    check("o", _host(o)[0], ref, to)
+
+
 def test_wrong_cu_seqlens_stay_in_range():
     """Offsets beyond the tokens, negative or decreasing: clamped, so finite garbage at worst and a clean exit."""
     q, k, v, g, st = make([300], 1, 2, 16, 16, "f32", seed=10)
