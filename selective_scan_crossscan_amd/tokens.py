@@ -88,14 +88,6 @@ def _workspace(bytes_, device):
 
 
 # ------------------------------------------------------------------ linear attention
-def _token_strides(name, x, lead):
-    """(sequence, token, head) strides of x (*lead, heads, dim), dim dense; lead is (T,) or (S, L)."""
-    st = x.stride()
-    if x.dim() == len(lead) + 2 and x.shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{name}'s last axis must be dense")
-    return (st[0], st[1], st[2]) if len(lead) == 2 else (0, st[0], st[1])
-
-
 def _attention_sizes(q, k, v, log_decay, cu_seqlens, do=None):
     """Checked (sizes array, lead, S, G, H, K, V, code)."""
     packed = cu_seqlens is not None
@@ -103,26 +95,35 @@ def _attention_sizes(q, k, v, log_decay, cu_seqlens, do=None):
     if v.dim() != n or q.dim() != n or k.dim() != n:
         raise ValueError("q, k, v must be (T, heads, dim) with cu_seqlens, else (S, L, heads, dim)")
     code, dtype = _code(v), v.dtype
-    shape = v.shape
-    lead, (H, V) = shape[:-2], shape[-2:]
-    G, K = q.shape[-2:]
-    _require(v, ("v", v, dtype, None, False), ("q", q, dtype, lead + (G, K), False),
-             ("k", k, dtype, lead + (G, K), False), ("log_decay", log_decay, torch.float32, lead + (H,), False))
+    shape, qshape = v.shape, q.shape
+    H, V, G, K = shape[-2], shape[-1], qshape[-2], qshape[-1]
+    lead = (shape[0],) if packed else (shape[0], shape[1])
+    items = [("v", v, dtype, None, False), ("q", q, dtype, lead + (G, K), False), ("k", k, dtype, qshape, False),
+             ("log_decay", log_decay, torch.float32, lead + (H,), False)]
+    if packed:
+        items.append(("cu_seqlens", cu_seqlens, torch.int32, None, True))
+    if do is not None:
+        items.append(("do", do, dtype, shape, False))
+    _require(v, *items)
     if G < 1 or H % G != 0:
         raise ValueError("the heads of v must be a multiple of those of q and k")
     if packed:
-        _require(v, ("cu_seqlens", cu_seqlens, torch.int32, None, True))
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
             raise ValueError("cu_seqlens must be (sequences + 1,)")
         S, T = cu_seqlens.shape[0] - 1, lead[0]
     else:
         S, T = lead[0], lead[0] * lead[1]
-    sizes = [S, T, G, H, K, V, *_token_strides("q", q, lead), *_token_strides("k", k, lead),
-             *_token_strides("v", v, lead), *_token_strides("log_decay", log_decay, lead)]
-    if do is not None:
-        _require(v, ("do", do, dtype, shape, False))
-        sizes += _token_strides("do", do, lead)
-    return _SIZES(*sizes), lead, S, G, H, K, V, code
+    sq, sk, sv, sg = q.stride(), k.stride(), v.stride(), log_decay.stride()
+    sd = sv if do is None else do.stride()
+    if (K > 1 and (sq[-1] != 1 or sk[-1] != 1)) or (V > 1 and (sv[-1] != 1 or sd[-1] != 1)):
+        raise ValueError("the last axis of q, k, v and do must be dense")
+    if packed:
+        sizes = _SIZES(S, T, G, H, K, V, 0, sq[0], sq[1], 0, sk[0], sk[1], 0, sv[0], sv[1], 0, sg[0], sg[1],
+                       0, sd[0], sd[1])
+    else:
+        sizes = _SIZES(S, T, G, H, K, V, sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], *sg,
+                       sd[0], sd[1], sd[2])
+    return sizes, lead, S, G, H, K, V, code
 
 
 def linear_attention(q, k, v, log_decay, state=None, cu_seqlens=None, scale: float = 1.0, final_state: bool = False,
