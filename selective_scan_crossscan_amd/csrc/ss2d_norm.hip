@@ -7,17 +7,19 @@
 //
 // Bound by memory: every value is read once and written once.  A row is held in
 // registers, eight consecutive channels per thread, between the sum over it and
-// the output, so no value is read twice.  A row gets one wave up to 512 channels
-// (four rows per workgroup) and otherwise one workgroup with as many waves as
-// there are groups of 512 channels up to 16, which also keeps a single row's
-// latency at one load, one sum and one store.  The sums are fp32.  16384 rows of
-// 2048 in bf16 with a residual: 52 us, 5.2 TB/s; the gradients 62 us, 4.3 TB/s.
+// the output, so no value is read twice.  A row gets the threads of up to 64 that
+// it needs (several rows per wave) up to 512 channels and otherwise one workgroup
+// with as many waves as there are groups of 512 channels up to 16, which also keeps
+// a single row's latency at one load, one sum and one store.  The sums are fp32.
+// 16384 rows of 2048 in bf16 with a residual: 51 us, 5.3 TB/s; the gradients 62 us,
+// 4.3 TB/s.
 //
 // Threads per row, us for 4 and 16384 rows (bf16 with a residual): 512 channels
 // 64 threads 3.0, 14.2, 256 threads 2.9, 22.2; 1024 channels 64 5.7, 26.8, 256
 // 2.9, 27.9; 2048 channels 64 5.3, 56.3, 256 3.0, 50.7, 512 3.0, 69.2; 4096
 // channels 256 3.8, 107, 512 3.1, 103, 1024 3.3, 144; 8192 channels 512 4.0, 203,
-// 1024 3.5, 206.
+// 1024 3.5, 206.  2^23 values in rows of 59 channels: 8 threads 21.5, 64 100; of
+// 64: 8 12.1, 64 43.9; of 128: 16 12.3, 64 24.6; of 256: 32 12.3, 64 15.3.
 #include "ss2d_token_ops.h"
 
 namespace ss2d {
@@ -28,6 +30,11 @@ using namespace tok;
 // Sum over the THREADS threads that share a row (`red`: one float per wave).
 template <int THREADS>
 __device__ __forceinline__ float row_sum(float v, float* red) {
+  if (THREADS < 64) {
+#pragma unroll
+    for (int m = 1; m < THREADS; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+  }
   v = wave_sum(v);
   if (THREADS > 64) {
     const int wave = threadIdx.x >> 6;
@@ -41,8 +48,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// Threads of a workgroup: one row's, or four rows of one wave each.
-constexpr int block_threads(int per_row) { return per_row == 64 ? 256 : per_row; }
+// Threads of a workgroup: one row's, or 256 for the rows of a wave each or less.
+constexpr int block_threads(int per_row) { return per_row <= 64 ? 256 : per_row; }
 
 template <typename S, int THREADS, int NV, bool FP8>
 __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
@@ -51,17 +58,18 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
   __shared__ float red[THREADS > 64 ? THREADS / 64 : 1];
   const int t = threadIdx.x % THREADS;
   const int64_t row = (int64_t)blockIdx.x * (block_threads(THREADS) / THREADS) + threadIdx.x / THREADS;
-  if (row >= rows) return;  // whole waves, and only where a row is one wave: no barrier follows there
+  if (row >= rows) return;  // whole rows, and only where a row is within a wave: no barrier follows there
   const int64_t at = row * dim;
-  float v[NV][8];
+  float v[NV][8], w[NV][8];
   float sq = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (t + j * THREADS) * 8;
-    load8(x + at + c, dim - c, v[j]);
+    load8(x + at + c, dim - c, dim >= 8, v[j]);
+    if (weight) load8(weight + c, dim - c, dim >= 8, w[j]);
     if (residual) {
       float r[8];
-      load8(residual + at + c, dim - c, r);
+      load8(residual + at + c, dim - c, dim >= 8, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] += r[i];
     }
@@ -73,13 +81,11 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
   for (int j = 0; j < NV; ++j) {
     const int c = (t + j * THREADS) * 8;
     if (residual_out) store8(residual_out + at + c, dim - c, v[j]);
-    float w[8];
-    if (weight) load8(weight + c, dim - c, w);
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (!FP8) v[j][i] *= rstd;
-      if (weight) v[j][i] *= w[i];
+      if (weight) v[j][i] *= w[j][i];
       if (FP8) amax = fmaxf(amax, fabsf(v[j][i]));  // a NaN is passed over here and stays one below
     }
     if (!FP8) {
@@ -119,34 +125,36 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
   }
 }
 
-// Each workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ... and keeps its
-// part of the weight's gradient in registers; norm_sum_partials adds the parts.
+// Each workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (a wave the
+// 64 / THREADS rows of its groups at a time) and keeps its part of the weight's
+// gradient in registers; norm_sum_partials adds the parts.
 template <typename S, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(
+__global__ __launch_bounds__(THREADS < 64 ? 64 : THREADS) void rms_norm_backward_kernel(
     const S* __restrict__ r, const float* __restrict__ weight, const S* dy, const S* dresidual, S* dx,
     float* __restrict__ partial, float eps, int64_t rows, int dim) {
   __shared__ float red[THREADS > 64 ? 2 * THREADS / 64 : 1];
-  const int t = threadIdx.x;
+  constexpr int ROWS = THREADS < 64 ? 64 / THREADS : 1;
+  const int t = threadIdx.x % THREADS;
   float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (t + j * THREADS) * 8;
-    if (weight) load8(weight + c, dim - c, w[j]);
+    if (weight) load8(weight + c, dim - c, dim >= 8, w[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (!weight) w[j][i] = 1.f;
       dw[j][i] = 0.f;
     }
   }
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS; row < rows; row += (int64_t)gridDim.x * ROWS) {
     const int64_t at = row * dim;
     float x[NV][8], g[NV][8];
     float sq = 0.f, dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + j * THREADS) * 8;
-      load8(r + at + c, dim - c, x[j]);
-      load8(dy + at + c, dim - c, g[j]);
+      load8(r + at + c, dim - c, dim >= 8, x[j]);
+      load8(dy + at + c, dim - c, dim >= 8, g[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sq = fmaf(x[j][i], x[j][i], sq);
@@ -161,7 +169,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(
     for (int j = 0; j < NV; ++j) {
       const int c = (t + j * THREADS) * 8;
       float d[8];
-      if (dresidual) load8(dresidual + at + c, dim - c, d);
+      if (dresidual) load8(dresidual + at + c, dim - c, dim >= 8, d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xh = x[j][i] * rstd;
@@ -176,7 +184,11 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (t + j * THREADS) * 8;
-      store8(partial + (int64_t)blockIdx.x * dim + c, dim - c, dw[j]);
+#pragma unroll
+      for (int m = THREADS; m < 64; m <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] += __shfl_xor(dw[j][i], m);
+      if (threadIdx.x < THREADS) store8(partial + (int64_t)blockIdx.x * dim + c, dim - c, dw[j]);
     }
   }
 }
@@ -224,7 +236,14 @@ void launch_norm_t(const NormArgs& a) {
 
 template <typename S>
 hipError_t launch_norm_s(const NormArgs& a) {
-  if (a.dim <= 512)
+  // 8 bits: at least the 16 threads that share a scale
+  if (a.dim <= 64 && !a.scales)
+    launch_norm_t<S, 8, 1>(a);
+  else if (a.dim <= 128)
+    launch_norm_t<S, 16, 1>(a);
+  else if (a.dim <= 256)
+    launch_norm_t<S, 32, 1>(a);
+  else if (a.dim <= 512)
     launch_norm_t<S, 64, 1>(a);
   else if (a.dim <= 2048)
     launch_norm_t<S, 256, 1>(a);
@@ -239,15 +258,21 @@ hipError_t launch_norm_s(const NormArgs& a) {
 
 template <typename S, int THREADS, int NV>
 void launch_norm_backward_t(const NormBackwardArgs& a) {
-  rms_norm_backward_kernel<S, THREADS, NV><<<dim3((unsigned)norm_backward_blocks(a.rows, a.dim)), dim3(THREADS), 0,
-                                             a.stream>>>((const S*)a.r, a.weight, (const S*)a.dy,
+  rms_norm_backward_kernel<S, THREADS, NV><<<dim3((unsigned)norm_backward_blocks(a.rows, a.dim)),
+                                             dim3(THREADS < 64 ? 64 : THREADS), 0, a.stream>>>((const S*)a.r, a.weight, (const S*)a.dy,
                                                          (const S*)a.dresidual, (S*)a.dx,
                                                          a.dweight ? a.partial : nullptr, a.eps, a.rows, (int)a.dim);
 }
 
 template <typename S>
 hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
-  if (a.dim <= 512)
+  if (a.dim <= 64)
+    launch_norm_backward_t<S, 8, 1>(a);
+  else if (a.dim <= 128)
+    launch_norm_backward_t<S, 16, 1>(a);
+  else if (a.dim <= 256)
+    launch_norm_backward_t<S, 32, 1>(a);
+  else if (a.dim <= 512)
     launch_norm_backward_t<S, 64, 1>(a);
   else if (a.dim <= 2048)
     launch_norm_backward_t<S, 256, 1>(a);
@@ -266,10 +291,13 @@ hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
 }  // namespace
 
 int64_t norm_backward_blocks(int64_t rows, int64_t dim) {
-  // 16 waves per CU (8 where each has a row: 512 channels 22.7 us against 25.9; 2048 channels with 8, 16 and 32 waves
-  // 90, 62 and 70 us, 4096 channels 177, 117 and 129), and no more parts than rows
-  const int64_t want = dim <= 512 ? 256 * 8 : 256 * 16 / (dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16);
-  return rows < want ? rows : want;
+  // 16 waves per CU (2048 channels with 8, 16 and 32 waves 90, 62 and 70 us, 4096 channels 177, 117 and 129), 8 where
+  // a wave has whole rows and no ragged ends to wait for (2^23 values in bf16, 8 against 16: rows of 64 22 us and 24,
+  // of 512 23 and 26, of 59 59 and 47, of 414 68 and 51), and no more parts than rows
+  const int64_t want = dim > 512 ? 256 * 16 / (dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16) : 256 * (dim % 8 ? 16 : 8);
+  const int per = dim <= 64 ? 8 : dim <= 128 ? 4 : dim <= 256 ? 2 : 1;  // rows of a wave
+  const int64_t all = (rows + per - 1) / per;
+  return all < want ? all : want;
 }
 
 hipError_t launch_rms_norm(const NormArgs& a) {

@@ -53,6 +53,8 @@ def _half(x, dtype):
 # eight channels, of a block of 128 and of a wave, one channel, odd counts of rows
 SHAPES = [(1, 1), (3, 7), (5, 128), (9, 130), (2, 511), (4, 512), (3, 520), (7, 1000), (2, 2048), (3, 2049), (2, 4096),
           (1, 5000), (2, 8192), (1, 8200), (2, 16384), (1, 16383), (600, 96)]
+# several rows of a wave, and a last group with fewer
+SHAPES += [(20001, 8), (9000, 59), (17000, 64), (9001, 65), (5003, 128), (5000, 129), (4999, 250), (3001, 256), (3000, 257)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
