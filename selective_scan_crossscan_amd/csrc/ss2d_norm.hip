@@ -9,17 +9,18 @@
 // registers, eight consecutive channels per thread, between the sum over it and
 // the output, so no value is read twice.  A row gets the threads of up to 64 that
 // it needs (several rows per wave) up to 512 channels and otherwise one workgroup
-// with as many waves as there are groups of 512 channels up to 16, which also keeps
-// a single row's latency at one load, one sum and one store.  The sums are fp32.
-// 16384 rows of 2048 in bf16 with a residual: 51 us, 5.3 TB/s; the gradients 62 us,
-// 4.3 TB/s.
+// of four waves up to 2048 channels, eight up to 8192 (the gradients' 16 behind 4096)
+// and 16 behind, which also keeps a single row's latency at one load, one sum and one
+// store.  The sums are fp32.
+// 16384 rows of 2048 in bf16 with a residual: 42 us, 6.3 TB/s (part of it from the
+// last-level cache); the gradients 54 us, 5.0 TB/s.
 //
 // Threads per row, us for 4 and 16384 rows (bf16 with a residual): 512 channels
-// 64 threads 3.0, 14.2, 256 threads 2.9, 22.2; 1024 channels 64 5.7, 26.8, 256
-// 2.9, 27.9; 2048 channels 64 5.3, 56.3, 256 3.0, 50.7, 512 3.0, 69.2; 4096
-// channels 256 3.8, 107, 512 3.1, 103, 1024 3.3, 144; 8192 channels 512 4.0, 203,
-// 1024 3.5, 206.  2^23 values in rows of 59 channels: 8 threads 21.5, 64 100; of
-// 64: 8 12.1, 64 43.9; of 128: 16 12.3, 64 24.6; of 256: 32 12.3, 64 15.3.
+// 64 threads 2.6, 12.1, 256 threads 2.9, 21.4; 1024 channels 64 4.2, 25.4, 256
+// 2.7, 25.6; 2048 channels 64 4.2, 49.9, 256 2.8, 42.3, 512 2.9, 54.1; 4096
+// channels 256 3.3, 98, 512 3.0, 92, 1024 3.3, 116; 8192 channels 512 3.6, 191,
+// 1024 3.6, 200.  2^23 values in rows of 59 channels: 8 threads 15.7, 64 50.4; of
+// 64: 8 11.9, 64 38.7; of 128: 16 11.9, 64 21.8; of 256: 32 12.1, 64 14.2.
 #include "ss2d_token_ops.h"
 
 namespace ss2d {
@@ -250,7 +251,7 @@ hipError_t launch_norm_s(const NormArgs& a) {
   else if (a.dim <= 4096)
     launch_norm_t<S, 512, 1>(a);
   else if (a.dim <= 8192)
-    launch_norm_t<S, 1024, 1>(a);
+    launch_norm_t<S, 512, 2>(a);
   else
     launch_norm_t<S, 1024, 2>(a);
   return hipGetLastError();
@@ -291,10 +292,10 @@ hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
 }  // namespace
 
 int64_t norm_backward_blocks(int64_t rows, int64_t dim) {
-  // 16 waves per CU (2048 channels with 8, 16 and 32 waves 90, 62 and 70 us, 4096 channels 177, 117 and 129), 8 where
-  // a wave has whole rows and no ragged ends to wait for (2^23 values in bf16, 8 against 16: rows of 64 22 us and 24,
-  // of 512 23 and 26, of 59 59 and 47, of 414 68 and 51), and no more parts than rows
-  const int64_t want = dim > 512 ? 256 * 16 / (dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16) : 256 * (dim % 8 ? 16 : 8);
+  // 16 waves per CU (2048 channels with 8, 16 and 32 waves 75, 54 and 58 us, 4096 channels 154, 110 and 112), 8 where
+  // a wave has whole rows (2^23 values in bf16, 8 against 16: rows of 64 20.6 us and 23.3, of 512 21.6 and 25.1, of 59
+  // 26.9 and 26.6, of 414 29.1 and 28.4), and no more parts than rows
+  const int64_t want = dim <= 512 ? 256 * 8 : 256 * 16 / (dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16);
   const int per = dim <= 64 ? 8 : dim <= 128 ? 4 : dim <= 256 ? 2 : 1;  // rows of a wave
   const int64_t all = (rows + per - 1) / per;
   return all < want ? all : want;
