@@ -17,7 +17,7 @@
 // by four quarters of a block, in both operands alike.
 //
 // Two kernels.  Products with enough outputs for tiles of 128x128 stage both
-// operands through LDS, double buffered (5001 x 4096 x 4096: 105 us, 1591
+// operands through LDS, double buffered (5001 x 4096 x 4096: 101 us, 1661
 // TFLOP/s).  Fewer are bound by reading b once: there a workgroup's waves split
 // the inner dimension over one strip of 16 n, each streaming its part of b from
 // global memory straight into fragments, and add their sums through LDS in a
