@@ -10,7 +10,8 @@
 // the output, so no value is read twice.  A row gets the threads of up to 64 that
 // it needs (several rows per wave) up to 512 channels and otherwise one workgroup
 // of four waves up to 2048 channels, eight up to 8192 (the gradients' 16 behind 4096)
-// and 16 behind, which also keeps a single row's latency at one load, one sum and one
+// and 16 behind (the gradients' eight, with registers for four times eight channels:
+// 16 waves spilled, 113 us against 71 for 2048 rows of 16384), which also keeps a single row's latency at one load, one sum and one
 // store.  The sums are fp32.
 // 16384 rows of 2048 in bf16 with a residual: 42 us, 6.3 TB/s (part of it from the
 // last-level cache); the gradients 54 us, 5.0 TB/s.
@@ -282,7 +283,7 @@ hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
   else if (a.dim <= 8192)
     launch_norm_backward_t<S, 1024, 1>(a);
   else
-    launch_norm_backward_t<S, 1024, 2>(a);
+    launch_norm_backward_t<S, 512, 4>(a);
   if (a.dweight)
     norm_sum_partials<<<dim3((unsigned)((a.dim + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumRanges), 0, a.stream>>>(
         a.partial, a.dweight, (int)norm_backward_blocks(a.rows, a.dim), (int)a.dim);
