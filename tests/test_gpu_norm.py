@@ -167,3 +167,31 @@ def test_norm_graph_replays_match_eager():
         torch.cuda.synchronize()
         assert torch.equal(y2.view(torch.uint8), y.view(torch.uint8)) and torch.equal(s2, s) and torch.equal(r2, r)
         assert torch.equal(g2["dx"], g["dx"]) and torch.equal(g2["dweight"], g["dweight"])
+
+
+@pytest.mark.parametrize("dim", [5, 59, 414, 1001, 8191, 9001])
+def test_ragged_rows_in_place(dim):
+    """Rows whose ends are loaded together with what lies before them, written over their own inputs."""
+    ss2d = _lib()
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x, r, dy, dr = (torch.randn(301, dim, generator=g, device="cuda").bfloat16() for _ in range(4))
+    w = torch.rand(dim, generator=g, device="cuda")
+    y, s = ss2d.rms_norm(x, w, residual=r)
+    x1, r1 = x.clone(), r.clone()
+    ss2d.rms_norm(x1, w, residual=r1, out=x1, residual_out=r1)
+    x2, r2 = x.clone(), r.clone()
+    ss2d.rms_norm(x2, w, residual=r2, out=r2, residual_out=x2)
+    want = ss2d.rms_norm_backward(s, w, dy, dresidual=dr)
+    L = ss2d.lib()
+    n = L.ss2d_rms_norm_backward_workspace(301, dim, ss2d.SS2D_BF16)
+    ws, dw = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(dim, device="cuda")
+    for over in (0, 1):
+        a, b = dy.clone(), dr.clone()
+        rc = L.ss2d_rms_norm_backward(s.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), 1e-6,
+                                      (a, b)[over].data_ptr(), dw.data_ptr(), 301, dim, ss2d.SS2D_BF16, ws.data_ptr(), n,
+                                      torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.equal((a, b)[over], want["dx"]) and torch.equal(dw, want["dweight"])
+    torch.cuda.synchronize()
+    assert torch.equal(x1, y) and torch.equal(r1, s) and torch.equal(r2, y) and torch.equal(x2, s)
