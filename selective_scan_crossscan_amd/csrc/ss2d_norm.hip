@@ -79,6 +79,10 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
     for (int i = 0; i < 8; ++i) sq = fmaf(v[j][i], v[j][i], sq);
   }
   const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red) / (float)dim + eps);
+  // 8 bits: rstd as a power of two and a factor in [1, 2)
+  const bool finite = rstd < __builtin_inff();
+  const float power = finite ? __uint_as_float(__float_as_uint(rstd) & 0x7f800000u) : rstd;
+  const float factor = finite ? __uint_as_float((__float_as_uint(rstd) & 0x007fffffu) | 0x3f800000u) : 1.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (t + j * THREADS) * 8;
@@ -86,27 +90,29 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (!FP8) v[j][i] *= rstd;
+      v[j][i] *= FP8 ? power : rstd;
       if (weight) v[j][i] *= w[j][i];
       if (FP8) amax = fmaxf(amax, fabsf(v[j][i]));  // a NaN is passed over here and stays one below
     }
     if (!FP8) {
       store8(static_cast<S*>(yv) + at + c, dim - c, v[j]);
     } else {
-      // 16 consecutive threads hold one block of 128 channels.  v is r weight still without rstd, which cancels in
-      // y / s = v 448 / max|v|: fewer roundings before the one to 8 bits, and one division per block
+      // 16 consecutive threads hold one block of 128 channels.  v is y / factor, which cancels out of
+      // y / s = v 448 / max|v|: fewer roundings before the one to 8 bits, and one division per block.  The power of two
+      // costs no rounding and keeps v within a factor of two of y, so the quotient stays in range: a scale over
+      // 2^-126 has max|v| over 224 x 2^-126, and 448 / max|v| under 2^127
 #pragma unroll
       for (int m = 1; m < 16; m <<= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
       constexpr float kLeast = 1.17549435e-38f;  // 2^-126
-      const float t = amax * rstd / 448.0f;
-      const bool least = !(t > kLeast);  // nearly nothing, or NaN
-      const float s = least ? kLeast : t, k = least ? rstd : 448.0f / amax, k2 = least ? 1.0f / kLeast : 1.0f;
+      const float top = amax * factor / 448.0f;
+      const bool least = !(top > kLeast);  // nearly nothing, or NaN
+      const float s = least ? kLeast : top, k = least ? factor : 448.0f / amax, k2 = least ? 1.0f / kLeast : 1.0f;
       const int blocks = (dim + kScaleBlock - 1) / kScaleBlock;
       if ((threadIdx.x & 15) == 0 && c < dim) scales[row * blocks + c / kScaleBlock] = s;
       float u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float z = v[j][i] * k * k2;
+        const float z = v[j][i] * k2 * k;
         u[i] = z > 448.f ? 448.f : z < -448.f ? -448.f : z;  // keeps NaN
       }
       uint32_t q[2];

@@ -195,3 +195,35 @@ def test_ragged_rows_in_place(dim):
         assert torch.equal((a, b)[over], want["dx"]) and torch.equal(dw, want["dweight"])
     torch.cuda.synchronize()
     assert torch.equal(x1, y) and torch.equal(r1, s) and torch.equal(r2, y) and torch.equal(x2, s)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_fp8_small_blocks(dtype, weighted):
+    """Blocks of 128 whose largest value is 2^-145 .. 2^-95, zeros among them, beside one that sets the row's rstd (about
+    140): the definition's values and scales, no NaN from a quotient past fp32's range.  Inputs under 2^-126 are exact;
+    what the tolerances allow is that of test_norm_fp8_matches_oracle."""
+    ss2d = _lib()
+    r = np.random.default_rng(8)
+    rows, dim = 51, 300
+    x = np.zeros((rows, dim), np.float32)
+    x[:, :128] = 0.01 * r.choice([-1, 1], (rows, 128))
+    for i in range(rows):
+        small = np.ldexp(r.uniform(-1, 1, dim - 128), -145 + i).astype(np.float32)
+        small[r.random(dim - 128) < 0.2] = 0
+        x[i, 128:] = small
+    if dtype == "bf16":
+        x = ss2d_inputs.round_to_bf16(x)
+    w = r.uniform(0.5, 1.5, dim).astype(np.float32) if weighted else None
+    q, s = ss2d.rms_norm_fp8(_dev(x, dtype), None if w is None else _dev(w), eps=1e-12)
+    torch.cuda.synchronize()
+    ry, _ = tokens.rms_norm(x, w, None, 1e-12)
+    rs = tokens.block_scales(ry)
+    s, q = _host(s), _host(q)
+    assert np.isfinite(q).all() and not q[ry == 0].any()
+    assert np.all(np.abs(s - rs) <= C * rs)
+    per = np.repeat(s, 128, 1)[:, :dim]
+    lo, hi = tokens.round_e4m3(ry / per * (1 - 2 * C)), tokens.round_e4m3(ry / per * (1 + 2 * C))
+    same = lo == hi
+    assert same.mean() > 0.99
+    assert np.array_equal(q[same], lo[same])
