@@ -31,7 +31,7 @@ namespace ss2d {
 // the lengths is needed.
 struct SequenceMap {
   const int32_t* cu;  // or null: equal lengths
-  int64_t tokens, seg_len;
+  int64_t tokens, seg_len, slots;
   int sequences, nseg;  // nseg: segments per sequence of equal lengths
   int64_t len;          // equal length
 };

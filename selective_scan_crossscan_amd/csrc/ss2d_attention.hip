@@ -60,11 +60,10 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void attention_kernel(AttentionPara
   __shared__ Decays<C> dec;
 
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const int vt = blockIdx.x % p.vtiles;
-  const int head = (blockIdx.x / p.vtiles) % p.heads;
-  const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
+  const int block = (int)block_id(), vt = block % p.vtiles, head = block / p.vtiles % p.heads;
+  const int64_t slot = block / (p.vtiles * p.heads);
   Segment seg;
-  if (!find_segment(p.map, slot, seg)) return;
+  if (slot >= p.map.slots || !find_segment(p.map, slot, seg)) return;
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
   const int vw = wave * 16 * NV;   // this wave's first column in the tile
@@ -251,8 +250,8 @@ namespace {
 
 template <typename E, int C, int VT>
 hipError_t launch_k(const AttentionParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles));
   constexpr int NV = VT / 64;
+  const dim3 grid = grid_of(pl.slots * p.heads * pl.vtiles, pl.kp == 256 && !pl.tiny ? VT * 4 : 256);
   if (pl.tiny) {
     attention_kernel<E, C, 256, 64, 1, true><<<grid, dim3(256), 0, st>>>(p);
     return hipGetLastError();
@@ -330,7 +329,8 @@ AttentionPlan plan_attention_backward(int64_t sequences, int64_t tokens, int64_t
 }
 
 SequenceMap sequence_map(const AttentionArgs& a, const AttentionPlan& pl) {
-  return SequenceMap{a.cu, a.tokens, pl.seg_len, (int)a.sequences, pl.nseg, a.cu ? 0 : a.tokens / a.sequences};
+  return SequenceMap{a.cu,    a.tokens, pl.seg_len, pl.slots, (int)a.sequences,
+                     pl.nseg, a.cu ? 0 : a.tokens / a.sequences};
 }
 
 size_t attention_workspace_bytes(const AttentionPlan& pl, int64_t heads, int64_t key_dim, int64_t value_dim) {

@@ -73,11 +73,10 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
   __shared__ float wrow[NW][C], wcol[NW][C], fs[NW][C], es[NW][C], xs[NW];
 
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const int vt = blockIdx.x % p.vtiles;
-  const int head = (blockIdx.x / p.vtiles) % p.heads;
-  const int64_t slot = blockIdx.x / (p.vtiles * p.heads);
+  const int block = (int)block_id(), vt = block % p.vtiles, head = block / p.vtiles % p.heads;
+  const int64_t slot = block / (p.vtiles * p.heads);
   Segment seg;
-  if (!find_segment(p.map, slot, seg)) return;
+  if (slot >= p.map.slots || !find_segment(p.map, slot, seg)) return;
   const int rep = p.heads / p.groups, group = head / rep;
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
   const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
@@ -427,7 +426,7 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
 template <typename E>
 __global__ __launch_bounds__(256) void sum_parts(const float* __restrict__ parts, E* __restrict__ out, int n,
                                                  int64_t per_token, SequenceMap map) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, size = map.tokens * per_token;
+  const int64_t e = block_id() * 256 + threadIdx.x, size = map.tokens * per_token;
   const int64_t token = e / per_token;
   if (e >= size || (map.cu && (token < cu_at(map, 0) || token >= cu_at(map, map.sequences)))) return;
   float s = parts[e];
@@ -463,7 +462,7 @@ Regions regions(const AttentionPlan& pl, int64_t tokens, int64_t groups, int64_t
 
 template <typename E, int C, int VT, int NW>
 hipError_t launch_k(const BackwardParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.slots * p.heads * pl.vtiles)), block(NW * 64);
+  const dim3 grid = grid_of(pl.slots * p.heads * pl.vtiles, NW * 64), block(NW * 64);
   if (pl.tiny) {
     attention_backward_kernel<E, C, 256, 64, 4, true><<<grid, dim3(256), 0, st>>>(p);
     return hipGetLastError();
@@ -479,7 +478,7 @@ hipError_t launch_k(const BackwardParams& p, const AttentionPlan& pl, hipStream_
 
 template <typename E>
 hipError_t launch_sum(const float* parts, void* out, int n, int64_t per_token, const SequenceMap& map, hipStream_t st) {
-  sum_parts<E><<<dim3((unsigned)((map.tokens * per_token + 255) / 256)), dim3(256), 0, st>>>(
+  sum_parts<E><<<grid_of((map.tokens * per_token + 255) / 256, 256), dim3(256), 0, st>>>(
       parts, static_cast<E*>(out), n, per_token, map);
   return hipGetLastError();
 }

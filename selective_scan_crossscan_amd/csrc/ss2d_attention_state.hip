@@ -33,7 +33,7 @@ struct StateTiles {
   Decays<C> dec;
 };
 
-// One segment's tile of 64 value columns; block: its number among the pass's.
+// One segment's tile of 64 value columns; block: its number among the pass's, nothing where it has none.
 template <typename E, int C, int KP, StatePass PASS, bool TINY>
 __device__ __forceinline__ void state_walk(const StateParams& p, int block, StateTiles<E, C, KP>& lds) {
   constexpr bool REVERSE = PASS == kSegmentGradients;
@@ -46,7 +46,7 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
   const int head = (block / p.tiles) % p.heads;
   const int64_t slot = block / (p.tiles * p.heads);
   Segment seg;
-  if (!find_segment(p.map, slot, seg)) return;
+  if (slot >= p.map.slots || !find_segment(p.map, slot, seg)) return;
   if (PASS == kSegmentStates ? seg.last : PASS == kSegmentGradients ? seg.begin == 0 : false) return;  // of no use
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), vw = wave * 16;
@@ -156,7 +156,7 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
 template <typename E, int C, int KP, StatePass PASS, bool TINY>
 __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_kernel(StateParams p) {
   __shared__ StateTiles<E, C, KP> lds;
-  state_walk<E, C, KP, PASS, TINY>(p, blockIdx.x, lds);
+  state_walk<E, C, KP, PASS, TINY>(p, (int)block_id(), lds);
 }
 
 // What the segments add to the state and to its gradient, one after the other in
@@ -164,11 +164,11 @@ __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_kernel(StateParam
 template <typename E, int C, int KP, bool TINY>
 __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_pair_kernel(StateParams p, StateParams r) {
   __shared__ StateTiles<E, C, KP> lds;
-  const int n = gridDim.x / 2;
-  if ((int)blockIdx.x < n)
-    state_walk<E, C, KP, kSegmentStates, TINY>(p, blockIdx.x, lds);
+  const int64_t block = block_id(), n = p.map.slots * p.heads * p.tiles;
+  if (block < n)
+    state_walk<E, C, KP, kSegmentStates, TINY>(p, (int)block, lds);
   else
-    state_walk<E, C, KP, kSegmentGradients, TINY>(r, blockIdx.x - n, lds);
+    state_walk<E, C, KP, kSegmentGradients, TINY>(r, (int)(block - n), lds);
 }
 
 // seg_state: from what each segment adds to the state before it, or, in reverse, to
@@ -181,7 +181,7 @@ __device__ __forceinline__ void carry_walk(const StateParams& p, const float* fr
   const int64_t blocks = (kv + 255) / 256;
   const int64_t e = block % blocks * 256 + threadIdx.x;
   const int head = (int)(block / blocks % p.heads), s = (int)(block / blocks / p.heads);
-  if (e >= kv) return;
+  if (e >= kv || s >= p.map.sequences) return;
   int64_t slot, len;
   if (p.map.cu) {
     const int64_t start = cu_at(p.map, s), end = cu_at(p.map, s + 1);
@@ -223,16 +223,16 @@ __device__ __forceinline__ void carry_walk(const StateParams& p, const float* fr
 }
 
 __global__ __launch_bounds__(256) void state_carry(StateParams p, const float* from) {
-  carry_walk(p, from, false, blockIdx.x);
+  carry_walk(p, from, false, block_id());
 }
 
 __global__ __launch_bounds__(256) void state_carry_pair(StateParams p, const float* from, StateParams r,
                                                         const float* behind) {
-  const int n = gridDim.x / 2;
-  if ((int)blockIdx.x < n)
-    carry_walk(p, from, false, blockIdx.x);
+  const int64_t block = block_id(), n = ((int64_t)p.K * p.V + 255) / 256 * p.heads * p.map.sequences;
+  if (block < n)
+    carry_walk(p, from, false, block);
   else
-    carry_walk(r, behind, true, blockIdx.x - n);
+    carry_walk(r, behind, true, block - n);
 }
 
 // Calls f with the padded key size and whether rows are tiny as constants.
@@ -251,25 +251,26 @@ void with_keys(const AttentionPlan& pl, F f) {
     f(integral_constant<int, 256>(), integral_constant<bool, false>());
 }
 
-unsigned grid_of(const StateParams& p, const AttentionPlan& pl) { return (unsigned)(pl.slots * p.heads * p.tiles); }
-unsigned carry_grid_of(const StateParams& p) {
-  return (unsigned)(((int64_t)p.K * p.V + 255) / 256 * p.heads * p.map.sequences);
+// passes: 1, or 2 in one launch
+dim3 state_grid(const StateParams& p, int passes) { return grid_of(passes * p.map.slots * p.heads * p.tiles, 256); }
+dim3 carry_grid(const StateParams& p, int passes) {
+  return grid_of(passes * (((int64_t)p.K * p.V + 255) / 256) * p.heads * p.map.sequences, 256);
 }
 
 template <typename E, int C>
 void launch_single(StatePass pass, const StateParams& p, const AttentionPlan& pl, hipStream_t st) {
   with_keys(pl, [&](auto kp, auto tiny) {
     if (pass == kSegmentStates)
-      state_kernel<E, C, kp(), kSegmentStates, tiny()><<<dim3(grid_of(p, pl)), dim3(256), 0, st>>>(p);
+      state_kernel<E, C, kp(), kSegmentStates, tiny()><<<state_grid(p, 1), dim3(256), 0, st>>>(p);
     else
-      state_kernel<E, C, kp(), kChunkStates, tiny()><<<dim3(grid_of(p, pl)), dim3(256), 0, st>>>(p);
+      state_kernel<E, C, kp(), kChunkStates, tiny()><<<state_grid(p, 1), dim3(256), 0, st>>>(p);
   });
 }
 
 template <typename E, int C>
 void launch_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, hipStream_t st) {
   with_keys(pl, [&](auto kp, auto tiny) {
-    state_pair_kernel<E, C, kp(), tiny()><<<dim3(2 * grid_of(p, pl)), dim3(256), 0, st>>>(p, r);
+    state_pair_kernel<E, C, kp(), tiny()><<<state_grid(p, 2), dim3(256), 0, st>>>(p, r);
   });
 }
 
@@ -277,14 +278,14 @@ void launch_pair(const StateParams& p, const StateParams& r, const AttentionPlan
 
 hipError_t launch_segment_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st) {
   dtype == 1 ? launch_single<uint16_t, 64>(kSegmentStates, p, pl, st) : launch_single<float, 32>(kSegmentStates, p, pl, st);
-  state_carry<<<dim3(carry_grid_of(p)), dim3(256), 0, st>>>(p, p.state_in);
+  state_carry<<<carry_grid(p, 1), dim3(256), 0, st>>>(p, p.state_in);
   return hipGetLastError();
 }
 
 hipError_t launch_segment_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, int dtype,
                                hipStream_t st) {
   dtype == 1 ? launch_pair<uint16_t, 64>(p, r, pl, st) : launch_pair<float, 32>(p, r, pl, st);
-  state_carry_pair<<<dim3(2 * carry_grid_of(p)), dim3(256), 0, st>>>(p, p.state_in, r, r.state_in);
+  state_carry_pair<<<carry_grid(p, 2), dim3(256), 0, st>>>(p, p.state_in, r, r.state_in);
   return hipGetLastError();
 }
 

@@ -45,8 +45,9 @@ __global__ __launch_bounds__(kStepThreads) void attention_step_kernel(StepParams
   __shared__ float part[4][VT];
   __shared__ int next_row;
   const int t = threadIdx.x, tv = t % TV, kg = t / TV;
-  const int vt = blockIdx.x % p.vtiles, rest = blockIdx.x / p.vtiles;
-  const int head = rest % p.heads, row0 = rest / p.heads;
+  const uint32_t block = (uint32_t)block_id(), rest = block / p.vtiles;
+  const int vt = block % p.vtiles, head = rest % p.heads, row0 = rest / p.heads;
+  if (row0 >= p.rows) return;  // behind the last workgroup
   const int v0 = vt * VT + tv * 4, nv = p.V - v0;  // this thread's columns, and how many exist
   const int group = head / (p.heads / p.groups);
   const int64_t slot = p.index ? p.index[row0] : row0;
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kStepThreads) void attention_step_kernel(StepParams
 template <typename S, int VT>
 void launch_step_v(const StepArgs& a, StepParams p) {
   p.vtiles = (int)((a.value_dim + VT - 1) / VT);
-  const dim3 grid((unsigned)(a.rows * a.heads * p.vtiles)), block(kStepThreads);
+  const dim3 grid = grid_of(a.rows * a.heads * p.vtiles, kStepThreads), block(kStepThreads);
   if (a.key_dim <= 64)
     attention_step_kernel<S, 64, VT><<<grid, block, 0, a.stream>>>(p);
   else if (a.key_dim <= 128)

@@ -151,8 +151,10 @@ __global__ __launch_bounds__(256, 2) void matmul_fp8_tiles(MatmulParams p) {
             l = lane & 15;
   // Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets a band of columns of tiles and walks
   // down it row by row, so that a row of a is read once for the whole band and the band's rows of b stay in its L2.
-  const int total = p.mtiles * p.ntiles, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
-  const int at = xcd * each + min(xcd, more) + (blockIdx.x >> 3);
+  const int block = (int)block_id(), total = p.mtiles * p.ntiles;
+  if (block >= total) return;
+  const int xcd = block & 7, each = total >> 3, more = total & 7;
+  const int at = xcd * each + min(xcd, more) + (block >> 3);
   const int width = (p.ntiles + 7) >> 3, band = at / (width * p.mtiles), rest = at - band * width * p.mtiles;
   const int here = min(width, p.ntiles - band * width);  // the last band may be narrower
   const int64_t m0 = (int64_t)(rest / here) * kTile, n0 = (int64_t)(band * width + rest % here) * kTile;
@@ -333,7 +335,7 @@ hipError_t launch_o(const MatmulArgs& x) {
   // 256 x 1024 15.6 (26.4), 512 x 1024 28.2 (26.3), 16 x 16384 22.9 (31.4), 48 x 16384 43.9 (32.4); fp32 outputs,
   // whose tiles take longer: 128 x 4096 29.1 (38.6), 256 x 4096 54.4 (38.8), 48 x 16384 46.6 (38.7).
   if (x.m * x.n >= (sizeof(O) == 2 ? 1 << 19 : 3 << 18)) {
-    const dim3 grid((unsigned)((int64_t)p.mtiles * p.ntiles)), block(256);
+    const dim3 grid = grid_of((int64_t)p.mtiles * p.ntiles, 256), block(256);
     // 16-byte copies into LDS; odd rows through registers (4096 cubed: 84 us against 118)
     if (x.k % 16 == 0 && (((uintptr_t)x.a | (uintptr_t)x.b) & 15) == 0)
       matmul_fp8_tiles<O, true><<<grid, block, 0, x.stream>>>(p);

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(block_threads(THREADS)) void rms_norm_kernel(
     float* __restrict__ scales, float eps, int64_t rows, int dim) {
   __shared__ float red[THREADS > 64 ? THREADS / 64 : 1];
   const int t = threadIdx.x % THREADS;
-  const int64_t row = (int64_t)blockIdx.x * (block_threads(THREADS) / THREADS) + threadIdx.x / THREADS;
+  const int64_t row = block_id() * (block_threads(THREADS) / THREADS) + threadIdx.x / THREADS;
   if (row >= rows) return;  // whole rows, and only where a row is within a wave: no barrier follows there
   const int64_t at = row * dim;
   float v[NV][8], w[NV][8];
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(kSumCols * kSumRanges) void norm_sum_partials(const
 template <typename S, int THREADS, int NV>
 void launch_norm_t(const NormArgs& a) {
   const int per = block_threads(THREADS) / THREADS;
-  const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(block_threads(THREADS));
+  const dim3 block(block_threads(THREADS)), grid = grid_of((a.rows + per - 1) / per, block.x);
   if (a.scales)
     rms_norm_kernel<S, THREADS, NV, true><<<grid, block, 0, a.stream>>>(
         (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, a.scales, a.eps, a.rows, (int)a.dim);

@@ -70,8 +70,19 @@ struct MatmulArgs {
 };
 hipError_t launch_matmul_fp8(const MatmulArgs& a);
 
+// A launch of `blocks` workgroups, along x and, where their threads pass 2^31, y too: an axis takes fewer than 2^32
+// threads, and one with more runs a part of them without an error.  The axes may hold a few workgroups too many, which
+// leave by block_id().
+inline dim3 grid_of(int64_t blocks, int threads) {
+  const int64_t most = ((int64_t)1 << 31) / threads, y = (blocks + most - 1) / most;
+  return dim3((unsigned)((blocks + y - 1) / y), (unsigned)y);
+}
+
 // ------------------------------------------------------------------ device helpers
 namespace tok {
+
+// This workgroup's number in a grid_of.
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 constexpr float kLog2e = 1.4426950408889634f;
 // A decay under exp(-104) is 0 in fp32; sums of clamped logarithms stay finite.
