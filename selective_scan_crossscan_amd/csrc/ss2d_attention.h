@@ -146,16 +146,20 @@ __device__ __forceinline__ bool find_segment(const SequenceMap& m, int64_t slot,
     g.start = (int64_t)g.s * m.len;
     g.len = m.len;
   } else {
-    // the last sequence whose first slot is at most `slot`: the lanes look at 64 sequences at a time (first slots
-    // ascend, so counting finds it), one load's latency where a search would take one per halving
+    // the last sequence whose first slot is at most `slot`, by counting (first slots ascend): the lanes look at 64
+    // sequences, spread over those left, until they are next to each other; one load's latency for up to 64 sequences,
+    // two for 4096, where a search by halves would take one per halving and a walk over all of them one per 64
     const uint32_t seg_len = (uint32_t)m.seg_len;
-    int lo = -1;
-    for (int s0 = 0; s0 < m.sequences; s0 += 64) {
-      const int s = s0 + (int)(threadIdx.x & 63);
-      const bool before = s < m.sequences && (int64_t)((uint32_t)cu_at(m, min(s, m.sequences - 1)) / seg_len) + s <= slot;
-      lo += __popcll(__ballot(before));
+    int lo = 0;
+    for (int left = m.sequences, step; left > 1; left = min(left, step)) {
+      step = (left + 63) / 64;
+      const int ahead = min((int)(threadIdx.x & 63) * step, left);
+      const bool before = ahead < left && (int64_t)((uint32_t)cu_at(m, lo + min(ahead, left - 1)) / seg_len) + lo + ahead <= slot;
+      const int count = (int)__popcll(__ballot(before));
+      const int skip = count > 1 ? (count - 1) * step : 0;  // offsets that do not ascend may leave none
+      lo += skip;
+      left -= skip;
     }
-    lo = max(lo, 0);  // offsets that do not ascend may leave none
     g.s = lo;
     g.start = cu_at(m, lo);
     const int64_t end = cu_at(m, lo + 1);

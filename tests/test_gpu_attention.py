@@ -354,3 +354,19 @@ def test_two_streams_at_once():
     for pair in outs:
         for got, (_, want) in zip(pair, sets):
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("count", [2, 63, 64, 65, 4096, 4097, 9000])
+def test_many_short_sequences(count):
+    """Sequences of 0 to 3 tokens, and one of 600 among them: every one is found, its states its own."""
+    r = np.random.default_rng(count)
+    lens = r.integers(0, 4, count).tolist()
+    lens[count * 2 // 3] = 600
+    q, k, v, g, st = make(lens, 1, 2, 8, 12, "f32", seed=count + 1)
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32).cuda()
+    o, last = _lib().linear_attention(_dev(q), _dev(k), _dev(v), _dev(g), state=_dev(st), cu_seqlens=cu, final_state=True)
+    torch.cuda.synchronize()
+    ref_o, ref_s = tokens.linear_attention(q, k, v, g, lens, st)
+    to, ts = bounds(q, k, v, g, st, lens, 1.0, "f32", ref_o)
+    check("o", _host(o), ref_o, to)
+    check("state", _host(last), ref_s, ts)
