@@ -31,7 +31,7 @@ namespace ss2d {
 // the lengths is needed.
 struct SequenceMap {
   const int32_t* cu;  // or null: equal lengths
-  int64_t tokens, seg_len, slots;
+  int64_t tokens, seg_len;
   int sequences, nseg;  // nseg: segments per sequence of equal lengths
   int64_t len;          // equal length
 };
@@ -101,9 +101,12 @@ struct StateParams {
   SequenceMap map;
   int64_t k_stride[3], v_stride[3], g_stride[3];
   int groups, heads, K, V, tiles;  // tiles of 64 value columns
+  uint32_t blocks, carry_blocks;   // workgroups of a pass over the segments, of a carry
   float scale;
   bool split;             // segments start from seg_state
 };
+// Sets blocks and carry_blocks from the other sizes.
+void count_blocks(StateParams& p, const AttentionPlan& pl);
 // seg_state: the state before every segment of a sequence of several.
 hipError_t launch_segment_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st);
 // The same, and r's seg_state: the gradient of the state behind every segment of a sequence of several.

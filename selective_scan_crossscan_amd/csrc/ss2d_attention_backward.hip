@@ -52,6 +52,7 @@ struct BackwardParams {
   SequenceMap map;
   int64_t q_stride[3], k_stride[3], v_stride[3], do_stride[3], g_stride[3];
   int groups, heads, K, V, vtiles;
+  uint32_t blocks;  // workgroups
   float scale;
   bool split;
 };
@@ -73,10 +74,12 @@ __global__ __launch_bounds__(NW * 64) void attention_backward_kernel(BackwardPar
   __shared__ float wrow[NW][C], wcol[NW][C], fs[NW][C], es[NW][C], xs[NW];
 
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const int block = (int)block_id(), vt = block % p.vtiles, head = block / p.vtiles % p.heads;
+  const uint32_t block = (uint32_t)block_id();
+  if (block >= p.blocks) return;
+  const int vt = block % p.vtiles, head = block / p.vtiles % p.heads;
   const int64_t slot = block / (p.vtiles * p.heads);
   Segment seg;
-  if (slot >= p.map.slots || !find_segment(p.map, slot, seg)) return;
+  if (!find_segment(p.map, slot, seg)) return;
   const int rep = p.heads / p.groups, group = head / rep;
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT);
   const int64_t first = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
@@ -462,7 +465,7 @@ Regions regions(const AttentionPlan& pl, int64_t tokens, int64_t groups, int64_t
 
 template <typename E, int C, int VT, int NW>
 hipError_t launch_k(const BackwardParams& p, const AttentionPlan& pl, hipStream_t st) {
-  const dim3 grid = grid_of(pl.slots * p.heads * pl.vtiles, NW * 64), block(NW * 64);
+  const dim3 grid = grid_of(p.blocks, NW * 64), block(NW * 64);
   if (pl.tiny) {
     attention_backward_kernel<E, C, 256, 64, 4, true><<<grid, dim3(256), 0, st>>>(p);
     return hipGetLastError();
@@ -506,6 +509,7 @@ hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const Atten
   s.K = (int)f.key_dim;
   s.V = (int)f.value_dim;
   s.tiles = pl.vtiles * (pl.vt / 64);
+  count_blocks(s, pl);
   s.scale = f.scale;
   s.split = pl.split;
   for (int i = 0; i < 3; ++i) s.g_stride[i] = f.g_stride[i];
@@ -565,6 +569,7 @@ hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const Atten
   p.K = s.K;
   p.V = s.V;
   p.vtiles = pl.vtiles;
+  p.blocks = (uint32_t)(pl.slots * f.heads * pl.vtiles);
   p.scale = f.scale;
   p.split = pl.split;
   if (f.dtype == 1)

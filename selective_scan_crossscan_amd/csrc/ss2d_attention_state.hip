@@ -33,9 +33,9 @@ struct StateTiles {
   Decays<C> dec;
 };
 
-// One segment's tile of 64 value columns; block: its number among the pass's, nothing where it has none.
+// One segment's tile of 64 value columns; block: its number among the pass's.
 template <typename E, int C, int KP, StatePass PASS, bool TINY>
-__device__ __forceinline__ void state_walk(const StateParams& p, int block, StateTiles<E, C, KP>& lds) {
+__device__ __forceinline__ void state_walk(const StateParams& p, uint32_t block, StateTiles<E, C, KP>& lds) {
   constexpr bool REVERSE = PASS == kSegmentGradients;
   constexpr int VT = 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   auto& ks = lds.ks;
@@ -46,7 +46,7 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
   const int head = (block / p.tiles) % p.heads;
   const int64_t slot = block / (p.tiles * p.heads);
   Segment seg;
-  if (slot >= p.map.slots || !find_segment(p.map, slot, seg)) return;
+  if (!find_segment(p.map, slot, seg)) return;
   if (PASS == kSegmentStates ? seg.last : PASS == kSegmentGradients ? seg.begin == 0 : false) return;  // of no use
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), vw = wave * 16;
@@ -156,7 +156,8 @@ __device__ __forceinline__ void state_walk(const StateParams& p, int block, Stat
 template <typename E, int C, int KP, StatePass PASS, bool TINY>
 __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_kernel(StateParams p) {
   __shared__ StateTiles<E, C, KP> lds;
-  state_walk<E, C, KP, PASS, TINY>(p, (int)block_id(), lds);
+  const uint32_t block = (uint32_t)block_id();
+  if (block < p.blocks) state_walk<E, C, KP, PASS, TINY>(p, block, lds);
 }
 
 // What the segments add to the state and to its gradient, one after the other in
@@ -164,11 +165,11 @@ __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_kernel(StateParam
 template <typename E, int C, int KP, bool TINY>
 __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_pair_kernel(StateParams p, StateParams r) {
   __shared__ StateTiles<E, C, KP> lds;
-  const int64_t block = block_id(), n = p.map.slots * p.heads * p.tiles;
+  const uint32_t block = (uint32_t)block_id(), n = p.blocks;
   if (block < n)
-    state_walk<E, C, KP, kSegmentStates, TINY>(p, (int)block, lds);
-  else
-    state_walk<E, C, KP, kSegmentGradients, TINY>(r, (int)(block - n), lds);
+    state_walk<E, C, KP, kSegmentStates, TINY>(p, block, lds);
+  else if (block - n < n)
+    state_walk<E, C, KP, kSegmentGradients, TINY>(r, block - n, lds);
 }
 
 // seg_state: from what each segment adds to the state before it, or, in reverse, to
@@ -176,12 +177,10 @@ __global__ __launch_bounds__(256, KP <= 64 ? 4 : 2) void state_pair_kernel(State
 // (the first one's is a copy of the initial state: the last segment's workgroup may
 // write the final state over that one before the first has begun).  One thread per
 // state entry walks its sequence's segments, eight sums read at a time.
-__device__ __forceinline__ void carry_walk(const StateParams& p, const float* from, bool reverse, int64_t block) {
-  const int64_t kv = (int64_t)p.K * p.V;
-  const int64_t blocks = (kv + 255) / 256;
-  const int64_t e = block % blocks * 256 + threadIdx.x;
-  const int head = (int)(block / blocks % p.heads), s = (int)(block / blocks / p.heads);
-  if (e >= kv || s >= p.map.sequences) return;
+__device__ __forceinline__ void carry_walk(const StateParams& p, const float* from, bool reverse, uint32_t block) {
+  const int kv = p.K * p.V, blocks = (kv + 255) / 256;
+  const int e = block % blocks * 256 + threadIdx.x, head = block / blocks % p.heads, s = block / blocks / p.heads;
+  if (e >= kv) return;
   int64_t slot, len;
   if (p.map.cu) {
     const int64_t start = cu_at(p.map, s), end = cu_at(p.map, s + 1);
@@ -196,7 +195,7 @@ __device__ __forceinline__ void carry_walk(const StateParams& p, const float* fr
   // along the walk: a segment's sum moves the state on, and what lies before (behind) the next one replaces its sum
   if (reverse) slot += n - 1;
   const int dir = reverse ? -1 : 1;
-  const int64_t step = dir * p.heads * kv;
+  const int64_t step = (int64_t)dir * p.heads * kv;
   float* u = p.seg_state + (slot * p.heads + head) * kv + e;
   const float* a = p.seg_decay + slot * p.heads + head;
   float h = from ? from[((int64_t)s * p.heads + head) * kv + e] : 0.f;
@@ -223,15 +222,16 @@ __device__ __forceinline__ void carry_walk(const StateParams& p, const float* fr
 }
 
 __global__ __launch_bounds__(256) void state_carry(StateParams p, const float* from) {
-  carry_walk(p, from, false, block_id());
+  const uint32_t block = (uint32_t)block_id();
+  if (block < p.carry_blocks) carry_walk(p, from, false, block);
 }
 
 __global__ __launch_bounds__(256) void state_carry_pair(StateParams p, const float* from, StateParams r,
                                                         const float* behind) {
-  const int64_t block = block_id(), n = ((int64_t)p.K * p.V + 255) / 256 * p.heads * p.map.sequences;
+  const uint32_t block = (uint32_t)block_id(), n = p.carry_blocks;
   if (block < n)
     carry_walk(p, from, false, block);
-  else
+  else if (block - n < n)
     carry_walk(r, behind, true, block - n);
 }
 
@@ -251,41 +251,41 @@ void with_keys(const AttentionPlan& pl, F f) {
     f(integral_constant<int, 256>(), integral_constant<bool, false>());
 }
 
-// passes: 1, or 2 in one launch
-dim3 state_grid(const StateParams& p, int passes) { return grid_of(passes * p.map.slots * p.heads * p.tiles, 256); }
-dim3 carry_grid(const StateParams& p, int passes) {
-  return grid_of(passes * (((int64_t)p.K * p.V + 255) / 256) * p.heads * p.map.sequences, 256);
-}
 
 template <typename E, int C>
 void launch_single(StatePass pass, const StateParams& p, const AttentionPlan& pl, hipStream_t st) {
   with_keys(pl, [&](auto kp, auto tiny) {
     if (pass == kSegmentStates)
-      state_kernel<E, C, kp(), kSegmentStates, tiny()><<<state_grid(p, 1), dim3(256), 0, st>>>(p);
+      state_kernel<E, C, kp(), kSegmentStates, tiny()><<<grid_of(p.blocks, 256), dim3(256), 0, st>>>(p);
     else
-      state_kernel<E, C, kp(), kChunkStates, tiny()><<<state_grid(p, 1), dim3(256), 0, st>>>(p);
+      state_kernel<E, C, kp(), kChunkStates, tiny()><<<grid_of(p.blocks, 256), dim3(256), 0, st>>>(p);
   });
 }
 
 template <typename E, int C>
 void launch_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, hipStream_t st) {
   with_keys(pl, [&](auto kp, auto tiny) {
-    state_pair_kernel<E, C, kp(), tiny()><<<state_grid(p, 2), dim3(256), 0, st>>>(p, r);
+    state_pair_kernel<E, C, kp(), tiny()><<<grid_of(2 * (int64_t)p.blocks, 256), dim3(256), 0, st>>>(p, r);
   });
 }
 
 }  // namespace
 
+void count_blocks(StateParams& p, const AttentionPlan& pl) {
+  p.blocks = (uint32_t)(pl.slots * p.heads * p.tiles);
+  p.carry_blocks = (uint32_t)(((int64_t)p.K * p.V + 255) / 256 * p.heads * p.map.sequences);
+}
+
 hipError_t launch_segment_states(const StateParams& p, const AttentionPlan& pl, int dtype, hipStream_t st) {
   dtype == 1 ? launch_single<uint16_t, 64>(kSegmentStates, p, pl, st) : launch_single<float, 32>(kSegmentStates, p, pl, st);
-  state_carry<<<carry_grid(p, 1), dim3(256), 0, st>>>(p, p.state_in);
+  state_carry<<<grid_of(p.carry_blocks, 256), dim3(256), 0, st>>>(p, p.state_in);
   return hipGetLastError();
 }
 
 hipError_t launch_segment_pair(const StateParams& p, const StateParams& r, const AttentionPlan& pl, int dtype,
                                hipStream_t st) {
   dtype == 1 ? launch_pair<uint16_t, 64>(p, r, pl, st) : launch_pair<float, 32>(p, r, pl, st);
-  state_carry_pair<<<carry_grid(p, 2), dim3(256), 0, st>>>(p, p.state_in, r, r.state_in);
+  state_carry_pair<<<grid_of(2 * (int64_t)p.carry_blocks, 256), dim3(256), 0, st>>>(p, p.state_in, r, r.state_in);
   return hipGetLastError();
 }
 
