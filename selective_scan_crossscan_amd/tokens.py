@@ -8,7 +8,9 @@ marshals arguments, and there is no CPU fallback.
 
 Every function runs on `stream`, or on the current stream of the tensors' device,
 and allocates its outputs and workspace from torch's allocator on that stream, so
-it can run under torch.cuda.graph.
+it can run under torch.cuda.graph.  With `stream` the caller orders the streams
+(wait_stream, events) where one uses what the other wrote; the tensors' memory is
+kept from others until both are done with it.
 """
 from __future__ import annotations
 
@@ -61,11 +63,20 @@ def _call(fn, device, *args):
         check(rc)
 
 
-def _on_stream(stream, device, fn, *args, **kwargs):
+def _on_stream(stream, device, fn, *args):
+    """fn(*args) with `stream` current.  Tensors that go in and come out are marked as used by both streams, so that the
+    allocator gives their memory to no one before either stream is done with it, however soon the caller lets them go."""
     if stream.device != device:
         raise ValueError("stream must belong to the tensors' device")
+    caller = torch.cuda.current_stream(device)
+    for x in args:
+        if isinstance(x, torch.Tensor) and x.is_cuda:
+            x.record_stream(stream)
     with torch.cuda.stream(stream):
-        return fn(*args, **kwargs)
+        out = fn(*args)
+    for x in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        x.record_stream(caller)
+    return out
 
 
 def _ptr(x):
