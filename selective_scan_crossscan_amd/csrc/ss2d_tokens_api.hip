@@ -65,15 +65,16 @@ bool partly(const Range& a, const Range& b) { return a.p != b.p && overlap(a, b)
 
 // ------------------------------------------------------------------ attention
 // Bytes from a strided tensor's first to behind its last element; -1 if they do
-// not fit.  Axes: sequence (unused when packed), token, head, and `inner` dense.
+// not fit.  Axes: sequence (unused when packed), token (at most `far` apart), head,
+// and `inner` dense.
 int64_t extent(const int64_t* stride, int64_t sequences, int64_t tokens, int64_t heads, int64_t inner, bool packed,
-               int64_t elem) {
+               int64_t elem, int64_t far = ss2d::kMaxTokenStride) {
   const int64_t n[3] = {packed ? 1 : sequences, packed ? tokens : tokens / sequences, heads};
   int64_t last = 0;
   for (int i = 0; i < 3; ++i) {
     int64_t part;
     if (n[i] == 1) continue;
-    if (stride[i] < 0 || (i == 1 && stride[i] > ss2d::kMaxTokenStride) || __builtin_mul_overflow(n[i] - 1, stride[i], &part) ||
+    if (stride[i] < 0 || (i == 1 && stride[i] > far) || __builtin_mul_overflow(n[i] - 1, stride[i], &part) ||
         __builtin_add_overflow(last, part, &last))
       return -1;
   }
@@ -269,9 +270,9 @@ int ss2d_linear_attention_step(const void* q, const void* k, const void* v, cons
   if (!dtype_ok(dtype)) return SS2D_ERR_DTYPE;
   const int64_t e = elem_bytes(dtype);
   const int64_t strides[3][3] = {{0, q_row, 0}, {0, k_row, 0}, {0, v_row, 0}};
-  const Range in[5] = {{q, extent(strides[0], 1, rows, 1, groups * key_dim, true, e)},
-                       {k, extent(strides[1], 1, rows, 1, groups * key_dim, true, e)},
-                       {v, extent(strides[2], 1, rows, 1, heads * value_dim, true, e)},
+  const Range in[5] = {{q, extent(strides[0], 1, rows, 1, groups * key_dim, true, e, INT64_MAX)},
+                       {k, extent(strides[1], 1, rows, 1, groups * key_dim, true, e, INT64_MAX)},
+                       {v, extent(strides[2], 1, rows, 1, heads * value_dim, true, e, INT64_MAX)},
                        {log_decay, rows * heads * 4},
                        {index, rows * 4}};
   for (const Range& r : in)

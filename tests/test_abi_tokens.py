@@ -258,3 +258,15 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         ss2d.linear_attention(x, x, x, x)
     with pytest.raises(AttributeError):
         ss2d.no_such_operator
+
+
+def test_step_rows_may_lie_any_distance_apart():
+    """Only prompts limit the distance of tokens to 24 bits."""
+    assert step(o=at(3), q_row=1 << 24) == ALIAS  # past the checks of sizes
+    assert step(o=at(3), q_row=1 << 30) == ALIAS
+    assert step(o=at(3), q_row=1 << 62) == SHAPE
+
+
+@needs_no_device
+def test_step_far_rows_reach_the_device():
+    assert step(q_row=1 << 24, q=at(100)) == NO_DEVICE

@@ -370,3 +370,20 @@ def test_many_short_sequences(count):
     to, ts = bounds(q, k, v, g, st, lens, 1.0, "f32", ref_o)
     check("o", _host(o), ref_o, to)
     check("state", _host(last), ref_s, ts)
+
+
+def test_step_rows_far_apart():
+    """Rows of v 2^31 + 3 elements apart: offsets beyond 32 bits."""
+    B, H, K, V, far = 3, 2, 16, 40, 2 ** 31 + 3
+    q, k, v, g, _ = make([B], 1, H, K, V, "bf16", seed=31)
+    st = np.random.default_rng(32).standard_normal((B, H, K, V)).astype(np.float32)
+    room = torch.empty((B - 1) * far + H * V, dtype=torch.bfloat16, device="cuda")
+    vd = room.as_strided((B, H, V), (far, V, 1))
+    vd.copy_(_dev(v, "bf16"))
+    sd = _dev(st)
+    o = _lib().linear_attention_step(_dev(q, "bf16"), _dev(k, "bf16"), vd, _dev(g), sd)
+    torch.cuda.synchronize()
+    ref_o, ref_s = tokens.linear_attention_step(q, k, v, g, st, np.arange(B))
+    abs_o, abs_s = tokens.linear_attention_step(abs(q), abs(k), abs(v), g, abs(st), np.arange(B))
+    check("o", _host(o), ref_o, (K + 16) * 2.0 ** -24 * abs_o + 2.0 ** -8 * np.abs(ref_o) + 1e-37)
+    check("state", _host(sd), ref_s, 8 * 2.0 ** -24 * abs_s)
