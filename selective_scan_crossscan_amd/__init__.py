@@ -8,19 +8,21 @@ library is missing or the tensors are not on a ROCm device, calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 
 from ._lib import SS2D_BF16, SS2D_F32, Peaks, SS2DError, lib, library_path, status_string
 from ._lib import check as _raise
 
 __all__ = ["forward", "ss2d_forward", "project", "ss2d_project", "forward_from_x", "ss2d_forward_from_x",
            "channel_last", "ss2d_channel_last", "backward", "ss2d_backward", "measure_peaks", "describe", "bidir_forward", "ss2d_bidir_forward", "bidir_backward", "ss2d_bidir_backward", "ss2d_forward_noalloc", "trim_memory", "status_string", "version", "library_path", "lib",
-           "SS2D_F32", "SS2D_BF16", "SS2DError",
-           "linear_attention", "linear_attention_backward", "linear_attention_step", "rms_norm",
-           "rms_norm_fp8", "rms_norm_backward", "matmul_fp8"]
+           "SS2D_F32", "SS2D_BF16", "SS2DError"]
 
-# The token-sequence operators (tokens.py), imported with torch when first used.
+# The token-sequence operators (tokens.py), imported with torch when first used; without torch the rest of the package
+# works on raw addresses, `from ... import *` too.
 _TOKENS = ("linear_attention", "linear_attention_backward", "linear_attention_step", "rms_norm",
            "rms_norm_fp8", "rms_norm_backward", "matmul_fp8")
+if importlib.util.find_spec("torch") is not None:
+    __all__ += _TOKENS
 
 
 def __getattr__(name):

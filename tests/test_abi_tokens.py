@@ -270,3 +270,15 @@ def test_step_rows_may_lie_any_distance_apart():
 @needs_no_device
 def test_step_far_rows_reach_the_device():
     assert step(q_row=1 << 24, q=at(100)) == NO_DEVICE
+
+
+@pytest.mark.parametrize("torch_there", [False, True])
+def test_everything_imports_with_and_without_torch(torch_there):
+    import subprocess
+    import sys
+    if torch_there:
+        pytest.importorskip("torch")
+    code = ("import sys\n" + ("" if torch_there else "sys.modules['torch'] = None\n")
+            + "from selective_scan_crossscan_amd import *\nassert version() > 0 and ss2d_forward\n"
+            + f"assert ('rms_norm' in dir()) == {torch_there}")
+    subprocess.check_call([sys.executable, "-c", code], cwd=ROOT)
