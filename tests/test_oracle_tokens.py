@@ -110,3 +110,22 @@ def test_block_scales_and_product():
     out = tokens.matmul_fp8(a, sa, b, sb)
     want = sum(a[2, k] * sa[2, k // 128] * b[140, k] * sb[1, k // 128] for k in range(200))
     np.testing.assert_allclose(out[2, 140], want, rtol=1e-12)
+
+
+def test_torch_reference_is_the_oracle():
+    """tests/token_reference.py, which the tests of long sequences use, against the oracle: both in 64 bits."""
+    torch = pytest.importorskip("torch")
+    import token_reference
+    r = np.random.default_rng(9)
+    lens, G, H, K, V = [5, 0, 7], 2, 4, 3, 6
+    T = sum(lens)
+    q, k, v, do = (r.standard_normal((T, n, d)) for n, d in ((G, K), (G, K), (H, V), (H, V)))
+    g, st, dl = -r.random((T, H)), r.standard_normal((3, H, K, V)), r.standard_normal((3, H, K, V))
+    t = [torch.from_numpy(x) for x in (q, k, v, g)]
+    for s, d in ((st, dl), (None, None)):
+        s_, d_ = (None if x is None else torch.from_numpy(x) for x in (s, d))
+        for a, b in zip(token_reference.attention(*t, lens, s_, 0.3), tokens.linear_attention(q, k, v, g, lens, s, 0.3)):
+            np.testing.assert_allclose(a.numpy(), b, rtol=1e-12, atol=1e-12)
+        for a, b in zip(token_reference.attention_backward(*t, torch.from_numpy(do), lens, s_, d_, 0.3),
+                        tokens.linear_attention_backward(q, k, v, g, do, lens, s, d, 0.3)):
+            np.testing.assert_allclose(a.numpy(), b, rtol=1e-12, atol=1e-12)
