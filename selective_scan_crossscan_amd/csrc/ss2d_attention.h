@@ -16,7 +16,7 @@
 // operand is split into bf16 parts that add up to it, each the rounding of what
 // the parts before left: three give all 24 bits.  What becomes an fp32 result
 // (states, gradients of the decay) takes three.  What only ends in a bf16 output
-// takes one, as the masked scores do: its rounding, 2^-9 of its share of the output
+// takes one, as the masked scores do: its rounding, 2^-8 of its share of the output
 // at most, is that of the output itself.  The fp32 product takes the value itself.
 #pragma once
 

@@ -8,8 +8,8 @@
 //   h  <- exp(G_last) h + sum_j exp(G_last - G_j) k_j v_j'.
 //
 // One workgroup walks a segment of one sequence and head for VT value columns,
-// chunk after chunk; the state never leaves its registers.  Each wave owns 16
-// value columns: their part of the state (all key rows, fp32, as result tiles
+// chunk after chunk; the state never leaves its registers.  Each wave owns 16 value
+// columns, 32 in tiles of 128 of up to 128 keys: their part of the state (all key rows, fp32, as result tiles
 // whose rows are the key index), of v and of the output.  The
 // scores are the one thing waves share: each computes 16 tokens' (transposed,
 // so that a lane has four consecutive keys' scores of one token), applies decay

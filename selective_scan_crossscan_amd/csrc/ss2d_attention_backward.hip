@@ -54,7 +54,6 @@ struct BackwardParams {
   int groups, heads, K, V, vtiles;
   uint32_t blocks;  // workgroups
   float scale;
-  bool split;
 };
 
 template <typename E, int C, int KP, int VT, int NW, bool TINY>
@@ -571,7 +570,6 @@ hipError_t launch_attention_backward(const AttentionBackwardArgs& a, const Atten
   p.vtiles = pl.vtiles;
   p.blocks = (uint32_t)(pl.slots * f.heads * pl.vtiles);
   p.scale = f.scale;
-  p.split = pl.split;
   if (f.dtype == 1)
     e = pl.vt == 64 ? launch_k<uint16_t, 64, 64, 4>(p, pl, f.stream) : launch_k<uint16_t, 64, 128, 8>(p, pl, f.stream);
   else

@@ -8,7 +8,7 @@
 // be left to the end.  That instruction adds its products in groups of eight, in
 // which it drops what lies below 2^-13 of the largest one (measured: beside 2^16,
 // 2^3 is kept and 2^2 is not; between groups 2^-7 is kept): about 1.5e-5 of a
-// block's sum for normal values, far under the output's rounding of 2^-9, but not
+// block's sum for normal values, far under the output's rounding of 2^-8, but not
 // good enough for an fp32 output.  There the values are converted to bf16, which
 // is exact, and a block is four v_mfma_f32_16x16x32_bf16 (1e-8), at half the rate.  Tiles are
 // formed transposed (rows n, columns m): a lane has one m, hence one product of

@@ -234,12 +234,15 @@ template <typename S, int THREADS, int NV>
 void launch_norm_t(const NormArgs& a) {
   const int per = block_threads(THREADS) / THREADS;
   const dim3 block(block_threads(THREADS)), grid = grid_of((a.rows + per - 1) / per, block.x);
-  if (a.scales)
-    rms_norm_kernel<S, THREADS, NV, true><<<grid, block, 0, a.stream>>>(
-        (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, a.scales, a.eps, a.rows, (int)a.dim);
-  else
-    rms_norm_kernel<S, THREADS, NV, false><<<grid, block, 0, a.stream>>>(
-        (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, nullptr, a.eps, a.rows, (int)a.dim);
+  if constexpr (THREADS >= 16) {  // a scale's threads
+    if (a.scales) {
+      rms_norm_kernel<S, THREADS, NV, true><<<grid, block, 0, a.stream>>>(
+          (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, a.scales, a.eps, a.rows, (int)a.dim);
+      return;
+    }
+  }
+  rms_norm_kernel<S, THREADS, NV, false><<<grid, block, 0, a.stream>>>(
+      (const S*)a.x, (const S*)a.residual, a.weight, (S*)a.residual_out, a.y, nullptr, a.eps, a.rows, (int)a.dim);
 }
 
 template <typename S>
@@ -264,49 +267,64 @@ hipError_t launch_norm_s(const NormArgs& a) {
   return hipGetLastError();
 }
 
+// The gradients' threads per row, each with `pieces` times eight channels, and their workgroups at most, each of one
+// row or of as many as a wave has groups of threads.  16 waves per CU (2048 channels with 8, 16 and 32 waves 75, 54 and
+// 58 us, 4096 channels 154, 110 and 112), 8 where a wave has whole rows (2^23 values in bf16, 8 against 16: rows of 64
+// 20.6 us and 23.3, of 512 21.6 and 25.1, of 59 26.9 and 26.6, of 414 29.1 and 28.4) and behind 8192 channels, whose
+// registers leave a CU one workgroup of eight (2048 rows of 16384 by 256, 512 and 1024 workgroups: bf16 70, 78 and 94
+// us, fp32 124, 122 and 141).
+struct BackwardShape {
+  int threads, pieces, most;
+  int64_t blocks(int64_t rows) const {  // no more than there are rows
+    const int per = threads < 64 ? 64 / threads : 1;
+    const int64_t all = (rows + per - 1) / per;
+    return all < most ? all : most;
+  }
+};
+BackwardShape backward_shape(int64_t dim) {
+  if (dim <= 64) return {8, 1, 2048};
+  if (dim <= 128) return {16, 1, 2048};
+  if (dim <= 256) return {32, 1, 2048};
+  if (dim <= 512) return {64, 1, 2048};
+  if (dim <= 2048) return {256, 1, 1024};
+  if (dim <= 4096) return {512, 1, 512};
+  if (dim <= 8192) return {1024, 1, 256};
+  return {512, 4, 256};
+}
+
 template <typename S, int THREADS, int NV>
-void launch_norm_backward_t(const NormBackwardArgs& a) {
-  rms_norm_backward_kernel<S, THREADS, NV><<<dim3((unsigned)norm_backward_blocks(a.rows, a.dim)),
-                                             dim3(THREADS < 64 ? 64 : THREADS), 0, a.stream>>>((const S*)a.r, a.weight, (const S*)a.dy,
-                                                         (const S*)a.dresidual, (S*)a.dx,
-                                                         a.dweight ? a.partial : nullptr, a.eps, a.rows, (int)a.dim);
+void launch_norm_backward_t(const NormBackwardArgs& a, int64_t blocks) {
+  rms_norm_backward_kernel<S, THREADS, NV><<<dim3((unsigned)blocks), dim3(THREADS < 64 ? 64 : THREADS), 0, a.stream>>>(
+      (const S*)a.r, a.weight, (const S*)a.dy, (const S*)a.dresidual, (S*)a.dx, a.dweight ? a.partial : nullptr, a.eps,
+      a.rows, (int)a.dim);
 }
 
 template <typename S>
 hipError_t launch_norm_backward_s(const NormBackwardArgs& a) {
-  if (a.dim <= 64)
-    launch_norm_backward_t<S, 8, 1>(a);
-  else if (a.dim <= 128)
-    launch_norm_backward_t<S, 16, 1>(a);
-  else if (a.dim <= 256)
-    launch_norm_backward_t<S, 32, 1>(a);
-  else if (a.dim <= 512)
-    launch_norm_backward_t<S, 64, 1>(a);
-  else if (a.dim <= 2048)
-    launch_norm_backward_t<S, 256, 1>(a);
-  else if (a.dim <= 4096)
-    launch_norm_backward_t<S, 512, 1>(a);
-  else if (a.dim <= 8192)
-    launch_norm_backward_t<S, 1024, 1>(a);
-  else
-    launch_norm_backward_t<S, 512, 4>(a);
+  const BackwardShape shape = backward_shape(a.dim);
+  const int64_t blocks = shape.blocks(a.rows);
+  switch (shape.threads) {
+    case 8: launch_norm_backward_t<S, 8, 1>(a, blocks); break;
+    case 16: launch_norm_backward_t<S, 16, 1>(a, blocks); break;
+    case 32: launch_norm_backward_t<S, 32, 1>(a, blocks); break;
+    case 64: launch_norm_backward_t<S, 64, 1>(a, blocks); break;
+    case 256: launch_norm_backward_t<S, 256, 1>(a, blocks); break;
+    case 1024: launch_norm_backward_t<S, 1024, 1>(a, blocks); break;
+    default:
+      if (shape.pieces == 1)
+        launch_norm_backward_t<S, 512, 1>(a, blocks);
+      else
+        launch_norm_backward_t<S, 512, 4>(a, blocks);
+  }
   if (a.dweight)
     norm_sum_partials<<<dim3((unsigned)((a.dim + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumRanges), 0, a.stream>>>(
-        a.partial, a.dweight, (int)norm_backward_blocks(a.rows, a.dim), (int)a.dim);
+        a.partial, a.dweight, (int)blocks, (int)a.dim);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t norm_backward_blocks(int64_t rows, int64_t dim) {
-  // 16 waves per CU (2048 channels with 8, 16 and 32 waves 75, 54 and 58 us, 4096 channels 154, 110 and 112), 8 where
-  // a wave has whole rows (2^23 values in bf16, 8 against 16: rows of 64 20.6 us and 23.3, of 512 21.6 and 25.1, of 59
-  // 26.9 and 26.6, of 414 29.1 and 28.4), and no more parts than rows
-  const int64_t want = dim <= 512 ? 256 * 8 : 256 * 16 / (dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16);
-  const int per = dim <= 64 ? 8 : dim <= 128 ? 4 : dim <= 256 ? 2 : 1;  // rows of a wave
-  const int64_t all = (rows + per - 1) / per;
-  return all < want ? all : want;
-}
+int64_t norm_backward_blocks(int64_t rows, int64_t dim) { return backward_shape(dim).blocks(rows); }
 
 hipError_t launch_rms_norm(const NormArgs& a) {
   return a.dtype == 1 ? launch_norm_s<uint16_t>(a) : launch_norm_s<float>(a);

@@ -35,7 +35,7 @@ struct NormBackwardArgs {
   const void* dresidual;  // or null
   void* dx;
   float* dweight;         // or null
-  float* partial;         // norm_backward_blocks(rows, dim, dtype) x dim, with dweight
+  float* partial;         // norm_backward_blocks(rows, dim) x dim, with dweight
   float eps;
   int64_t rows, dim;
   int dtype;
