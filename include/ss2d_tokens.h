@@ -58,7 +58,8 @@ typedef struct {
  *   q, k       [tokens, groups, key_dim]   dtype   strided as `sizes` says
  *   v          [tokens, heads, value_dim]  dtype   strided
  *   log_decay  [tokens, heads]             fp32    strided; g, usually <= 0.  Values
- *              under -104 (exp of them is 0 in fp32), -Inf too, count as a decay to 0.
+ *              under -104 (exp of them is 0 in fp32), -Inf too, count as a decay to 0;
+ *              sums over 88 within 64 tokens (exp of them is Inf) may give NaN.
  *   state_in   [sequences, heads, key_dim, value_dim] fp32, or NULL for 0
  *   cu_seqlens [sequences + 1] int32, or NULL: sequence s is the tokens
  *              cu_seqlens[s] .. cu_seqlens[s+1]-1 (none: an empty sequence, whose final
@@ -72,9 +73,14 @@ typedef struct {
  * Outputs must not overlap inputs otherwise (SS2D_ERR_ALIAS).  States, decays and
  * sums are fp32 (decays summed in fp64).  For bf16 the masked scores and the state
  * are rounded to bf16 for their products into o, whose own rounding is as large; what
- * the state itself is made of keeps all its bits.  NaN and Inf propagate: from a token to its sequence's outputs from up to 63 tokens before it on
- * (tokens are taken in chunks as matrix products).  Results do not depend on the
+ * the state itself is made of keeps all its bits.  NaN and Inf propagate: from a token to its
+ * sequence's outputs from up to 63 tokens before it on (tokens are taken in chunks as
+ * matrix products), so padding behind a sequence's end has to be finite, or left out
+ * by cu_seqlens.  Results do not depend on the
  * workspace, other sequences or streams: no atomics, sums in a fixed order.
+ * SS2D_ERR_SHAPE for sizes outside the ranges above, token strides of 2^24 and more,
+ * and over 2^30 tiles of 64 value columns of all heads and segments (a sequence has one
+ * or more) or blocks of 256 entries of all states.
  */
 int ss2d_linear_attention(const void* q, const void* k, const void* v, const float* log_decay,
                           const float* state_in, const int32_t* cu_seqlens, void* o, float* state_out,
@@ -143,7 +149,8 @@ int ss2d_linear_attention_step(const void* q, const void* k, const void* v, cons
  *   scales       [rows, ceil(dim/128)] fp32 or NULL: per 128 channels (the last block
  *                may be shorter) s = max(max|y| / 448, 2^-126), and the stored value is
  *                y / s rounded to nearest even; NaN stays NaN
- * y is formed from the unrounded fp32 sum.  rows >= 1, dim 1..16384; eps >= 0 and
+ * y is formed from the unrounded fp32 sum; squares are summed in fp32, so a row with
+ * values over 2^63 gives 0.  rows 1..2^31-1, dim 1..16384; eps >= 0 and
  * finite (SS2D_ERR_SHAPE otherwise).  One kernel, no workspace.
  */
 int ss2d_rms_norm(const void* x, const void* residual, const float* weight, float eps, void* residual_out, void* y,
@@ -173,11 +180,13 @@ int64_t ss2d_rms_norm_backward_workspace(int64_t rows, int64_t dim, int dtype);
  *   a         [m, k] e4m3         a_scales  [m, ceil(k/128)] fp32
  *   b         [n, k] e4m3         b_scales  [ceil(n/128), ceil(k/128)] fp32
  *   out       [m, n] dtype (fp32 or bf16, rounded once)
- * All dense; out must not overlap an input.  Sums are fp32 on the matrix cores, in a
+ * All dense; out must not overlap an input.  The two scales' product is formed in fp32
+ * (under 2^-126 it loses bits).  Sums are fp32 on the matrix cores, in a
  * fixed order.  For a bf16 output the products run in 8 bits, where the instruction
  * drops, in each group of eight inner indices, what lies below 2^-13 of the group's
  * largest product; for an fp32 output they run in bf16 (exact values), all bits kept.
- * m, n >= 1 and at most 2^30, k 1..2^20 (SS2D_ERR_SHAPE otherwise).  One kernel, no
+ * m, n 1..2^30, at most 2^31-1 tiles of 16 x 16 in out, k 1..2^20 (SS2D_ERR_SHAPE
+ * otherwise).  One kernel, no
  * workspace; any k and any addresses, fastest with k a multiple of 16 and a and b
  * aligned to 16 bytes.
  */

@@ -21,11 +21,12 @@
 // state from 0 and its whole decay, a carry turns these into the states before
 // the segments (ss2d_attention_state.hip), and the walk starts from them.
 //
-// 38144 packed tokens, 16 heads of 128 in bf16: the walk 231 us (2.7 TB/s, 173
-// TFLOP/s), with segments 312.  Bound by instruction issue and the latency between
+// 38144 packed tokens, 16 heads of 128 in bf16: the walk 227 to 243 us (240 in the
+// middle: 2.7 TB/s, 167 TFLOP/s), the call with segments 319.  Bound by instruction issue and the latency between
 // a chunk's barriers: vector instructions run in 35% of the busy cycles, LDS in 27%,
 // matrix products in 22%, and it takes as long without its loads.  Two workgroups
-// per CU: one with twice the LDS for two chunks took 271 us.
+// per CU: one with twice the LDS for two chunks took 271 us where two took 232.  In
+// the 256 registers of two the 128 x 128 bf16 instance spills 24 (52 bytes a lane).
 #include "ss2d_attention.h"
 
 namespace ss2d {

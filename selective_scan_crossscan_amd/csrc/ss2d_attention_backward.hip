@@ -25,9 +25,11 @@
 // parts through LDS at every chunk.  S, D and W are split over the waves, S M
 // and D M go through LDS.
 //
-// 2 x 4096 tokens, 16 heads of 128 in bf16: 174 us of 284 in all (123 TFLOP/s).
+// 2 x 4096 tokens, 16 heads of 128 in bf16: 180 us of 284 in all (119 TFLOP/s).
 // One workgroup of eight waves per CU (97 KiB of LDS, 256 registers), bound by the
-// latency of a chunk's phases, of which the registers leave no more to overlap.
+// latency of a chunk's phases, of which the registers leave no more to overlap: in
+// bf16 17 are spilled at 128 x 128 (72 bytes a lane), 4 at 64 x 128, 88 to 150 for
+// keys over 128 channels.
 //
 // Where several heads share keys and queries or the values take several tiles,
 // dq, dk (and dg) are written as fp32 parts and added in order by sum_parts.

@@ -13,10 +13,10 @@
 // it lies in registers, an operand whose inner index is v.  The decayed v (do) goes
 // into the product in parts that keep all of its bits.
 //
-// 38144 packed tokens, 16 heads of 128 in bf16: segment states 111 us, bound as the
-// walk that follows, their carry 18 us for 30 segments' 31 MB read and written in
-// order.  2 x 4096 tokens: states before all chunks 52 us (268 MB written, 5.1 TB/s),
-// both ways' segments 44 us, their carries 20 us.
+// 38144 packed tokens, 16 heads of 128 in bf16: segment states 116 us, bound as the
+// walk that follows, their carry 20 us for 30 segments' 31 MB read and written in
+// order.  2 x 4096 tokens: states before all chunks 54 us (268 MB written, 5.0 TB/s),
+// both ways' segments 45 us, their carries 20 us.
 #include <type_traits>
 
 #include "ss2d_attention.h"

@@ -5,8 +5,9 @@
 // and nothing else of that size), so one workgroup owns a tile of VT value
 // columns of one head, holds all its key rows in registers (16 bytes along the
 // value axis per thread and key row), and every load is issued before the first
-// is used.  192 rows of 16 heads of 128 x 128 take 95 us (4.3 TB/s) among states
-// that no cache holds, one row 4.2 us, the latency of its loads and stores.
+// is used.  192 rows of 16 heads of 128 x 128 take 94 us (4.3 TB/s) among states
+// that no cache holds, one row 5.4 us by itself and 4.2 after another in a graph, the
+// latency of its loads and stores.
 //
 // Rows of one slot are consecutive tokens: the workgroups of the first such row
 // run the later ones too, in order, on the state they hold; the others' leave.
@@ -177,7 +178,7 @@ hipError_t launch_step_s(const StepArgs& a) {
                a.q_row, a.k_row, a.v_row,   a.slots,      (int)a.rows,   (int)a.groups,  (int)a.heads,
                (int)a.key_dim,   (int)a.value_dim, 0,     a.scale};
   // Tiles of 16 columns spread a few rows over four times as many CUs, tiles of 64 read 256 bytes at once.  16 heads
-  // of 128 x 128, tiles of 16 against 64: one row 4.2 us (5.0), two 4.9 (5.1), four 6.9 (5.8), 192 134 (95).
+  // of 128 x 128, one launch after another in a graph, tiles of 16 against 64: one row 4.2 us (5.0), two 4.9 (5.1), four 6.9 (5.8), 192 134 (95).
   if (a.rows * a.heads * ((a.value_dim + 63) / 64) < 128)
     launch_step_v<S, 16>(a, p);
   else

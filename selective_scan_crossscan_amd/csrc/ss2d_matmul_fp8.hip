@@ -17,11 +17,11 @@
 // by four quarters of a block, in both operands alike.
 //
 // Two kernels.  Products with enough outputs for tiles of 128x128 stage both
-// operands through LDS, double buffered (5001 x 4096 x 4096: 101 us, 1661
-// TFLOP/s).  Fewer are bound by reading b once: there a workgroup's waves split
+// operands through LDS, double buffered (5001 x 4096 x 4096: 102 us among
+// other calls, 1646 TFLOP/s; 107 to 118 by itself).  Fewer are bound by reading b once: there a workgroup's waves split
 // the inner dimension over one strip of 16 n, each streaming its part of b from
 // global memory straight into fragments, and add their sums through LDS in a
-// fixed order (3 x 6144 x 4096: 8.6 us, 2.9 TB/s).
+// fixed order (3 x 6144 x 4096: 8.4 us, 3.0 TB/s).
 #include "ss2d_token_ops.h"
 
 namespace ss2d {

@@ -13,10 +13,12 @@
 // and 16 behind (the gradients' eight, with registers for four times eight channels:
 // 16 waves spilled, 113 us against 71 for 2048 rows of 16384), which also keeps a single row's latency at one load, one sum and one
 // store.  The sums are fp32.
-// 16384 rows of 2048 in bf16 with a residual: 42 us, 6.3 TB/s (part of it from the
-// last-level cache); the gradients 54 us, 5.0 TB/s.
+// 16384 rows of 2048 in bf16 with a residual: 47 us on inputs that change from call to
+// call, 5.8 TB/s; 38 on the same ones, part of which the last-level cache holds.  The
+// gradients 58 us, 4.6 TB/s, and 53.
 //
-// Threads per row, us for 4 and 16384 rows (bf16 with a residual): 512 channels
+// Threads per row, us for 4 and 16384 rows (bf16 with a residual, one launch after another in a graph, four sets of
+// inputs): 512 channels
 // 64 threads 2.6, 12.1, 256 threads 2.9, 21.4; 1024 channels 64 4.2, 25.4, 256
 // 2.7, 25.6; 2048 channels 64 4.2, 49.9, 256 2.8, 42.3, 512 2.9, 54.1; 4096
 // channels 256 3.3, 98, 512 3.0, 92, 1024 3.3, 116; 8192 channels 512 3.6, 191,

@@ -146,6 +146,7 @@ def linear_attention(q, k, v, log_decay, state=None, cu_seqlens=None, scale: flo
     With cu_seqlens (S+1,) int32 on the device the sequences are packed: q, k (T,G,K), v (T,H,V), log_decay (T,H),
     sequence s being tokens cu_seqlens[s]..cu_seqlens[s+1]-1; outputs of tokens in no sequence are left as they were.
     Any strides with a dense last axis (slices of one projection's output, expanded decays); K <= 256, V <= 1024.
+    A padded batch's padding has to be finite: tokens are taken in chunks, in which NaN reaches the ones before it.
     state (S,H,K,V) float32: the states to start from (None: 0).
     Returns o (v's shape, contiguous), and with final_state also the states after the last tokens (S,H,K,V) float32.
     """
