@@ -54,7 +54,7 @@ constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 int check_norm(const void* x, const void* y, const float* weight, float eps, int64_t rows, int64_t dim, int dtype) {
   if (!x || !y) return SS2D_ERR_NULL;
   if (rows < 1 || rows > kMaxRows || dim < 1 || dim > ss2d::kMaxNormDim) return SS2D_ERR_SHAPE;
-  if (!(eps >= 0.f && eps <= 1e30f)) return SS2D_ERR_SHAPE;  // also rejects NaN
+  if (!(eps >= 0.f && eps < __builtin_inff())) return SS2D_ERR_SHAPE;  // also rejects NaN
   if (!dtype_ok(dtype)) return SS2D_ERR_DTYPE;
   if (misaligned(weight, 4)) return SS2D_ERR_ALIGN;
   return SS2D_OK;

@@ -282,3 +282,9 @@ def test_everything_imports_with_and_without_torch(torch_there):
             + "from selective_scan_crossscan_amd import *\nassert version() > 0 and ss2d_forward\n"
             + f"assert ('rms_norm' in dir()) == {torch_there}")
     subprocess.check_call([sys.executable, "-c", code], cwd=ROOT)
+
+
+@needs_no_device
+def test_norm_takes_any_finite_eps():
+    for eps in (0.0, 2e30, 3.4e38):
+        assert norm(eps=eps) == NO_DEVICE and norm_backward(eps=eps) == NO_DEVICE
