@@ -17,20 +17,21 @@ __all__ = ["forward", "ss2d_forward", "project", "ss2d_project", "forward_from_x
            "channel_last", "ss2d_channel_last", "backward", "ss2d_backward", "measure_peaks", "describe", "bidir_forward", "ss2d_bidir_forward", "bidir_backward", "ss2d_bidir_backward", "ss2d_forward_noalloc", "trim_memory", "status_string", "version", "library_path", "lib",
            "SS2D_F32", "SS2D_BF16", "SS2DError"]
 
-# The token-sequence operators (tokens.py), imported with torch when first used; without torch the rest of the package
-# works on raw addresses, `from ... import *` too.
+# The token-sequence operators (tokens.py, delta.py), imported with torch when first used; without torch the rest of the
+# package works on raw addresses, `from ... import *` too.
+_DELTA = ("delta_rule", "delta_rule_backward", "delta_rule_step", "qk_norm", "qk_norm_backward", "rotation_table")
 _TOKENS = ("linear_attention", "linear_attention_backward", "linear_attention_step", "rms_norm",
-           "rms_norm_fp8", "rms_norm_backward", "matmul_fp8")
+           "rms_norm_fp8", "rms_norm_backward", "matmul_fp8") + _DELTA
 if importlib.util.find_spec("torch") is not None:
     __all__ += _TOKENS
 
 
 def __getattr__(name):
     if name in _TOKENS:
-        from . import tokens
+        from . import delta, tokens
 
         # kept, so that later calls find it without coming here (0.4 us of a single token's 10)
-        return globals().setdefault(name, getattr(tokens, name))
+        return globals().setdefault(name, getattr(delta if name in _DELTA else tokens, name))
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -17,7 +17,8 @@ SOURCES = ["ss2d_api.hip", "ss2d_plan.hip", "ss2d_f32_t16.hip", "ss2d_f32_t8.hip
            "ss2d_bf16_t8.hip", "ss2d_peaks.hip", "ss2d_project.hip",
            "ss2d_epilogue.hip", "ss2d_backward.hip", "ss2d_tokens_api.hip", "ss2d_norm.hip",
            "ss2d_attention_step.hip", "ss2d_attention.hip", "ss2d_attention_state.hip",
-           "ss2d_attention_backward.hip", "ss2d_matmul_fp8.hip"]
+           "ss2d_attention_backward.hip", "ss2d_matmul_fp8.hip", "ss2d_delta_api.hip", "ss2d_delta_systems.hip",
+           "ss2d_delta.hip", "ss2d_delta_backward.hip", "ss2d_delta_step.hip", "ss2d_qk_norm.hip"]
 
 # -packed-fp32-ops: no packed FP32 instructions are generated (plain VALU only).
 HIPCC_FLAGS = [

@@ -95,6 +95,22 @@ def lib():
             L.ss2d_rms_norm_backward.restype = ci
             L.ss2d_rms_norm_backward_workspace.argtypes = [i64, i64, ci]
             L.ss2d_rms_norm_backward_workspace.restype = i64
+            L.ss2d_delta_rule.argtypes = [vp] * 9 + [sizes, f32, ci, vp, i64, vp]
+            L.ss2d_delta_rule.restype = ci
+            L.ss2d_delta_rule_workspace.argtypes = [sizes, ci, ci]
+            L.ss2d_delta_rule_workspace.restype = i64
+            L.ss2d_delta_rule_backward.argtypes = [vp] * 15 + [sizes, f32, ci, vp, i64, vp]
+            L.ss2d_delta_rule_backward.restype = ci
+            L.ss2d_delta_rule_backward_workspace.argtypes = [sizes, ci, ci]
+            L.ss2d_delta_rule_backward_workspace.restype = i64
+            L.ss2d_delta_rule_step.argtypes = [vp] * 8 + [i64] * 9 + [f32, ci, vp]
+            L.ss2d_delta_rule_step.restype = ci
+            L.ss2d_qk_norm.argtypes = [vp] * 8 + [sizes, f32, ci, ci, vp]
+            L.ss2d_qk_norm.restype = ci
+            L.ss2d_qk_norm_backward.argtypes = [vp] * 12 + [sizes, f32, ci, ci, vp, i64, vp]
+            L.ss2d_qk_norm_backward.restype = ci
+            L.ss2d_qk_norm_backward_workspace.argtypes = [sizes, ci]
+            L.ss2d_qk_norm_backward_workspace.restype = i64
             _lib = L
     return _lib
 

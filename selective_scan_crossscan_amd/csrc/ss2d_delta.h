@@ -1,0 +1,183 @@
+// The gated delta rule over prompts: what its forward (ss2d_delta.hip) and its
+// gradients (ss2d_delta_backward.hip) share.
+//
+//   h_t = a_t h_{t-1} + b_t k_t (v_t - a_t h_{t-1}' k_t)',   o_t = scale h_t' q_t,
+// a = exp(g), b = beta.  In chunks of C tokens, with G the sum of g inside the chunk up
+// to a token, H the state before the chunk, L_ij = exp(G_i - G_j) k_i . k_j for j < i
+// and P_ij = scale exp(G_i - G_j) q_i . k_j for j <= i (both 0 otherwise):
+//   E = (1 + L diag(b))^-1 (V - exp(G) K H)     the tokens' errors v - a h' k
+//   U = b E,   o = scale exp(G) Q H + P U,   H <- exp(G_last) H + K' (w U),
+// w_j = exp(G_last - G_j): with U known, linear attention whose values are U.  What does
+// not depend on the state, the inverse and P, is formed for all chunks at once before
+// (delta_systems); the walk over the chunks is left with products only.
+//
+// Fragments, parts and tiles are ss2d_attention.h's.  The state is kept as result tiles
+// with rows k and columns v, E and U with rows token and columns v: each then lies in
+// registers as the next product's operand (K H sums over k, the inverse and K' U over
+// tokens), so a wave that owns value columns needs nothing from other waves.
+#pragma once
+
+#include "ss2d_attention.h"
+
+namespace ss2d {
+
+// Sizes of a chunk's systems in memory: fragments in the order of their tiles, those
+// of a triangle's 16-row tiles x by pairs of 16-column tiles.
+template <typename E, int C>
+struct Systems {
+  static constexpr int NI = C / 16;
+  static constexpr int kFrags = NI / 2 * (NI / 2 + 1);
+  static constexpr int kParts = sizeof(E) == 2 ? 3 : 1;
+  static constexpr int kFragBytes = 64 * 8 * (int)sizeof(E);
+  static constexpr int kInverse = kFrags * kParts * kFragBytes;  // all parts
+  static constexpr int kScores = kFrags * kFragBytes;            // one part: the forward's P
+  // Rows i, columns j <= i: tile row x has the pairs 0 .. x / 2.
+  static __host__ __device__ constexpr int lower(int x, int pair) { return (x / 2) * (x / 2 + 1) + (x & 1) * (x / 2 + 1) + pair; }
+  // Rows j, columns i >= j: tile row x has the pairs x / 2 .. NI / 2 - 1; the mirror image.
+  static __host__ __device__ constexpr int upper(int x, int pair) { return lower(NI - 1 - x, NI / 2 - 1 - pair); }
+};
+
+struct DeltaArgs {
+  AttentionArgs f;  // as linear attention's
+  const float* beta;
+  int64_t beta_stride[3];
+};
+
+struct DeltaPlan {
+  AttentionPlan a;      // kp, chunk, segments, slots, chunks; vt the walk's
+  bool backward;
+};
+DeltaPlan plan_delta(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
+                     int dtype);
+DeltaPlan plan_delta_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
+                              bool packed, int dtype);
+size_t delta_workspace_bytes(const DeltaPlan& pl, int64_t heads, int64_t key_dim, int64_t value_dim, int dtype);
+hipError_t launch_delta(const DeltaArgs& a, const DeltaPlan& pl);
+
+struct DeltaBackwardArgs {
+  DeltaArgs d;  // the forward's inputs; workspace, stream
+  const void* d_o;
+  int64_t do_stride[3];
+  const float* dstate_out;  // or null
+  void *dq, *dk, *dv;
+  float *dlog_decay, *dbeta;
+  float* dstate_in;  // or null
+};
+size_t delta_backward_workspace_bytes(const DeltaPlan& pl, int64_t tokens, int64_t groups, int64_t heads,
+                                      int64_t key_dim, int64_t value_dim, int dtype);
+hipError_t launch_delta_backward(const DeltaBackwardArgs& a, const DeltaPlan& pl);
+
+// Workgroups of the largest grid a plan launches.
+int64_t delta_blocks(const DeltaPlan& pl, int64_t sequences, int64_t heads, int64_t value_dim);
+
+struct DeltaStepArgs {
+  StepArgs s;
+  const float* beta;
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a);
+
+// ------------------------------------------------------------------ passes
+struct DeltaParams {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const float* state_in;    // or null
+  void* o;
+  float* state_out;         // or null
+  char* systems;            // (chunk, head): inverse, scores; backward: inverse, transposed inverse and scores
+  float* seg_state;         // (slot, head, K, V): what a segment adds, after the carry the state before it
+  float* seg_map;           // (slot, head, KP, KP): the segment's map of the state before it
+  float* chunk_state;       // (chunk, head, K, V): the state before every chunk
+  float* errors;            // (token, head, V)
+  SequenceMap map;          // segments
+  SequenceMap chunk_map;    // segments of one chunk
+  int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], b_stride[3];
+  int groups, heads, K, V, vtiles, ktiles;  // tiles of the pass's columns of values; of the segment maps' columns
+  uint32_t blocks;
+  float scale;
+  bool split;               // segments start from seg_state
+  bool last_maps;           // segment maps of the sequences' last segments too, for the way back
+  int64_t system_stride;    // bytes of a chunk's and head's systems
+};
+DeltaParams delta_params(const DeltaArgs& a, const DeltaPlan& pl);
+// The systems of all chunks.
+hipError_t launch_delta_systems(const DeltaParams& p, const DeltaPlan& pl, int dtype, hipStream_t st);
+// seg_state and seg_map of all segments but their sequence's last, then seg_state as the states before all of them.
+hipError_t launch_delta_segments(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st);
+// chunk_state and errors.
+hipError_t launch_delta_states(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st);
+// seg: what segments add to the state (to the gradient behind them, in reverse) to the states before (behind) them.
+struct CarryParams {
+  float* seg;            // (slot, head, K, V)
+  const float* seg_map;  // (slot, head, KP, KP)
+  const float* from;     // (sequence, head, K, V) or null
+  SequenceMap map;
+  int heads, K, V, vtiles;
+  uint32_t blocks;
+};
+hipError_t launch_delta_carry(CarryParams p, const DeltaPlan& pl, bool reverse, hipStream_t st);
+// Bytes of one chunk's and head's systems.
+int64_t system_bytes(const DeltaPlan& pl, int dtype);
+
+namespace tok {
+
+// Sum over parts of a fragment product whose operands both come in parts, the smallest first.
+template <int N, typename E>
+__device__ __forceinline__ f32x4 mma_parts(const Frag<E> (&a)[N], const Frag<E> (&b)[N], f32x4 c) {
+  // parts p and q of a 24-bit value each: those with p + q >= N lie under its last bit
+#pragma unroll
+  for (int s = N - 1; s >= 0; --s)
+#pragma unroll
+    for (int p = 0; p <= s; ++p) c = mma(a[p], b[s - p], c);
+  return c;
+}
+
+// A lane's fragment at `at` of a chunk's systems.
+template <typename E>
+__device__ __forceinline__ Frag<E> system_frag(const char* at) {
+  Frag<E> f;
+  __builtin_memcpy(&f, __builtin_assume_aligned(at + (threadIdx.x & 63) * (8 * sizeof(E)), 16), sizeof(f));
+  return f;
+}
+
+// Four consecutive elements of a row of which the first n are there (the others are 0).
+__device__ __forceinline__ f32x4 load4(const float* p, int n) {
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  if (n >= 4) {
+    const Bytes16 w = *reinterpret_cast<const Bytes16*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) x[i] = p[i];
+  }
+  return x;
+}
+__device__ __forceinline__ f32x4 load4(const uint16_t* p, int n) {
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  if (n >= 4) {
+    const Bytes8 w = *reinterpret_cast<const Bytes8*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = bf16_bits_to_f32(w.w[i] & 0xffffu);
+      x[2 * i + 1] = __uint_as_float(w.w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) x[i] = load1(p + i);
+  }
+  return x;
+}
+
+// Two result tiles stacked along their rows as the eight inner values of an operand.
+__device__ __forceinline__ void stack(const f32x4& a, const f32x4& b, float (&u)[8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    u[r] = a[r];
+    u[4 + r] = b[r];
+  }
+}
+
+}  // namespace tok
+}  // namespace ss2d
