@@ -42,8 +42,8 @@ typedef struct {
  * Outputs must not overlap inputs, but state_out may be state_in itself
  * (SS2D_ERR_ALIAS).  States, decays, sums and the triangular systems of 64 tokens
  * (32 in fp32) are fp32, decays summed in fp64.  For bf16 an output takes the masked
- * scores, the state and the replaced values rounded to bf16 once each, its own rounding
- * being as large; what the state itself is made of keeps all its bits.  NaN and Inf
+ * scores and the state rounded to bf16 once, its own rounding being as large; what the
+ * state itself is made of keeps all its bits.  NaN and Inf
  * propagate: from a token to its sequence's outputs from up to 63 tokens before it on,
  * so padding behind a sequence's end has to be finite, or left out by cu_seqlens.
  * Results do not depend on the workspace, other sequences or streams.
@@ -73,9 +73,9 @@ int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int
  *                       value, the gradient of each of its uses)
  *           dstate_in   [sequences, heads, key_dim, value_dim] fp32 or NULL
  * Outputs are overwritten, not added to; tokens outside the sequences keep what they
- * were.  Outputs must not overlap inputs or each other.  For bf16 dq and dk take the
- * states, their gradients, the masked products and the replaced values rounded to bf16
- * once each; the other outputs keep all bits up to their own rounding.
+ * were.  Outputs must not overlap inputs or each other.  For bf16 dk takes the states,
+ * their gradients and the masked products rounded to bf16 once each; the other outputs
+ * keep all bits up to their own rounding.
  */
 int ss2d_delta_rule_backward(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
                              const float* state_in, const int32_t* cu_seqlens, const void* d_o,

@@ -27,10 +27,13 @@ template <typename E, int C>
 struct Systems {
   static constexpr int NI = C / 16;
   static constexpr int kFrags = NI / 2 * (NI / 2 + 1);
-  static constexpr int kParts = sizeof(E) == 2 ? 3 : 1;
+  static constexpr int kParts = sizeof(E) == 2 ? 2 : 1;       // of an inverse without its diagonal of ones
+  static constexpr int kScoreParts = sizeof(E) == 2 ? 3 : 1;  // of the gradients' P'
   static constexpr int kFragBytes = 64 * 8 * (int)sizeof(E);
-  static constexpr int kInverse = kFrags * kParts * kFragBytes;  // all parts
-  static constexpr int kScores = kFrags * kFragBytes;            // one part: the forward's P
+  static constexpr int kInverse = kFrags * kParts * kFragBytes;
+  static constexpr int kScores = kFrags * kFragBytes;  // one part: the forward's P
+  static constexpr int kForward = kInverse + kScores;
+  static constexpr int kBackward = 2 * kInverse + kScoreParts * kScores;
   // Rows i, columns j <= i: tile row x has the pairs 0 .. x / 2.
   static __host__ __device__ constexpr int lower(int x, int pair) { return (x / 2) * (x / 2 + 1) + (x & 1) * (x / 2 + 1) + pair; }
   // Rows j, columns i >= j: tile row x has the pairs x / 2 .. NI / 2 - 1; the mirror image.
@@ -92,7 +95,7 @@ struct DeltaParams {
   SequenceMap chunk_map;    // segments of one chunk
   int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], b_stride[3];
   int groups, heads, K, V, vtiles, ktiles;  // tiles of the pass's columns of values; of the segment maps' columns
-  uint32_t blocks;
+  uint32_t blocks;          // workgroups; of a walk: units of a segment and head, each with its tiles
   float scale;
   bool split;               // segments start from seg_state
   bool last_maps;           // segment maps of the sequences' last segments too, for the way back
@@ -120,15 +123,47 @@ int64_t system_bytes(const DeltaPlan& pl, int dtype);
 
 namespace tok {
 
-// Sum over parts of a fragment product whose operands both come in parts, the smallest first.
-template <int N, typename E>
-__device__ __forceinline__ f32x4 mma_parts(const Frag<E> (&a)[N], const Frag<E> (&b)[N], f32x4 c) {
-  // parts p and q of a 24-bit value each: those with p + q >= N lie under its last bit
+// c[x] += a[x] b for x in from .. to - 1, both operands in parts: those whose share of the product lies under the last
+// part's (p + q >= N) are left out, the smallest come first, and products of different x stand next to each other.
+template <int FROM, int TO, int N, int M, typename E>
+__device__ __forceinline__ void mma_parts(const Frag<E> (&a)[M][N], const Frag<E> (&b)[N], f32x4 (&c)[M]) {
 #pragma unroll
   for (int s = N - 1; s >= 0; --s)
 #pragma unroll
-    for (int p = 0; p <= s; ++p) c = mma(a[p], b[s - p], c);
-  return c;
+    for (int p = 0; p <= s; ++p)
+#pragma unroll
+      for (int x = FROM; x < TO; ++x) c[x] = mma(a[x][p], b[s - p], c[x]);
+}
+
+// What a chunk's cumulative decays G give for each of its tokens.
+template <int C>
+struct Rates {
+  __attribute__((aligned(16))) float since[C], left[C], beta[C];  // exp(G), exp(G_last - G)
+  __device__ __forceinline__ static f32x4 four(const float* x) { return *reinterpret_cast<const f32x4*>(x); }
+};
+// One wave: lane t holds token t's log decay and beta (0 behind the end).
+template <int C>
+__device__ __forceinline__ void scan_rates(float g, float beta, Rates<C>& m) {
+  const int lane = threadIdx.x & 63;
+  const double s = wave_scan((double)clamp_log_decay(g) * 1.4426950408889634074);
+  const double last = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(s), C - 1),
+                                       __builtin_amdgcn_readlane(__double2loint(s), C - 1));
+  if (lane < C) {
+    m.since[lane] = __builtin_amdgcn_exp2f((float)s);
+    m.left[lane] = __builtin_amdgcn_exp2f((float)(last - s));
+    m.beta[lane] = beta;
+  }
+}
+
+// Workgroups go round the eight XCDs, each with an L2 of its own: a unit's tiles are eight workgroups apart, on one XCD at
+// about the same time, so that what they share is read from memory once.  False behind the last unit.
+constexpr uint32_t kXcds = 8;
+__host__ __device__ constexpr int64_t spread_blocks(int64_t units, int tiles) { return (units + kXcds - 1) / kXcds * kXcds * tiles; }
+__device__ __forceinline__ bool spread(uint32_t block, uint32_t units, uint32_t tiles, uint32_t& unit, uint32_t& tile) {
+  const uint32_t round = block / (kXcds * tiles), rest = block - round * (kXcds * tiles);
+  tile = rest / kXcds;
+  unit = round * kXcds + rest % kXcds;
+  return unit < units;
 }
 
 // A lane's fragment at `at` of a chunk's systems.

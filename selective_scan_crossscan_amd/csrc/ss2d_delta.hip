@@ -17,27 +17,28 @@ namespace {
 
 using namespace tok;
 
+constexpr int kCarryColumns = 32;
+
 enum DeltaPass { kOutputs, kSegments, kStates };
 
 template <typename E, int C, int KP, int VT, int NV, DeltaPass PASS, bool TINY>
 __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
   constexpr int NW = VT / 16 / NV, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   using S = Systems<E, C>;
-  constexpr int kSystem = PASS == kOutputs ? S::kInverse + S::kScores : S::kInverse;  // bytes read per chunk
+  constexpr int PN = S::kParts;
+  constexpr int kSystem = PASS == kOutputs ? S::kForward : S::kInverse;  // bytes read per chunk
   constexpr int kPieces = (kSystem / 16 + THREADS - 1) / THREADS;
   __shared__ Tile<E, PASS == kOutputs ? C : 1, KP> qs;
-  __shared__ Tile<E, C, KP, 32> ks;
+  __shared__ Tile<E, C, KP, 16> ks;
   __shared__ Tile<E, C, VT, 32> vs;
   __shared__ __attribute__((aligned(16))) char sys[kSystem];
-  __shared__ Decays<C> dec;
-  __shared__ __attribute__((aligned(16))) float bs[C];
+  __shared__ Rates<C> rates;
 
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const uint32_t block = (uint32_t)block_id();
-  if (block >= p.blocks) return;
-  const int tiles = PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles;
-  const int tile = block % tiles, head = block / tiles % p.heads;
-  const int64_t slot = block / (tiles * p.heads);
+  uint32_t unit, at_tile;
+  if (!spread((uint32_t)block_id(), p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles, unit, at_tile)) return;
+  const int tile = at_tile, head = unit % p.heads;
+  const int64_t slot = unit / p.heads;
   Segment seg;
   if (!find_segment(p.map, slot, seg)) return;
   const bool map = PASS == kSegments && tile >= p.vtiles;  // columns of the identity instead of values
@@ -58,7 +59,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
 
   struct Chunk {
     TileLoad<E, PASS == kOutputs ? C : 1, KP, 16, THREADS, TINY> q;
-    TileLoad<E, C, KP, 32, THREADS, TINY> k;
+    TileLoad<E, C, KP, 16, THREADS, TINY> k;
     TileLoad<E, C, VT, 32, THREADS, TINY> v;
     uint4 s[kPieces];
     float g, b;
@@ -85,10 +86,7 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
     for (int i = 0; i < kPieces; ++i)
       if (kSystem / 16 % THREADS == 0 || threadIdx.x + i * THREADS < kSystem / 16)
         *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
-    if (wave == 0) {
-      scan_decays<C>(lane < n ? x.g : 0.f, dec);
-      if (lane < C) bs[lane] = lane < n ? x.b : 0.f;
-    }
+    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
   };
   Chunk first;  // on its way while the state is read
   if (seg.begin < seg.end) fetch(first, seg.begin);
@@ -155,56 +153,63 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
           stack(h[c][t], h[c + 1][t], u);
           split_parts(u, b[t]);
         }
+        Frag<E> k[NI];
 #pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const Frag<E> k = frag_row_split(ks, x * 16 + l, c * 16);
+        for (int x = 0; x < NI; ++x) k[x] = frag_row_split(ks, x * 16 + l, c * 16);
 #pragma unroll
-          for (int q = PF - 1; q >= 0; --q)
+        for (int q = PF - 1; q >= 0; --q)  // independent products next to each other
 #pragma unroll
-            for (int t = 0; t < NV; ++t) z[x][t] = mma(k, b[t][q], z[x][t]);
-          if (PASS == kOutputs) {
+          for (int x = 0; x < NI; ++x)
+#pragma unroll
+            for (int t = 0; t < NV; ++t) z[x][t] = mma(k[x], b[t][q], z[x][t]);
+        if (PASS == kOutputs)
+#pragma unroll
+          for (int x = 0; x < NI; ++x) {
             const Frag<E> f = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
             for (int t = 0; t < NV; ++t) o[t][x] = mma(b[t][0], f, o[t][x]);
           }
-        }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (PASS == kOutputs)
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
-          const float f = p.scale * __builtin_amdgcn_exp2f(dec.whole[x * 16 + l] + dec.frac[x * 16 + l]);
+          const float f = p.scale * rates.since[x * 16 + l];
 #pragma unroll
           for (int t = 0; t < NV; ++t) o[t][x] *= f;
         }
-      // the errors: the inverse by V - exp(G) K h
-      f32x4 e[NI][NV];
-#pragma unroll
-      for (int x = 0; x < NI; ++x)
-#pragma unroll
-        for (int t = 0; t < NV; ++t) e[x][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // the errors E = Z + N Z, Z = V - exp(G) K h
+      f32x4 e[NV][NI];
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        Frag<E> b[NV][PF];
-        const f32x4 f0 = dec.since4(j * 16 + 4 * g), f1 = dec.since4(j * 16 + 16 + 4 * g);
+        const f32x4 f0 = rates.four(&rates.since[j * 16 + 4 * g]), f1 = rates.four(&rates.since[j * 16 + 16 + 4 * g]);
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
           float u[8];
           frag_values(frag_col_split(vs, j * 16, vw + t * 16), u);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            u[r] = fmaf(-f0[r], z[j][t][r], u[r]);
-            u[4 + r] = fmaf(-f1[r], z[j + 1][t][r], u[4 + r]);
+            z[j][t][r] = fmaf(-f0[r], z[j][t][r], u[r]);
+            z[j + 1][t][r] = fmaf(-f1[r], z[j + 1][t][r], u[4 + r]);
           }
-          split_parts(u, b[t]);
+          e[t][j] = z[j][t];
+          e[t][j + 1] = z[j + 1][t];
         }
+      }
 #pragma unroll
-        for (int x = j; x < NI; ++x) {
-          Frag<E> a[PF];
+      for (int j = 0; j < NI; j += 2) {
+        Frag<E> a[NI][PN];
 #pragma unroll
-          for (int q = 0; q < PF; ++q) a[q] = system_frag<E>(sys + (S::lower(x, j / 2) * PF + q) * S::kFragBytes);
+        for (int x = j; x < NI; ++x)
 #pragma unroll
-          for (int t = 0; t < NV; ++t) e[x][t] = mma_parts(a, b[t], e[x][t]);
+          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys + (S::lower(x, j / 2) * PN + q) * S::kFragBytes);
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          float u[8];
+          Frag<E> b[PN];
+          stack(z[j][t], z[j + 1][t], u);
+          split_parts(u, b);
+          j == 0 ? mma_parts<0, NI>(a, b, e[t]) : mma_parts<2, NI>(a, b, e[t]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -217,38 +222,42 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int i = x * 16 + 4 * g + r, v = vw + t * 16 + l;
-              if (i < n && v < nv) to[(uint32_t)i * (uint32_t)(p.heads * p.V) + v] = e[x][t][r];
+              if (i < n && v < nv) to[(uint32_t)i * (uint32_t)(p.heads * p.V) + v] = e[t][x][r];
             }
       }
       // U = b E; P U to the outputs, K' (w U) to the state
 #pragma unroll
       for (int x = 0; x < NI; ++x) {
-        const f32x4 b = *reinterpret_cast<const f32x4*>(&bs[x * 16 + 4 * g]);
+        const f32x4 b = rates.four(&rates.beta[x * 16 + 4 * g]);
 #pragma unroll
-        for (int t = 0; t < NV; ++t) e[x][t] *= b;
+        for (int t = 0; t < NV; ++t) e[t][x] *= b;
       }
       if (PASS == kOutputs) {
 #pragma unroll
         for (int j = 0; j < NI; j += 2) {
-          Frag<E> a[NV][1];
+          // two parts: the scores and the state are rounded once, and so is all that an output is made of
+          constexpr int PU = PF > 1 ? 2 : 1;
+          Frag<E> a[NV][PU];
 #pragma unroll
           for (int t = 0; t < NV; ++t) {
             float u[8];
-            stack(e[j][t], e[j + 1][t], u);
+            stack(e[t][j], e[t][j + 1], u);
             split_parts(u, a[t]);
           }
 #pragma unroll
           for (int x = j; x < NI; ++x) {
             const Frag<E> s = system_frag<E>(sys + S::kInverse + S::lower(x, j / 2) * S::kFragBytes);
 #pragma unroll
-            for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][0], s, o[t][x]);
+            for (int q = PU - 1; q >= 0; --q)
+#pragma unroll
+              for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], s, o[t][x]);
           }
         }
         E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
         put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
         __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
       }
-      const float all = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
+      const float all = rates.since[C - 1];
 #pragma unroll
       for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
@@ -256,20 +265,23 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
         Frag<E> b[NV][PF];
-        const f32x4 w0 = dec.between4(C - 1, j * 16 + 4 * g), w1 = dec.between4(C - 1, j * 16 + 16 + 4 * g);
+        const f32x4 w0 = rates.four(&rates.left[j * 16 + 4 * g]), w1 = rates.four(&rates.left[j * 16 + 16 + 4 * g]);
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
           float u[8];
-          stack(e[j][t] * w0, e[j + 1][t] * w1, u);
+          stack(e[t][j] * w0, e[t][j + 1] * w1, u);
           split_parts(u, b[t]);
         }
 #pragma unroll
-        for (int kt = 0; kt < NK; ++kt) {
-          const Frag<E> k = frag_col_split(ks, j * 16, kt * 16);
+        for (int kt = 0; kt < NK; kt += 2) {
+          const Frag<E> k0 = frag_col_split(ks, j * 16, kt * 16), k1 = frag_col_split(ks, j * 16, kt * 16 + 16);
 #pragma unroll
           for (int q = PF - 1; q >= 0; --q)
 #pragma unroll
-            for (int t = 0; t < NV; ++t) h[kt][t] = mma(k, b[t][q], h[kt][t]);
+            for (int t = 0; t < NV; ++t) {
+              h[kt][t] = mma(k0, b[t][q], h[kt][t]);
+              h[kt + 1][t] = mma(k1, b[t][q], h[kt + 1][t]);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -294,12 +306,15 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
   }
 }
 
-// One workgroup carries 64 value columns of a head along its sequence's segments, 16 per wave: h <- M h + u forwards,
-// h <- M' h + u backwards, h before (behind) each segment in the place of its u.  The first one's too: the last
-// segment's workgroup may write the final state over the initial one before the first has begun.
+// One workgroup carries 32 value columns of a head along its sequence's segments: h <- M h + u forwards, h <- M' h + u
+// backwards, h before (behind) each segment in the place of its u.  The first one's too: the last segment's workgroup may
+// write the final state over the initial one before the first has begun.  A wave owns 16 (at 256 keys 32) rows of the
+// result and reads those of M alone, the next segment's while this one's are multiplied; h goes round through LDS as
+// fragments in parts.  (With 16 columns per wave and all of M read by each, a step took 10 us where it takes 2.)
 template <int KP, bool REVERSE>
-__global__ __launch_bounds__(256) void delta_carry(CarryParams p) {
-  constexpr int NK = KP / 16, PF = 3;
+__global__ __launch_bounds__(KP == 256 ? 512 : KP * 4) void delta_carry(CarryParams p) {
+  constexpr int NK = KP / 16, NW = NK < 8 ? NK : 8, OWN = NK / NW, NC = KP / 32, NV = kCarryColumns / 16, PF = 3;
+  __shared__ __attribute__((aligned(16))) uint32_t parts[2][NC][NV][PF][64][4];
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const uint32_t block = (uint32_t)block_id();
   if (block >= p.blocks) return;
@@ -314,68 +329,104 @@ __global__ __launch_bounds__(256) void delta_carry(CarryParams p) {
     len = p.map.len;
   }
   const int64_t n = (len + p.map.seg_len - 1) / p.map.seg_len;  // segments
-  const int v = tile * 64 + wave * 16 + l;
   if (n < 2) return;
-  const bool has = v < p.V;
   const int64_t kv = (int64_t)p.K * p.V;
-  const int col = has ? v : p.V - 1;
-  auto row = [&](int kt, int r) { return kt * 16 + 4 * g + r; };
-  f32x4 h[NK];
-  const float* from = p.from ? p.from + ((int64_t)s * p.heads + head) * kv + col : nullptr;
+  auto row = [&](int a, int r) { return (wave + a * NW) * 16 + 4 * g + r; };
+  auto col = [&](int t) { return tile * kCarryColumns + t * 16 + l; };
+  auto place = [&](int a, int t, int r) { return (int64_t)min(row(a, r), p.K - 1) * p.V + min(col(t), p.V - 1); };
+  auto inside = [&](int a, int t, int r) { return row(a, r) < p.K && col(t) < p.V; };
+  auto at = [&](int64_t i) { return (slot + (REVERSE ? n - 1 - i : i)) * p.heads + head; };
+  f32x4 h[OWN][NV], add[OWN][NV];
+  float m[OWN][NC][8];
+  auto load = [&](int64_t i) {  // segment i's u and M
+    const float *u = p.seg + at(i) * kv, *map = p.seg_map + at(i) * (KP * KP);
 #pragma unroll
-  for (int kt = 0; kt < NK; ++kt)
+    for (int a = 0; a < OWN; ++a) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float x = from ? from[(int64_t)min(row(kt, r), p.K - 1) * p.V] : 0.f;
-      h[kt][r] = row(kt, r) < p.K ? x : 0.f;
-    }
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t at = (slot + (REVERSE ? n - 1 - i : i)) * p.heads + head;
-    float* u = p.seg + at * kv + col;
-    f32x4 add[NK];
+      for (int t = 0; t < NV; ++t)
 #pragma unroll
-    for (int kt = 0; kt < NK; ++kt)
+        for (int r = 0; r < 4; ++r) add[a][t][r] = u[place(a, t, r)];
+      const int k = (wave + a * NW) * 16 + l;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) add[kt][r] = i + 1 < n ? u[(int64_t)min(row(kt, r), p.K - 1) * p.V] : 0.f;
-    Frag<uint16_t> b[NK / 2][PF];
-#pragma unroll
-    for (int c = 0; c < NK; c += 2) {
-      float x[8];
-      stack(h[c], h[c + 1], x);
-      split_parts(x, b[c / 2]);
-    }
-    if (has)
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (row(kt, r) < p.K) u[(int64_t)row(kt, r) * p.V] = h[kt][r];
-    if (i + 1 == n) break;
-    const float* m = p.seg_map + at * (KP * KP);
-#pragma unroll
-    for (int kt = 0; kt < NK; ++kt) {
-      f32x4 acc;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = row(kt, r) < p.K ? add[kt][r] : 0.f;
-#pragma unroll
-      for (int c = 0; c < NK; c += 2) {
-        float x[8];
+      for (int c = 0; c < NC; ++c) {
         if (REVERSE) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            x[r] = m[(c * 16 + 4 * g + r) * KP + kt * 16 + l];
-            x[4 + r] = m[(c * 16 + 16 + 4 * g + r) * KP + kt * 16 + l];
+            m[a][c][r] = map[(c * 32 + 4 * g + r) * KP + k];
+            m[a][c][4 + r] = map[(c * 32 + 16 + 4 * g + r) * KP + k];
           }
         } else {
-          const float* a = m + (kt * 16 + l) * KP + c * 16 + 4 * g;
-          stack(*reinterpret_cast<const f32x4*>(a), *reinterpret_cast<const f32x4*>(a + 16), x);
+          const float* x = map + k * KP + c * 32 + 4 * g;
+          stack(*reinterpret_cast<const f32x4*>(x), *reinterpret_cast<const f32x4*>(x + 16), m[a][c]);
         }
-        Frag<uint16_t> a[PF];
-        split_parts(x, a);
-        acc = mma_parts(a, b[c / 2], acc);
       }
-      h[kt] = acc;
     }
+  };
+  load(0);
+  const float* from = p.from ? p.from + ((int64_t)s * p.heads + head) * kv : nullptr;
+#pragma unroll
+  for (int a = 0; a < OWN; ++a)
+#pragma unroll
+    for (int t = 0; t < NV; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = from ? from[place(a, t, r)] : 0.f;
+        h[a][t][r] = inside(a, t, r) ? x : 0.f;
+      }
+  for (int64_t i = 0; i < n; ++i) {
+    float* u = p.seg + at(i) * kv;
+#pragma unroll
+    for (int a = 0; a < OWN; ++a)
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (inside(a, t, r)) u[place(a, t, r)] = h[a][t][r];
+    if (i + 1 == n) break;
+    auto& buffer = parts[i & 1];
+#pragma unroll
+    for (int a = 0; a < OWN; ++a)
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        const int k = wave + a * NW;
+        f32x4 x = h[a][t];
+#pragma unroll
+        for (int q = 0; q < PF; ++q) {
+          const uint32_t w[2] = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+          __builtin_memcpy(__builtin_assume_aligned(&buffer[k / 2][t][q][lane][2 * (k & 1)], 8), w, 8);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            x[2 * r] -= __uint_as_float(w[r] << 16);
+            x[2 * r + 1] -= __uint_as_float(w[r] & 0xffff0000u);
+          }
+        }
+      }
+    Frag<uint16_t> f[OWN][NC][PF];
+#pragma unroll
+    for (int a = 0; a < OWN; ++a) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) split_parts(m[a][c], f[a][c]);
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[a][t][r] = inside(a, t, r) ? add[a][t][r] : 0.f;
+    }
+    __syncthreads();  // h is whole; the buffer is next written behind the next barrier
+    load(i + 2 < n ? i + 1 : i);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        Frag<uint16_t> b[PF];
+#pragma unroll
+        for (int q = 0; q < PF; ++q) __builtin_memcpy(&b[q], __builtin_assume_aligned(buffer[c][t][q][lane], 16), 16);
+#pragma unroll
+        for (int x = PF - 1; x >= 0; --x)
+#pragma unroll
+          for (int q = 0; q <= x; ++q)
+#pragma unroll
+            for (int a = 0; a < OWN; ++a) h[a][t] = mma(f[a][c][q], b[x - q], h[a][t]);
+      }
   }
 }
 
@@ -399,15 +450,18 @@ template <typename E, int C, DeltaPass PASS>
 hipError_t launch_walk(DeltaParams p, const DeltaPlan& pl, hipStream_t st) {
   p.vtiles = (p.V + 63) / 64;
   p.ktiles = (pl.a.kp + 63) / 64;
-  p.blocks = (uint32_t)(pl.a.slots * p.heads * (PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles));
+  p.blocks = (uint32_t)(pl.a.slots * p.heads);
+  const int64_t blocks = spread_blocks(p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles);
   with_keys(pl, [&](auto kp, auto tiny) {
-    delta_walk<E, C, kp(), 64, 1, PASS, tiny()><<<grid_of(p.blocks, 256), dim3(256), 0, st>>>(p);
+    delta_walk<E, C, kp(), 64, 1, PASS, tiny()><<<grid_of(blocks, 256), dim3(256), 0, st>>>(p);
   });
   return hipGetLastError();
 }
 
-// Chunks of 64 tokens (32 in fp32).  Sequences are cut so that there are about `want` workgroups, if that makes `least`
-// segments of a sequence.
+// Chunks of 64 tokens (32 in fp32).  Sequences are cut so that there are about two workgroups per CU, packed ones, of which
+// only some may be long, four; into three segments at least, as two would be walked twice for less than twice the speed.
+// 16 heads of 128, us for 2, 3 and 4 workgroups per CU: 8192 tokens in one sequence 220, 258, 283, 38144 in six packed
+// ones 897, 771, 750; gradients of 2 x 4096 tokens 718 (one 846, four 799).
 DeltaPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
                     int dtype, int64_t want, int least) {
   DeltaPlan pl;
@@ -419,6 +473,7 @@ DeltaPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t ke
   a.vtiles = (int)((value_dim + 63) / 64);
   const int64_t chunk = a.chunk = dtype == 1 ? 64 : 32;
   const int64_t longest = packed ? tokens : tokens / sequences;
+  if (packed && sequences > 1) want *= 2;
   const int64_t each = want / (heads * a.vtiles);  // segments of all sequences together
   int64_t parts = packed ? (each - sequences > each / 2 ? each - sequences : each / 2) : each / sequences;
   if (parts < 1) parts = 1;
@@ -470,7 +525,7 @@ DeltaPlan plan_delta_backward(int64_t sequences, int64_t tokens, int64_t heads, 
 
 int64_t delta_blocks(const DeltaPlan& pl, int64_t sequences, int64_t heads, int64_t value_dim) {
   const int64_t v = (value_dim + 63) / 64, k = (pl.a.kp + 63) / 64;
-  const int64_t walk = pl.a.slots * heads * (v + k), systems = pl.a.chunks * heads, carry = 2 * sequences * heads * v;
+  const int64_t walk = tok::spread_blocks(pl.a.slots * heads, (int)(v + k)), systems = pl.a.chunks * heads, carry = sequences * heads * ((value_dim + kCarryColumns - 1) / kCarryColumns);
   return walk > systems ? (walk > carry ? walk : carry) : systems > carry ? systems : carry;
 }
 
@@ -518,14 +573,15 @@ hipError_t launch_delta_segments(DeltaParams p, const DeltaPlan& pl, int dtype, 
 }
 
 hipError_t launch_delta_carry(CarryParams c, const DeltaPlan& pl, bool reverse, hipStream_t st) {
-  c.vtiles = (c.V + 63) / 64;
+  c.vtiles = (c.V + kCarryColumns - 1) / kCarryColumns;
   c.blocks = (uint32_t)((int64_t)c.map.sequences * c.heads * c.vtiles);
   with_keys(pl, [&](auto kp, auto) {
-    const dim3 grid = grid_of(c.blocks, 256);
+    constexpr int threads = kp() == 256 ? 512 : kp() * 4;
+    const dim3 grid = grid_of(c.blocks, threads), block(threads);
     if (reverse)
-      delta_carry<kp(), true><<<grid, dim3(256), 0, st>>>(c);
+      delta_carry<kp(), true><<<grid, block, 0, st>>>(c);
     else
-      delta_carry<kp(), false><<<grid, dim3(256), 0, st>>>(c);
+      delta_carry<kp(), false><<<grid, block, 0, st>>>(c);
   });
   return hipGetLastError();
 }

@@ -330,8 +330,9 @@ int64_t ss2d_qk_norm_backward_workspace(const ss2d_qk_sizes* sizes, int dtype) {
   static const float one = 1.f;
   const int rc = check_qk(&one, &one, nullptr, nullptr, sizes->rotated > 0 ? &one : nullptr, nullptr, sizes, 0.f, dtype);
   if (rc != SS2D_OK) return rc;
-  return (int64_t)ss2d::qk_norm_backward_workspace_bytes(sizes->sequences * sizes->tokens, sizes->q_heads,
-                                                         sizes->k_heads, sizes->dim);
+  const int64_t heads[2] = {sizes->q_heads, sizes->k_heads};
+  return (int64_t)ss2d::qk_norm_backward_workspace_bytes(sizes->sequences * sizes->tokens, heads, sizes->dim,
+                                                         sizes->rotated);
 }
 
 int ss2d_qk_norm_backward(const void* q, const void* k, const float* q_weight, const float* k_weight,

@@ -50,19 +50,19 @@ __global__ __launch_bounds__(VT * 4, VT == 64 ? 1 : 2) void delta_walk_back(Back
   const DeltaParams& p = b.d;
   constexpr int NW = VT / 16, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   using S = Systems<E, C>;
-  constexpr int kSystem = 2 * S::kInverse;  // the transposed inverse and P'
+  constexpr int PN = S::kParts;
+  constexpr int kSystem = S::kBackward - S::kInverse;  // the transposed inverse and P'
   constexpr int kPieces = (kSystem / 16 + THREADS - 1) / THREADS;
   __shared__ Tile<E, C, KP, 32> qs, ks;
   __shared__ Tile<E, C, VT, 32> ds;
   __shared__ __attribute__((aligned(16))) char sys[kSystem];
-  __shared__ Decays<C> dec;
-  __shared__ __attribute__((aligned(16))) float bs[C];
+  __shared__ Rates<C> rates;
 
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const uint32_t block = (uint32_t)block_id();
-  if (block >= b.blocks) return;
-  const int vt = block % p.vtiles, head = block / p.vtiles % p.heads;
-  const int64_t slot = block / (p.vtiles * p.heads);
+  uint32_t unit, tile;
+  if (!spread((uint32_t)block_id(), b.blocks, p.vtiles, unit, tile)) return;
+  const int vt = tile, head = unit % p.heads;
+  const int64_t slot = unit / p.heads;
   Segment seg;
   if (!find_segment(p.map, slot, seg)) return;
   if (SUM && seg.begin == 0) return;  // of no use
@@ -107,10 +107,7 @@ __global__ __launch_bounds__(VT * 4, VT == 64 ? 1 : 2) void delta_walk_back(Back
     for (int i = 0; i < kPieces; ++i)
       if (kSystem / 16 % THREADS == 0 || threadIdx.x + i * THREADS < kSystem / 16)
         *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
-    if (wave == 0) {
-      scan_decays<C>(lane < n ? x.g : 0.f, dec);
-      if (lane < C) bs[lane] = lane < n ? x.b : 0.f;
-    }
+    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
   };
   const int64_t chunks = (seg.end - seg.begin + C - 1) / C;
   Chunk first;  // on its way while the gradient is read
@@ -166,21 +163,22 @@ __global__ __launch_bounds__(VT * 4, VT == 64 ? 1 : 2) void delta_walk_back(Back
         float y[8];
         stack(d[a], d[a + 1], y);
         split_parts(y, f);
+        Frag<E> k[NI];
 #pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const Frag<E> k = frag_row_split(ks, x * 16 + l, a * 16);
+        for (int x = 0; x < NI; ++x) k[x] = frag_row_split(ks, x * 16 + l, a * 16);
 #pragma unroll
-          for (int q = PF - 1; q >= 0; --q) u[x] = mma(k, f[q], u[x]);
-        }
+        for (int q = PF - 1; q >= 0; --q)  // independent products next to each other
+#pragma unroll
+          for (int x = 0; x < NI; ++x) u[x] = mma(k[x], f[q], u[x]);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int x = 0; x < NI; ++x) u[x] *= dec.between4(C - 1, x * 16 + 4 * g);
+      for (int x = 0; x < NI; ++x) u[x] *= rates.four(&rates.left[x * 16 + 4 * g]);
       if (!SUM) {
         float s = 0.f;  // errors behind the end and outside the columns meet a 0
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
-          const f32x4 be = *reinterpret_cast<const f32x4*>(&bs[x * 16 + 4 * g]);
+          const f32x4 be = rates.four(&rates.beta[x * 16 + 4 * g]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) s = x * 16 + 4 * g + r < n && v < nv ? fmaf(be[r] * e[x][r], u[x][r], s) : s;
         }
@@ -191,29 +189,27 @@ __global__ __launch_bounds__(VT * 4, VT == 64 ? 1 : 2) void delta_walk_back(Back
       for (int j = 0; j < NI; j += 2) {
         const Frag<E> f = frag_col_split(ds, j * 16, wave * 16);
 #pragma unroll
-        for (int x = 0; x < j + 2; ++x)
+        for (int q = PF - 1; q >= 0; --q)
 #pragma unroll
-          for (int q = PF - 1; q >= 0; --q)
+          for (int x = 0; x < j + 2; ++x)
             u[x] = mma(system_frag<E>(sys + S::kInverse + (S::upper(x, j / 2) * PF + q) * S::kFragBytes), f, u[x]);
       }
       __builtin_amdgcn_sched_barrier(0);
-      // dF
+      // dF = dU + N' dU
       f32x4 z[NI];
 #pragma unroll
-      for (int x = 0; x < NI; ++x) z[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < NI; ++x) z[x] = u[x];
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        Frag<E> f[PF];
+        Frag<E> f[PN], a[NI][PN];
         float y[8];
+#pragma unroll
+        for (int x = 0; x < j + 2; ++x)
+#pragma unroll
+          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys + (S::upper(x, j / 2) * PN + q) * S::kFragBytes);
         stack(u[j], u[j + 1], y);
         split_parts(y, f);
-#pragma unroll
-        for (int x = 0; x < j + 2; ++x) {
-          Frag<E> a[PF];
-#pragma unroll
-          for (int q = 0; q < PF; ++q) a[q] = system_frag<E>(sys + (S::upper(x, j / 2) * PF + q) * S::kFragBytes);
-          z[x] = mma_parts(a, f, z[x]);
-        }
+        j == 0 ? mma_parts<0, 2>(a, f, z) : mma_parts<0, NI>(a, f, z);
       }
       if (!SUM) {
         float* to = b.df + rows;
@@ -227,12 +223,12 @@ __global__ __launch_bounds__(VT * 4, VT == 64 ? 1 : 2) void delta_walk_back(Back
       }
       __builtin_amdgcn_sched_barrier(0);
       // D for the chunk before
-      const float all = __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]);
+      const float all = rates.since[C - 1];
 #pragma unroll
       for (int kt = 0; kt < NK; ++kt) d[kt] *= all;
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        const f32x4 f0 = dec.since4(j * 16 + 4 * g), f1 = dec.since4(j * 16 + 16 + 4 * g);
+        const f32x4 f0 = rates.four(&rates.since[j * 16 + 4 * g]), f1 = rates.four(&rates.since[j * 16 + 16 + 4 * g]);
         Frag<E> fo[PF], fz[PF];
         float y[8];
         frag_values(frag_col_split(ds, j * 16, wave * 16), y);
@@ -242,17 +238,23 @@ __global__ __launch_bounds__(VT * 4, VT == 64 ? 1 : 2) void delta_walk_back(Back
           y[4 + r] *= p.scale * f1[r];
         }
         split_parts(y, fo);
-        const f32x4 b0 = *reinterpret_cast<const f32x4*>(&bs[j * 16 + 4 * g]);
-        const f32x4 b1 = *reinterpret_cast<const f32x4*>(&bs[j * 16 + 16 + 4 * g]);
+        const f32x4 b0 = rates.four(&rates.beta[j * 16 + 4 * g]), b1 = rates.four(&rates.beta[j * 16 + 16 + 4 * g]);
         stack(z[j] * (b0 * -f0), z[j + 1] * (b1 * -f1), y);
         split_parts(y, fz);
 #pragma unroll
-        for (int kt = 0; kt < NK; ++kt) {
-          const Frag<E> q = frag_col_split(qs, j * 16, kt * 16), k = frag_col_split(ks, j * 16, kt * 16);
+        for (int kt = 0; kt < NK; kt += 2) {
+          Frag<E> q[2], k[2];
 #pragma unroll
-          for (int i = PF - 1; i >= 0; --i) {
-            d[kt] = mma(q, fo[i], d[kt]);
-            d[kt] = mma(k, fz[i], d[kt]);
+          for (int i = 0; i < 2; ++i) {
+            q[i] = frag_col_split(qs, j * 16, (kt + i) * 16);
+            k[i] = frag_col_split(ks, j * 16, (kt + i) * 16);
+          }
+#pragma unroll
+          for (int n = PF - 1; n >= 0; --n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) d[kt + i] = mma(q[i], fo[n], d[kt + i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) d[kt + i] = mma(k[i], fz[n], d[kt + i]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -301,11 +303,12 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
   const DeltaParams& p = b.d;
   constexpr int THREADS = NW * 64, NI = C / 16, NK = KP / 16, VT = 64, NV = VT / 16, PF = kFullParts<E>;
   constexpr int OK = (NK + NW - 1) / NW;
+  constexpr int PB = PF > 1 ? 2 : 1;  // parts of U and dZ towards dk, whose products round one operand only
   constexpr int JS = NW / NI < NI ? NW / NI : NI;  // waves that share 16 tokens' scores
   constexpr int TT = THREADS / C, PC = VT / TT;    // threads per token, each with PC columns of values
   static_assert(NW >= NI && PC % 4 == 0, "score tiles and columns are dealt evenly");
   struct Values {
-    Tile<E, C, VT> d, z, u[PF];
+    Tile<E, C, VT> d, z[PB], u[PF];
   };
   struct Scores {
     Tile<E, C, C, 32> x[PF], y;
@@ -376,7 +379,7 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
           vsum = fmaf(z[r], v[r], vsum);
         }
         put4_parts(m.v.u, ti * m.v.u[0].stride + tc + c, e * be);
-        put4(&m.v.z.e[ti * m.v.z.stride + tc + c], z);
+        put4_parts(m.v.z, ti * m.v.z[0].stride + tc + c, z);
         if (left > 0) store4(static_cast<E*>(b.dv) + row + c, left, z);
       }
       d.store(m.v.d, n, nv);
@@ -388,10 +391,18 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
       if (share < JS && jt % JS == share && jt <= it)
 #pragma unroll
         for (int c = 0; c < VT; c += 32) {
-          const Frag<E> fd = frag_row(m.v.d, i0, c), fz = frag_row(m.v.z, i0, c);
+          const Frag<E> fd = frag_row(m.v.d, i0, c);
+          Frag<E> fu[PF], fz[PB];
 #pragma unroll
-          for (int q = PF - 1; q >= 0; --q) sx[jt] = mma(frag_row(m.v.u[q], jt * 16 + l, c), fd, sx[jt]);
-          sy[jt] = mma(frag_row(m.v.u[0], jt * 16 + l, c), fz, sy[jt]);
+          for (int q = 0; q < PF; ++q) fu[q] = frag_row(m.v.u[q], jt * 16 + l, c);
+#pragma unroll
+          for (int q = 0; q < PB; ++q) fz[q] = frag_row(m.v.z[q], i0, c);
+#pragma unroll
+          for (int q = PF - 1; q >= 0; --q) sx[jt] = mma(fu[q], fd, sx[jt]);
+#pragma unroll
+          for (int s = PB - 1; s >= 0; --s)
+#pragma unroll
+            for (int q = 0; q <= s; ++q) sy[jt] = mma(fu[q], fz[s - q], sy[jt]);
         }
 #pragma unroll
     for (int a = 0; a < OK; ++a)
@@ -415,8 +426,11 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
             const Frag<E> o = frag_row_split(m.v.d, x * 16 + l, c * 16);
 #pragma unroll
             for (int q = PF - 1; q >= 0; --q) dq[a][0][x] = mma(fh[q], o, dq[a][0][x]);
-            dk[a][0][x] = mma(fd[0], frag_row_split(m.v.u[0], x * 16 + l, c * 16), dk[a][0][x]);
-            dz[a][x] = mma(fh[0], frag_row_split(m.v.z, x * 16 + l, c * 16), dz[a][x]);
+#pragma unroll
+            for (int q = PB - 1; q >= 0; --q) {
+              dk[a][0][x] = mma(fd[0], frag_row_split(m.v.u[q], x * 16 + l, c * 16), dk[a][0][x]);
+              dz[a][x] = mma(fh[0], frag_row_split(m.v.z[q], x * 16 + l, c * 16), dz[a][x]);
+            }
           }
         }
       }
@@ -583,10 +597,10 @@ template <typename E, int C, bool SUM>
 hipError_t launch_walk_back(BackParams b, const DeltaPlan& pl, hipStream_t st) {
   const int vt = back_tile(b.d.V, pl);
   b.d.vtiles = (b.d.V + vt - 1) / vt;
-  b.blocks = (uint32_t)(pl.a.slots * b.d.heads * b.d.vtiles);
+  b.blocks = (uint32_t)(pl.a.slots * b.d.heads);
   b.columns = columns_of(b.d.V, pl);
   with_keys(pl, [&](auto kp, auto tiny) {
-    const dim3 grid = grid_of(b.blocks, vt * 4), block(vt * 4);
+    const dim3 grid = grid_of(spread_blocks(b.blocks, b.d.vtiles), vt * 4), block(vt * 4);
     if (vt == 64)
       delta_walk_back<E, C, kp(), 64, SUM, tiny()><<<grid, block, 0, st>>>(b);
     else if constexpr (!tiny())

@@ -2,10 +2,12 @@
 //
 // With L_ij = exp(G_i - G_j) k_i . k_j for j < i, b = beta and P_ij = scale exp(G_i - G_j) q_i . k_j for j <= i, per
 // chunk of C tokens and head
-//   forward    (1 + L diag(b))^-1 in parts and P in one;
-//   gradients  the same inverse, and ((1 + diag(b) L)^-1)' and P' in parts,
-// as fragments in the order in which the walks read them.  Parts: as for states, what becomes an fp32 result keeps 24
-// bits.
+//   forward    N = (1 + L diag(b))^-1 - 1 in parts and P in one;
+//   gradients  the same N, and ((1 + diag(b) L)^-1)' - 1 and P' in parts,
+// as fragments in the order in which the walks read them.  Parts: P' becomes an fp32 result and keeps 24 bits in three.
+// Of an inverse the ones on the diagonal are left to the walks, which add their operand as it is, and the rest, entries of
+// about beta k_i . k_j, takes two parts: 17 bits of what is added to the operand, a quarter of it for keys that are
+// nothing to each other (error of a state of 2048 tokens 1.8e-7 with three parts, 2.6e-7 with two).
 //
 // A triangle is inverted in blocks of 16.  A diagonal block by substitution: a lane holds one row of the inverse and
 // the block's entries are read by all lanes at once; as stable as the system is, where a series of powers would cancel
@@ -87,6 +89,16 @@ __device__ __forceinline__ void invert(Triangle<C>& m, int w, f32x4 (&x)[C / 16]
   }
 }
 
+// The diagonal's ones are the walks'.
+template <int NI>
+__device__ __forceinline__ void drop_ones(int w, f32x4 (&x)[NI]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+#pragma unroll
+  for (int t = 0; t < NI; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[t][r] = t == w && 4 * g + r == l ? 0.f : x[t][r];
+}
+
 // Two stacked tiles to memory as a fragment's N parts.
 template <int N, typename E>
 __device__ __forceinline__ void put_frag(char* at, const f32x4& a, const f32x4& b) {
@@ -115,8 +127,14 @@ template <typename E, int C, int KP, bool BACK, bool TINY>
 __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
   constexpr int NI = C / 16, THREADS = NI * 64;
   using S = Systems<E, C>;
-  __shared__ Tile<E, C, KP> ks, qs;
-  __shared__ Triangle<C> m;
+  __shared__ Tile<E, C, KP> ks;
+  __shared__ union Rest {  // the queries are done with before the triangle is written
+    Tile<E, C, KP> qs;
+    Triangle<C> m;
+    __device__ Rest() {}
+  } rest;
+  auto& qs = rest.qs;
+  auto& m = rest.m;
   __shared__ Decays<C> dec;
   __shared__ float bs[C];
   const int w = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
@@ -145,7 +163,7 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
     k.store(ks, n, p.K);
   }
   __syncthreads();
-  char* out = p.systems + (int64_t)block * (BACK ? 3 * S::kInverse : S::kInverse + S::kScores);
+  char* out = p.systems + (int64_t)block * (BACK ? S::kBackward : S::kForward);
   const int i0 = w * 16 + l;
 
   // P by tiles: rows j of column i in tile column w, for gradients rows i of column j in tile column w
@@ -172,11 +190,12 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
     for (int pair = 0; pair < NI / 2; ++pair)
       if (BACK ? pair >= w / 2 : pair <= w / 2) {
         if (BACK)
-          put_frag<S::kParts, E>(out + 2 * S::kInverse + S::upper(w, pair) * S::kParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
+          put_frag<S::kScoreParts, E>(out + 2 * S::kInverse + S::upper(w, pair) * S::kScoreParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
         else
           put_frag<1, E>(out + S::kInverse + S::lower(w, pair) * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
       }
   }
+  __syncthreads();  // the queries have been read
   // (1 + L diag(b))^-1 transposed, an upper triangle: rows j, columns i
 #pragma unroll
   for (int t = 0; t < NI; ++t)
@@ -192,6 +211,7 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
     }
   f32x4 x[NI];
   invert<C, true>(m, w, x);
+  drop_ones(w, x);
 #pragma unroll
   for (int pair = 0; pair < NI / 2; ++pair)
     if (pair <= w / 2)
@@ -212,6 +232,7 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
       *reinterpret_cast<f32x4*>(&m.z[i0 * m.kStride + t * 16 + 4 * g]) = s;
     }
   invert<C, false>(m, w, x);
+  drop_ones(w, x);
 #pragma unroll
   for (int pair = 0; pair < NI / 2; ++pair)
     if (pair >= w / 2)
@@ -236,9 +257,8 @@ void launch(const DeltaParams& p, const DeltaPlan& pl, hipStream_t st) {
 }  // namespace
 
 int64_t system_bytes(const DeltaPlan& pl, int dtype) {
-  if (dtype == 1)
-    return pl.backward ? 3 * Systems<uint16_t, 64>::kInverse : Systems<uint16_t, 64>::kInverse + Systems<uint16_t, 64>::kScores;
-  return pl.backward ? 3 * Systems<float, 32>::kInverse : Systems<float, 32>::kInverse + Systems<float, 32>::kScores;
+  if (dtype == 1) return pl.backward ? Systems<uint16_t, 64>::kBackward : Systems<uint16_t, 64>::kForward;
+  return pl.backward ? Systems<float, 32>::kBackward : Systems<float, 32>::kForward;
 }
 
 hipError_t launch_delta_systems(const DeltaParams& q, const DeltaPlan& pl, int dtype, hipStream_t st) {

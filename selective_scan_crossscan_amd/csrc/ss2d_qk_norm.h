@@ -28,6 +28,6 @@ struct QkArgs {
 };
 hipError_t launch_qk_norm(const QkArgs& a);
 hipError_t launch_qk_norm_backward(const QkArgs& a);
-size_t qk_norm_backward_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim);
+size_t qk_norm_backward_workspace_bytes(int64_t tokens, const int64_t (&heads)[2], int64_t dim, int64_t rotated);
 
 }  // namespace ss2d

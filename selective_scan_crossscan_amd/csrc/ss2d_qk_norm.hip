@@ -8,6 +8,8 @@
 // 64 threads between the sum over it and the output.  A thread has eight channels as two quads a, b: of rotating
 // channels the two quads whose values are pairs, wherever the pairs' halves lie, so a pair never crosses threads.
 // Table rows and weights are shared by all heads of a token, or all rows, and come from the caches.
+#include <type_traits>
+
 #include "ss2d_delta.h"
 #include "ss2d_qk_norm.h"
 
@@ -21,12 +23,12 @@ struct QkParams {
   const float* table;
   const int32_t* positions;
   float* partial;  // gradients: (workgroup, dim)
-  int64_t tokens, length, table_rows;  // all tokens; of a sequence
+  uint32_t tokens, length, table_rows;  // all tokens; of a sequence
   int heads[2];
+  int runs[2];     // runs of heads of a token
   int dim, rotated, pair_pieces, interleaved;
   int blocks[2];   // gradients: workgroups of each side
-  uint32_t rows;
-  float eps;
+  float eps, share;  // share: 1 / dim
 };
 
 // A thread's channels: quads at a and b, of which na and nb exist; pairs: they rotate.
@@ -52,117 +54,157 @@ __device__ __forceinline__ Piece piece_of(const QkParams& p, int t) {
   }
   return x;
 }
-template <typename S>
+// WHOLE: every thread has eight channels, and the ends are not asked for.
+template <bool WHOLE, typename S>
 __device__ __forceinline__ void load_piece(const S* row, const Piece& x, f32x4& a, f32x4& b) {
-  a = load4(row + x.a, x.na);
-  b = load4(row + x.b, x.nb);
+  a = load4(row + x.a, WHOLE ? 4 : x.na);
+  b = load4(row + x.b, WHOLE ? 4 : x.nb);
   if (x.zip) {
     const f32x4 u = {a[0], a[2], b[0], b[2]}, v = {a[1], a[3], b[1], b[3]};
     a = u;
     b = v;
   }
 }
-template <typename S>
+template <bool WHOLE, typename S>
 __device__ __forceinline__ void store_piece(S* row, const Piece& x, f32x4 a, f32x4 b) {
   if (x.zip) {
     const f32x4 u = {a[0], b[0], a[1], b[1]}, v = {a[2], b[2], a[3], b[3]};
     a = u;
     b = v;
   }
-  if (x.na > 0) store4(row + x.a, x.na, a);
-  if (x.nb > 0) store4(row + x.b, x.nb, b);
+  if (WHOLE || x.na > 0) store4(row + x.a, WHOLE ? 4 : x.na, a);
+  if (WHOLE || x.nb > 0) store4(row + x.b, WHOLE ? 4 : x.nb, b);
 }
+// Sum over the THREADS threads that share a row: within 16 lanes by permutations that cost no LDS access.
 template <int THREADS>
 __device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < THREADS; m <<= 1) v += __shfl_xor(v, m);
+  constexpr int kPairs = 0xb1, kHalves = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;  // of a quad, of eight, of a row
+  v += dpp<kPairs>(v);
+  v += dpp<kHalves>(v);
+  if (THREADS >= 8) v += dpp<kHalfMirror>(v);
+  if (THREADS >= 16) v += dpp<kMirror>(v);
+  if (THREADS >= 32) v += __shfl_xor(v, 16);
+  if (THREADS >= 64) v += __shfl_xor(v, 32);
   return v;
 }
+// A token's place: its sequence and its number there.
+struct Place {
+  uint32_t token, sequence, at;
+  __device__ __forceinline__ Place(const QkParams& p, uint32_t t) : token(t), sequence(0), at(t) {
+    if (p.length < p.tokens) {
+      sequence = t / p.length;
+      at = t - sequence * p.length;
+    }
+  }
+  __device__ __forceinline__ int64_t offset(const int64_t (&stride)[3]) const {
+    return sequence * stride[0] + at * stride[1];
+  }
+};
 // Cosines and sines of a token's pairs.
-__device__ __forceinline__ void angles(const QkParams& p, const Piece& x, int64_t token, f32x4& c, f32x4& s) {
-  int64_t at = p.positions ? p.positions[token] : token % p.length;
-  at = at < 0 ? 0 : at >= p.table_rows ? p.table_rows - 1 : at;
-  const float* row = p.table + at * p.rotated + x.pair;
-  const int n = min(4, p.rotated / 2 - x.pair);
-  c = load4(row, n);
-  s = load4(row + p.rotated / 2, n);
-}
-__device__ __forceinline__ int64_t offset(const int64_t (&stride)[3], const QkParams& p, int64_t token, int head) {
-  const int64_t s = token / p.length;
-  return s * stride[0] + (token - s * p.length) * stride[1] + head * stride[2];
+template <bool WHOLE>
+__device__ __forceinline__ void angles(const QkParams& p, const Piece& x, const Place& at, f32x4& c, f32x4& s) {
+  int64_t row = p.positions ? (int64_t)p.positions[at.token] : (int64_t)at.at;
+  row = row < 0 ? 0 : row >= p.table_rows ? p.table_rows - 1 : row;
+  const float* from = p.table + row * p.rotated + x.pair;
+  const int n = WHOLE ? 4 : min(4, p.rotated / 2 - x.pair);
+  c = load4(from, n);
+  s = load4(from + p.rotated / 2, n);
 }
 
-template <typename S, int THREADS>
+// THREADS threads take a run of RUN heads of one token, all loads before the first sum.
+template <typename S, int THREADS, int RUN, bool WHOLE>
 __global__ __launch_bounds__(256) void qk_norm_kernel(QkParams p) {
-  const uint32_t row = (uint32_t)block_id() * (256 / THREADS) + threadIdx.x / THREADS;
-  if (row >= p.rows) return;  // whole rows; no barrier follows
-  const uint32_t heads = p.heads[0] + p.heads[1];
-  const int64_t token = row / heads;
-  const int side = row % heads >= (uint32_t)p.heads[0], head = row % heads - (side ? p.heads[0] : 0);
+  const uint32_t item = (uint32_t)block_id() * (256 / THREADS) + threadIdx.x / THREADS;
+  const uint32_t runs = p.runs[0] + p.runs[1], token = item / runs;
+  if (token >= p.tokens) return;  // whole groups of threads; no barrier follows
+  uint32_t run = item - token * runs;
+  const int side = run >= (uint32_t)p.runs[0];
+  if (side) run -= p.runs[0];
   const QkSide& z = p.side[side];
+  const int head = run * RUN, last = p.heads[side] - 1;
+  const Place at(p, token);
   const Piece x = piece_of(p, threadIdx.x % THREADS);
-  f32x4 a, b, c, s, wa, wb;
-  load_piece(static_cast<const S*>(z.x) + offset(z.x_stride, p, token, head), x, a, b);
-  if (x.turns) angles(p, x, token, c, s);
-  if (z.weight) load_piece(z.weight, x, wa, wb);
-  float sq = 0.f;
+  f32x4 a[RUN], b[RUN], c, s, wa, wb;
+  const S* from = static_cast<const S*>(z.x) + at.offset(z.x_stride);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
-  const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq) / (float)p.dim + p.eps);
-  a *= rstd;
-  b *= rstd;
-  if (z.weight) {
-    a *= wa;
-    b *= wb;
+  for (int i = 0; i < RUN; ++i) load_piece<WHOLE>(from + min(head + i, last) * z.x_stride[2], x, a[i], b[i]);
+  if (x.turns) angles<WHOLE>(p, x, at, c, s);
+  if (z.weight) load_piece<WHOLE>(z.weight, x, wa, wb);
+  S* to = static_cast<S*>(z.y) + at.offset(z.y_stride);
+#pragma unroll
+  for (int i = 0; i < RUN; ++i) {
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sq = fmaf(a[i][j], a[i][j], fmaf(b[i][j], b[i][j], sq));
+    const float rstd = rsqrtf(row_sum<THREADS>(sq) * p.share + p.eps);
+    f32x4 u = a[i] * rstd, v = b[i] * rstd;
+    if (z.weight) {
+      u *= wa;
+      v *= wb;
+    }
+    if (x.turns) {
+      const f32x4 w = u * c - v * s;
+      v = u * s + v * c;
+      u = w;
+    }
+    if (head + i <= last) store_piece<WHOLE>(to + (head + i) * z.y_stride[2], x, u, v);
   }
-  if (x.turns) {
-    const f32x4 u = a * c - b * s;
-    b = a * s + b * c;
-    a = u;
-  }
-  store_piece(static_cast<S*>(z.y) + offset(z.y_stride, p, token, head), x, a, b);
 }
 
-// One wave per workgroup; workgroups 0 .. blocks[0] - 1 take the queries' rows, the others the keys'.
-template <typename S, int THREADS>
-__global__ __launch_bounds__(64) void qk_norm_backward_kernel(QkParams p) {
-  constexpr int ROWS = 64 / THREADS;
+// Workgroups 0 .. blocks[0] - 1 take the queries' runs of heads, the others the keys'; each leaves one part of the
+// weight's gradient.
+template <typename S, int THREADS, int RUN, bool WHOLE>
+__global__ __launch_bounds__(256) void qk_norm_backward_kernel(QkParams p) {
+  constexpr int ITEMS = 256 / THREADS;
+  __shared__ f32x4 parts[2][4][THREADS];
   const int side = (int)blockIdx.x >= p.blocks[0], block = (int)blockIdx.x - (side ? p.blocks[0] : 0);
   const QkSide& z = p.side[side];
   const int heads = p.heads[side];
-  const int64_t rows = p.tokens * heads, step = (int64_t)p.blocks[side] * ROWS;
+  const uint32_t runs = p.runs[side], step = p.blocks[side] * ITEMS, items = p.tokens * runs;
   const Piece x = piece_of(p, threadIdx.x % THREADS);
   f32x4 wa = {1.f, 1.f, 1.f, 1.f}, wb = wa, da = {0.f, 0.f, 0.f, 0.f}, db = da;
-  if (z.weight) load_piece(z.weight, x, wa, wb);
-  for (int64_t row = (int64_t)block * ROWS + threadIdx.x / THREADS; row < rows; row += step) {
-    const int64_t token = row / heads;
-    const int head = (int)(row - token * heads);
-    f32x4 a, b, ga, gb;
-    load_piece(static_cast<const S*>(z.x) + offset(z.x_stride, p, token, head), x, a, b);
-    load_piece(static_cast<const S*>(z.dy) + offset(z.y_stride, p, token, head), x, ga, gb);
-    if (x.turns) {
-      f32x4 c, s;
-      angles(p, x, token, c, s);
-      const f32x4 u = ga * c + gb * s;
-      gb = gb * c - ga * s;
-      ga = u;
-    }
-    const f32x4 ha = ga * wa, hb = gb * wb;
-    float sq = 0.f, dot = 0.f;
+  if (z.weight) load_piece<WHOLE>(z.weight, x, wa, wb);
+  for (uint32_t item = block * ITEMS + threadIdx.x / THREADS; item < items; item += step) {
+    const uint32_t token = item / runs;
+    const int head = (item - token * runs) * RUN;
+    const Place at(p, token);
+    const S* from = static_cast<const S*>(z.x) + at.offset(z.x_stride);
+    const S* dfrom = static_cast<const S*>(z.dy) + at.offset(z.y_stride);
+    f32x4 a[RUN], b[RUN], ga[RUN], gb[RUN], c, s;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
-      dot = fmaf(a[i], ha[i], fmaf(b[i], hb[i], dot));
+    for (int i = 0; i < RUN; ++i) {
+      const int h = min(head + i, heads - 1);
+      load_piece<WHOLE>(from + h * z.x_stride[2], x, a[i], b[i]);
+      load_piece<WHOLE>(dfrom + h * z.y_stride[2], x, ga[i], gb[i]);
     }
-    sq = row_sum<THREADS>(sq);
-    dot = row_sum<THREADS>(dot);
-    const float rstd = 1.0f / sqrtf(sq / (float)p.dim + p.eps);
-    const float mean = dot * rstd / (float)p.dim;
-    a *= rstd;
-    b *= rstd;
-    da += ga * a;
-    db += gb * b;
-    store_piece(static_cast<S*>(z.y) + row * p.dim, x, rstd * (ha - a * mean), rstd * (hb - b * mean));
+    if (x.turns) angles<WHOLE>(p, x, at, c, s);
+    S* to = static_cast<S*>(z.y) + ((int64_t)token * heads + head) * p.dim;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      if (x.turns) {
+        const f32x4 u = ga[i] * c + gb[i] * s;
+        gb[i] = gb[i] * c - ga[i] * s;
+        ga[i] = u;
+      }
+      const f32x4 ha = ga[i] * wa, hb = gb[i] * wb;
+      float sq = 0.f, dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sq = fmaf(a[i][j], a[i][j], fmaf(b[i][j], b[i][j], sq));
+        dot = fmaf(a[i][j], ha[j], fmaf(b[i][j], hb[j], dot));
+      }
+      sq = row_sum<THREADS>(sq);
+      dot = row_sum<THREADS>(dot);
+      const float rstd = rsqrtf(sq * p.share + p.eps);
+      const float mean = dot * rstd * p.share;
+      a[i] *= rstd;
+      b[i] *= rstd;
+      if (head + i < heads) {
+        da += ga[i] * a[i];
+        db += gb[i] * b[i];
+        store_piece<WHOLE>(to + i * p.dim, x, rstd * (ha - a[i] * mean), rstd * (hb - b[i] * mean));
+      }
+    }
   }
   if (z.dweight) {
 #pragma unroll
@@ -172,7 +214,20 @@ __global__ __launch_bounds__(64) void qk_norm_backward_kernel(QkParams p) {
         da[i] += __shfl_xor(da[i], m);
         db[i] += __shfl_xor(db[i], m);
       }
-    if (threadIdx.x < THREADS) store_piece(p.partial + (int64_t)blockIdx.x * p.dim, x, da, db);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane < THREADS) {
+      parts[0][wave][lane] = da;
+      parts[1][wave][lane] = db;
+    }
+    __syncthreads();
+    if (threadIdx.x < THREADS) {
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        da += parts[0][w][lane];
+        db += parts[1][w][lane];
+      }
+      store_piece<WHOLE>(p.partial + (int64_t)blockIdx.x * p.dim, x, da, db);
+    }
   }
 }
 
@@ -204,86 +259,110 @@ __global__ __launch_bounds__(kSumCols * kSumRanges) void qk_sum_partials(QkParam
   }
 }
 
-QkParams params_of(const QkArgs& a) {
+QkParams params_of(const QkArgs& a, int run) {
   QkParams p{};
   for (int i = 0; i < 2; ++i) p.side[i] = a.side[i];
   p.table = a.table;
   p.positions = a.positions;
   p.partial = a.partial;
-  p.tokens = a.sequences * a.length;
-  p.length = a.length;
-  p.table_rows = a.table_rows;
-  p.heads[0] = (int)a.heads[0];
-  p.heads[1] = (int)a.heads[1];
+  p.tokens = (uint32_t)(a.sequences * a.length);
+  p.length = (uint32_t)a.length;
+  p.table_rows = (uint32_t)a.table_rows;
+  for (int i = 0; i < 2; ++i) {
+    p.heads[i] = (int)a.heads[i];
+    p.runs[i] = (int)((a.heads[i] + run - 1) / run);
+  }
   p.dim = (int)a.dim;
   p.rotated = a.table ? (int)a.rotated : 0;
   p.pair_pieces = (p.rotated + 7) / 8;
   p.interleaved = a.interleaved;
-  p.rows = (uint32_t)(p.tokens * (a.heads[0] + a.heads[1]));
   p.eps = a.eps;
+  p.share = 1.0f / (float)a.dim;
   return p;
 }
 // Threads per row: a power of two of at least its pieces of eight channels.
-int threads_of(const QkParams& p) {
-  const int pieces = p.pair_pieces + (p.dim - p.rotated + 7) / 8;
+int threads_of(int64_t dim, int64_t rotated) {
+  const int pieces = (int)((rotated + 7) / 8 + (dim - rotated + 7) / 8);
   int t = 4;
   while (t < pieces) t *= 2;
   return t;
 }
-// Workgroups of each side, as many of both as there are rows, at most kMost together.
-constexpr int64_t kMost = 2048;
-void share(int64_t tokens, int64_t hq, int64_t hk, int rows_each, int (&blocks)[2]) {
-  const int64_t h[2] = {hq, hk};
+// Heads in a run, and the gradients' workgroups of both sides at most: 16384 tokens of 16 + 16 heads of 128 in bf16, us of
+// runs of 1, 2 and 4 heads 65, 52, 48; gradients of runs of 1, 2 and 4 by 1024 to 4096 workgroups 89 to 103, 88 to 98 and
+// 89 (the fewer the better).
+constexpr int kRun = 4, kBackRun = 2;
+constexpr int64_t kMost = 1024;
+void share(int64_t tokens, const int64_t (&heads)[2], int threads, int run, int (&blocks)[2]) {
+  int64_t items[2];
+  for (int i = 0; i < 2; ++i) items[i] = tokens * ((heads[i] + run - 1) / run);
   for (int i = 0; i < 2; ++i) {
-    const int64_t all = (tokens * h[i] + rows_each - 1) / rows_each, most = kMost * h[i] / (hq + hk);
+    const int64_t all = (items[i] + 256 / threads - 1) / (256 / threads);
+    const int64_t most = kMost * items[i] / (items[0] + items[1]);
     blocks[i] = (int)(all < most ? all : most < 1 ? 1 : most);
   }
 }
 
-template <typename S>
-void launch_forward(const QkParams& p, hipStream_t st) {
-  const int t = threads_of(p);
-  const dim3 grid = grid_of(((int64_t)p.rows + 256 / t - 1) / (256 / t), 256), block(256);
+// Calls f with the threads per row and whether each has eight channels as constants.
+template <typename F>
+void with_threads(const QkParams& p, F f) {
+  using std::integral_constant;
+  const int t = threads_of(p.dim, p.rotated);
+  auto of = [&](auto threads) {
+    if (p.dim == 8 * t && p.rotated % 8 == 0)
+      f(threads, integral_constant<bool, true>());
+    else
+      f(threads, integral_constant<bool, false>());
+  };
   switch (t) {
-    case 4: qk_norm_kernel<S, 4><<<grid, block, 0, st>>>(p); break;
-    case 8: qk_norm_kernel<S, 8><<<grid, block, 0, st>>>(p); break;
-    case 16: qk_norm_kernel<S, 16><<<grid, block, 0, st>>>(p); break;
-    case 32: qk_norm_kernel<S, 32><<<grid, block, 0, st>>>(p); break;
-    default: qk_norm_kernel<S, 64><<<grid, block, 0, st>>>(p);
+    case 4: of(integral_constant<int, 4>()); break;
+    case 8: of(integral_constant<int, 8>()); break;
+    case 16: of(integral_constant<int, 16>()); break;
+    case 32: of(integral_constant<int, 32>()); break;
+    default: of(integral_constant<int, 64>());
   }
 }
+
+template <typename S, int RUN>
+void launch_forward(const QkArgs& a, hipStream_t st) {
+  const QkParams p = params_of(a, RUN);
+  const int t = threads_of(p.dim, p.rotated);
+  const int64_t items = (int64_t)p.tokens * (p.runs[0] + p.runs[1]);
+  const dim3 grid = grid_of((items + 256 / t - 1) / (256 / t), 256), block(256);
+  with_threads(p, [&](auto threads, auto whole) { qk_norm_kernel<S, threads(), RUN, whole()><<<grid, block, 0, st>>>(p); });
+}
 template <typename S>
-void launch_backward(const QkParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)(p.blocks[0] + p.blocks[1])), block(64);
-  switch (threads_of(p)) {
-    case 4: qk_norm_backward_kernel<S, 4><<<grid, block, 0, st>>>(p); break;
-    case 8: qk_norm_backward_kernel<S, 8><<<grid, block, 0, st>>>(p); break;
-    case 16: qk_norm_backward_kernel<S, 16><<<grid, block, 0, st>>>(p); break;
-    case 32: qk_norm_backward_kernel<S, 32><<<grid, block, 0, st>>>(p); break;
-    default: qk_norm_backward_kernel<S, 64><<<grid, block, 0, st>>>(p);
-  }
+void launch_backward(const QkArgs& a, hipStream_t st) {
+  QkParams p = params_of(a, kBackRun);
+  const int t = threads_of(p.dim, p.rotated);
+  share(p.tokens, a.heads, t, kBackRun, p.blocks);
+  const dim3 grid((unsigned)(p.blocks[0] + p.blocks[1])), block(256);
+  with_threads(p, [&](auto threads, auto whole) {
+    qk_norm_backward_kernel<S, threads(), kBackRun, whole()><<<grid, block, 0, st>>>(p);
+  });
   if (p.side[0].dweight || p.side[1].dweight)
     qk_sum_partials<<<dim3((unsigned)((p.dim + kSumCols - 1) / kSumCols), 2), dim3(kSumCols * kSumRanges), 0, st>>>(p);
 }
 
 }  // namespace
 
-size_t qk_norm_backward_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
+size_t qk_norm_backward_workspace_bytes(int64_t tokens, const int64_t (&heads)[2], int64_t dim, int64_t rotated) {
   int blocks[2];
-  share(tokens, q_heads, k_heads, 1, blocks);  // as if each row had a wave: an upper bound
+  share(tokens, heads, threads_of(dim, rotated), kBackRun, blocks);
   return (size_t)(blocks[0] + blocks[1]) * (size_t)dim * 4;
 }
 
 hipError_t launch_qk_norm(const QkArgs& a) {
-  const QkParams p = params_of(a);
-  a.dtype == 1 ? launch_forward<uint16_t>(p, a.stream) : launch_forward<float>(p, a.stream);
+  // Runs of heads share a token's angles and have more loads in flight; few rows are spread over the CUs instead.
+  const bool few = a.sequences * a.length * (a.heads[0] + a.heads[1]) < 16384;
+  if (a.dtype == 1)
+    few ? launch_forward<uint16_t, 1>(a, a.stream) : launch_forward<uint16_t, kRun>(a, a.stream);
+  else
+    few ? launch_forward<float, 1>(a, a.stream) : launch_forward<float, kRun>(a, a.stream);
   return hipGetLastError();
 }
 
 hipError_t launch_qk_norm_backward(const QkArgs& a) {
-  QkParams p = params_of(a);
-  share(p.tokens, a.heads[0], a.heads[1], 64 / threads_of(p), p.blocks);
-  a.dtype == 1 ? launch_backward<uint16_t>(p, a.stream) : launch_backward<float>(p, a.stream);
+  a.dtype == 1 ? launch_backward<uint16_t>(a, a.stream) : launch_backward<float>(a, a.stream);
   return hipGetLastError();
 }
 
