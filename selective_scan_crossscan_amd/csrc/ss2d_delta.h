@@ -89,11 +89,12 @@ struct DeltaParams {
   char* systems;            // (chunk, head): inverse, scores; backward: inverse, transposed inverse and scores
   float* seg_state;         // (slot, head, K, V): what a segment adds, after the carry the state before it
   float* seg_map;           // (slot, head, KP, KP): the segment's map of the state before it
-  float* chunk_state;       // (chunk, head, K, V): the state before every chunk
-  float* errors;            // (token, head, V)
+  float* chunk_state;       // (chunk, head, KP, VP): the state before every chunk, 0 outside K and V
+  float* errors;            // (chunk, head, C, VP): E, 0 behind the chunk's tokens and outside V
   SequenceMap map;          // segments
   SequenceMap chunk_map;    // segments of one chunk
   int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], b_stride[3];
+  int VP;  // values padded for the chunks' arrays
   int groups, heads, K, V, vtiles, ktiles;  // tiles of the pass's columns of values; of the segment maps' columns
   uint32_t blocks;          // workgroups; of a walk: units of a segment and head, each with its tiles
   float scale;
@@ -108,7 +109,7 @@ hipError_t launch_delta_systems(const DeltaParams& p, const DeltaPlan& pl, int d
 hipError_t launch_delta_segments(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st);
 // chunk_state and errors.
 hipError_t launch_delta_states(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st);
-// seg: what segments add to the state (to the gradient behind them, in reverse) to the states before (behind) them.
+// seg: what segments add to the state (backwards: to its gradient) becomes the states before (the gradients behind) them.
 struct CarryParams {
   float* seg;            // (slot, head, K, V)
   const float* seg_map;  // (slot, head, KP, KP)
@@ -117,7 +118,8 @@ struct CarryParams {
   int heads, K, V, vtiles;
   uint32_t blocks;
 };
-hipError_t launch_delta_carry(CarryParams p, const DeltaPlan& pl, bool reverse, hipStream_t st);
+// back: the same of the states' gradients, or null.
+hipError_t launch_delta_carry(CarryParams p, const CarryParams* back, const DeltaPlan& pl, hipStream_t st);
 // Bytes of one chunk's and head's systems.
 int64_t system_bytes(const DeltaPlan& pl, int dtype);
 
@@ -203,6 +205,15 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p, int n) {
       if (i < n) x[i] = load1(p + i);
   }
   return x;
+}
+
+// A padded array's value at rows 16 t + r of a result tile: from a uniform base by a lane's own offset in bytes, the same
+// for all tiles and rows, so that an address takes no registers of its own.
+__device__ __forceinline__ uint32_t tile_bytes(int step, int column) {
+  return 4u * (uint32_t)(4 * ((threadIdx.x & 63) >> 4) * step + column);
+}
+__device__ __forceinline__ float* tile_at(float* base, int t, int r, int step, uint32_t bytes) {
+  return reinterpret_cast<float*>(reinterpret_cast<char*>(base + (t * 16 + r) * step) + bytes);
 }
 
 // Two result tiles stacked along their rows as the eight inner values of an operand.

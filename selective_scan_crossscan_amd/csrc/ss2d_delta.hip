@@ -8,302 +8,17 @@
 // Few sequences and heads leave CUs idle, so sequences are then cut into segments.  What a segment does to the state is
 // affine, h -> M h + u: u is the walk from 0, M (keys x keys) the walk from the identity with values 0, both by the same
 // kernel, and a carry along the segments gives the states before them.
-#include <type_traits>
-
-#include "ss2d_delta.h"
+#include "ss2d_delta_walk.h"
 
 namespace ss2d {
 namespace {
 
-using namespace tok;
-
 constexpr int kCarryColumns = 32;
 
-enum DeltaPass { kOutputs, kSegments, kStates };
-
-template <typename E, int C, int KP, int VT, int NV, DeltaPass PASS, bool TINY>
-__global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
-  constexpr int NW = VT / 16 / NV, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
-  using S = Systems<E, C>;
-  constexpr int PN = S::kParts;
-  constexpr int kSystem = PASS == kOutputs ? S::kForward : S::kInverse;  // bytes read per chunk
-  constexpr int kPieces = (kSystem / 16 + THREADS - 1) / THREADS;
-  __shared__ Tile<E, PASS == kOutputs ? C : 1, KP> qs;
-  __shared__ Tile<E, C, KP, 16> ks;
-  __shared__ Tile<E, C, VT, 32> vs;
-  __shared__ __attribute__((aligned(16))) char sys[kSystem];
-  __shared__ Rates<C> rates;
-
-  const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  uint32_t unit, at_tile;
-  if (!spread((uint32_t)block_id(), p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles, unit, at_tile)) return;
-  const int tile = at_tile, head = unit % p.heads;
-  const int64_t slot = unit / p.heads;
-  Segment seg;
-  if (!find_segment(p.map, slot, seg)) return;
-  const bool map = PASS == kSegments && tile >= p.vtiles;  // columns of the identity instead of values
-  if (PASS == kSegments && seg.last && !(map && p.last_maps && seg.begin > 0)) return;  // of no use
-  const int group = head / (p.heads / p.groups);
-  const int K = p.K, v0 = (map ? tile - p.vtiles : tile) * VT, nv = min((map ? KP : p.V) - v0, VT);
-  const int vw = wave * 16 * NV;
-  const bool active = vw < nv;
-  const int64_t token0 = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
-  const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + token0 * p.q_stride[1] + group * p.q_stride[2];
-  const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + token0 * p.k_stride[1] + group * p.k_stride[2];
-  const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + token0 * p.v_stride[1] + head * p.v_stride[2] + (map ? 0 : v0);
-  const float* gb = p.g + sq * p.g_stride[0] + token0 * p.g_stride[1] + head * p.g_stride[2];
-  const float* bb = p.beta + sq * p.b_stride[0] + token0 * p.b_stride[1] + head * p.b_stride[2];
-  const int64_t chunk0 = chunk_number<C>(p.map, seg, seg.begin);
-  const char* sb = p.systems + (chunk0 * p.heads + head) * p.system_stride;
-  const int64_t sstep = p.heads * p.system_stride;
-
-  struct Chunk {
-    TileLoad<E, PASS == kOutputs ? C : 1, KP, 16, THREADS, TINY> q;
-    TileLoad<E, C, KP, 16, THREADS, TINY> k;
-    TileLoad<E, C, VT, 32, THREADS, TINY> v;
-    uint4 s[kPieces];
-    float g, b;
-  };
-  auto fetch = [&](Chunk& x, int64_t at) {
-    const int n = (int)min((int64_t)C, seg.end - at);
-    if (PASS == kOutputs) x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
-    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
-    if (!map) x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
-    const char* from = sb + (at - seg.begin) / C * sstep;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      x.s[i] = *reinterpret_cast<const uint4*>(from + min((int)threadIdx.x + i * THREADS, kSystem / 16 - 1) * 16);
-    const int64_t t = at + min(lane, n - 1);
-    x.g = gb[t * p.g_stride[1]];
-    x.b = bb[t * p.b_stride[1]];
-  };
-  auto land = [&](const Chunk& x, int64_t at) {
-    const int n = (int)min((int64_t)C, seg.end - at);
-    if (PASS == kOutputs) x.q.store(qs, n, K);
-    x.k.store(ks, n, K);
-    if (!map) x.v.store(vs, n, nv);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (kSystem / 16 % THREADS == 0 || threadIdx.x + i * THREADS < kSystem / 16)
-        *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
-    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
-  };
-  Chunk first;  // on its way while the state is read
-  if (seg.begin < seg.end) fetch(first, seg.begin);
-
-  // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
-  f32x4 h[NK][NV];
-  const int64_t kv = (int64_t)K * p.V, sh = ((int64_t)slot * p.heads + head) * kv, qh = ((int64_t)seg.s * p.heads + head) * kv;
-  const float* from = PASS == kSegments ? nullptr : p.split && seg.several() ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
-#pragma unroll
-  for (int t = 0; t < NV; ++t) {
-    const int v = vw + t * 16 + l;
-    if (from) {
-      const float* c = from + v0 + min(v, nv - 1);
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h[kt][t][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
-    }
-#pragma unroll
-    for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = kt * 16 + 4 * g + r;
-        h[kt][t][r] = from ? (k < K && v < nv ? h[kt][t][r] : 0.f) : map && k == v0 + v && k < K ? 1.f : 0.f;
-      }
-  }
-  if (map)
-    for (int i = threadIdx.x; i < C * vs.stride; i += THREADS) vs.e[i] = (E)0;
-  if (seg.begin < seg.end) land(first, seg.begin);
-  for (int64_t at = seg.begin; at < seg.end; at += C) {
-    const int n = (int)min((int64_t)C, seg.end - at);
-    __syncthreads();  // the chunk has landed
-    // the next chunk's loads run beside this one's products; always, the last one's again: a load under a condition
-    // would be waited for where the paths meet
-    Chunk next;
-    const int64_t ahead = at + C < seg.end ? at + C : at;
-    fetch(next, ahead);
-
-    if (active) {
-      if (PASS == kStates) {
-        float* to = p.chunk_state + ((chunk_number<C>(p.map, seg, at) * p.heads + head) * kv + v0);
-#pragma unroll
-        for (int t = 0; t < NV; ++t)
-#pragma unroll
-          for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
-              if (k < K && v < nv) to[k * p.V + v] = h[kt][t][r];
-            }
-      }
-      f32x4 z[NI][NV], o[NV][NI];
-#pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int x = 0; x < NI; ++x) z[x][t] = o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // K h and h' Q'
-#pragma unroll
-      for (int c = 0; c < NK; c += 2) {
-        Frag<E> b[NV][PF];
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          stack(h[c][t], h[c + 1][t], u);
-          split_parts(u, b[t]);
-        }
-        Frag<E> k[NI];
-#pragma unroll
-        for (int x = 0; x < NI; ++x) k[x] = frag_row_split(ks, x * 16 + l, c * 16);
-#pragma unroll
-        for (int q = PF - 1; q >= 0; --q)  // independent products next to each other
-#pragma unroll
-          for (int x = 0; x < NI; ++x)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) z[x][t] = mma(k[x], b[t][q], z[x][t]);
-        if (PASS == kOutputs)
-#pragma unroll
-          for (int x = 0; x < NI; ++x) {
-            const Frag<E> f = frag_row_split(qs, x * 16 + l, c * 16);
-#pragma unroll
-            for (int t = 0; t < NV; ++t) o[t][x] = mma(b[t][0], f, o[t][x]);
-          }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (PASS == kOutputs)
-#pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const float f = p.scale * rates.since[x * 16 + l];
-#pragma unroll
-          for (int t = 0; t < NV; ++t) o[t][x] *= f;
-        }
-      // the errors E = Z + N Z, Z = V - exp(G) K h
-      f32x4 e[NV][NI];
-#pragma unroll
-      for (int j = 0; j < NI; j += 2) {
-        const f32x4 f0 = rates.four(&rates.since[j * 16 + 4 * g]), f1 = rates.four(&rates.since[j * 16 + 16 + 4 * g]);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          frag_values(frag_col_split(vs, j * 16, vw + t * 16), u);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            z[j][t][r] = fmaf(-f0[r], z[j][t][r], u[r]);
-            z[j + 1][t][r] = fmaf(-f1[r], z[j + 1][t][r], u[4 + r]);
-          }
-          e[t][j] = z[j][t];
-          e[t][j + 1] = z[j + 1][t];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NI; j += 2) {
-        Frag<E> a[NI][PN];
-#pragma unroll
-        for (int x = j; x < NI; ++x)
-#pragma unroll
-          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys + (S::lower(x, j / 2) * PN + q) * S::kFragBytes);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          Frag<E> b[PN];
-          stack(z[j][t], z[j + 1][t], u);
-          split_parts(u, b);
-          j == 0 ? mma_parts<0, NI>(a, b, e[t]) : mma_parts<2, NI>(a, b, e[t]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (PASS == kStates) {
-        float* to = p.errors + ((seg.start + at) * p.heads + head) * p.V + v0;
-#pragma unroll
-        for (int x = 0; x < NI; ++x)
-#pragma unroll
-          for (int t = 0; t < NV; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int i = x * 16 + 4 * g + r, v = vw + t * 16 + l;
-              if (i < n && v < nv) to[(uint32_t)i * (uint32_t)(p.heads * p.V) + v] = e[t][x][r];
-            }
-      }
-      // U = b E; P U to the outputs, K' (w U) to the state
-#pragma unroll
-      for (int x = 0; x < NI; ++x) {
-        const f32x4 b = rates.four(&rates.beta[x * 16 + 4 * g]);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) e[t][x] *= b;
-      }
-      if (PASS == kOutputs) {
-#pragma unroll
-        for (int j = 0; j < NI; j += 2) {
-          // two parts: the scores and the state are rounded once, and so is all that an output is made of
-          constexpr int PU = PF > 1 ? 2 : 1;
-          Frag<E> a[NV][PU];
-#pragma unroll
-          for (int t = 0; t < NV; ++t) {
-            float u[8];
-            stack(e[t][j], e[t][j + 1], u);
-            split_parts(u, a[t]);
-          }
-#pragma unroll
-          for (int x = j; x < NI; ++x) {
-            const Frag<E> s = system_frag<E>(sys + S::kInverse + S::lower(x, j / 2) * S::kFragBytes);
-#pragma unroll
-            for (int q = PU - 1; q >= 0; --q)
-#pragma unroll
-              for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], s, o[t][x]);
-          }
-        }
-        E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-        put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
-        __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
-      }
-      const float all = rates.since[C - 1];
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int t = 0; t < NV; ++t) h[kt][t] *= all;
-#pragma unroll
-      for (int j = 0; j < NI; j += 2) {
-        Frag<E> b[NV][PF];
-        const f32x4 w0 = rates.four(&rates.left[j * 16 + 4 * g]), w1 = rates.four(&rates.left[j * 16 + 16 + 4 * g]);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          stack(e[t][j] * w0, e[t][j + 1] * w1, u);
-          split_parts(u, b[t]);
-        }
-#pragma unroll
-        for (int kt = 0; kt < NK; kt += 2) {
-          const Frag<E> k0 = frag_col_split(ks, j * 16, kt * 16), k1 = frag_col_split(ks, j * 16, kt * 16 + 16);
-#pragma unroll
-          for (int q = PF - 1; q >= 0; --q)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) {
-              h[kt][t] = mma(k0, b[t][q], h[kt][t]);
-              h[kt + 1][t] = mma(k1, b[t][q], h[kt + 1][t]);
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    __syncthreads();  // the chunk has been read
-    land(next, ahead);
-  }
-
-  float* to = PASS == kSegments ? (map ? p.seg_map + ((int64_t)slot * p.heads + head) * (KP * KP) : p.seg_state + sh)
-              : PASS == kOutputs && seg.last && p.state_out ? p.state_out + qh : nullptr;
-  if (to) {
-    const int rows = map ? KP : K, step = map ? KP : p.V;
-#pragma unroll
-    for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
-          if (k < rows && v < nv) to[(int64_t)k * step + v0 + v] = h[kt][t][r];
-        }
-  }
+template <typename E, int C, int KP, DeltaPass PASS, bool TINY>
+__global__ __launch_bounds__(256, 2) void delta_walk(DeltaParams p) {
+  __shared__ WalkTiles<E, C, KP, 64, PASS> lds;
+  walk<E, C, KP, 64, 1, PASS, TINY>(p, (uint32_t)block_id(), lds);
 }
 
 // One workgroup carries 32 value columns of a head along its sequence's segments: h <- M h + u forwards, h <- M' h + u
@@ -311,13 +26,17 @@ __global__ __launch_bounds__(VT * 4 / NV, 2) void delta_walk(DeltaParams p) {
 // write the final state over the initial one before the first has begun.  A wave owns 16 (at 256 keys 32) rows of the
 // result and reads those of M alone, the next segment's while this one's are multiplied; h goes round through LDS as
 // fragments in parts.  (With 16 columns per wave and all of M read by each, a step took 10 us where it takes 2.)
+template <int KP>
+constexpr int kCarryThreads = KP == 256 ? 512 : KP * 4;
+template <int KP>
+struct CarryTiles {
+  __attribute__((aligned(16))) uint32_t parts[2][KP / 32][kCarryColumns / 16][3][64][4];
+};
 template <int KP, bool REVERSE>
-__global__ __launch_bounds__(KP == 256 ? 512 : KP * 4) void delta_carry(CarryParams p) {
+__device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, CarryTiles<KP>& lds) {
   constexpr int NK = KP / 16, NW = NK < 8 ? NK : 8, OWN = NK / NW, NC = KP / 32, NV = kCarryColumns / 16, PF = 3;
-  __shared__ __attribute__((aligned(16))) uint32_t parts[2][NC][NV][PF][64][4];
+  auto& parts = lds.parts;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const uint32_t block = (uint32_t)block_id();
-  if (block >= p.blocks) return;
   const int tile = block % p.vtiles, head = block / p.vtiles % p.heads, s = block / p.vtiles / p.heads;
   int64_t slot, len;
   if (p.map.cu) {
@@ -430,20 +149,15 @@ __global__ __launch_bounds__(KP == 256 ? 512 : KP * 4) void delta_carry(CarryPar
   }
 }
 
-// Calls f with the padded key size and whether rows are tiny as constants.
-template <typename F>
-void with_keys(const DeltaPlan& pl, F f) {
-  using std::integral_constant;
-  if (pl.a.tiny)
-    f(integral_constant<int, 256>(), integral_constant<bool, true>());
-  else if (pl.a.kp == 32)
-    f(integral_constant<int, 32>(), integral_constant<bool, false>());
-  else if (pl.a.kp == 64)
-    f(integral_constant<int, 64>(), integral_constant<bool, false>());
-  else if (pl.a.kp == 128)
-    f(integral_constant<int, 128>(), integral_constant<bool, false>());
-  else
-    f(integral_constant<int, 256>(), integral_constant<bool, false>());
+// The carry of the states, or of both ways' in one grid: each alone leaves CUs idle.
+template <int KP, bool BOTH>
+__global__ __launch_bounds__(kCarryThreads<KP>) void delta_carry(CarryParams p, CarryParams r) {
+  __shared__ CarryTiles<KP> lds;
+  const uint32_t block = (uint32_t)block_id(), n = p.blocks;
+  if (block < n)
+    carry<KP, false>(p, block, lds);
+  else if (BOTH && block - n < n)
+    carry<KP, true>(r, block - n, lds);
 }
 
 template <typename E, int C, DeltaPass PASS>
@@ -453,7 +167,7 @@ hipError_t launch_walk(DeltaParams p, const DeltaPlan& pl, hipStream_t st) {
   p.blocks = (uint32_t)(pl.a.slots * p.heads);
   const int64_t blocks = spread_blocks(p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles);
   with_keys(pl, [&](auto kp, auto tiny) {
-    delta_walk<E, C, kp(), 64, 1, PASS, tiny()><<<grid_of(blocks, 256), dim3(256), 0, st>>>(p);
+    delta_walk<E, C, kp(), PASS, tiny()><<<grid_of(blocks, 256), dim3(256), 0, st>>>(p);
   });
   return hipGetLastError();
 }
@@ -525,7 +239,7 @@ DeltaPlan plan_delta_backward(int64_t sequences, int64_t tokens, int64_t heads, 
 
 int64_t delta_blocks(const DeltaPlan& pl, int64_t sequences, int64_t heads, int64_t value_dim) {
   const int64_t v = (value_dim + 63) / 64, k = (pl.a.kp + 63) / 64;
-  const int64_t walk = tok::spread_blocks(pl.a.slots * heads, (int)(v + k)), systems = pl.a.chunks * heads, carry = sequences * heads * ((value_dim + kCarryColumns - 1) / kCarryColumns);
+  const int64_t walk = spread_blocks(pl.a.slots * heads, (int)(2 * v + k)), systems = pl.a.chunks * heads, carry = 2 * sequences * heads * ((value_dim + kCarryColumns - 1) / kCarryColumns);
   return walk > systems ? (walk > carry ? walk : carry) : systems > carry ? systems : carry;
 }
 
@@ -568,20 +282,23 @@ DeltaParams delta_params(const DeltaArgs& a, const DeltaPlan& pl) {
 hipError_t launch_delta_segments(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st) {
   const hipError_t e = dtype == 1 ? launch_walk<uint16_t, 64, kSegments>(p, pl, st) : launch_walk<float, 32, kSegments>(p, pl, st);
   if (e != hipSuccess) return e;
-  CarryParams c{p.seg_state, p.seg_map, p.state_in, p.map, p.heads, p.K, p.V, 0, 0};
-  return launch_delta_carry(c, pl, false, st);
+  const CarryParams c{p.seg_state, p.seg_map, p.state_in, p.map, p.heads, p.K, p.V, 0, 0};
+  return launch_delta_carry(c, nullptr, pl, st);
 }
 
-hipError_t launch_delta_carry(CarryParams c, const DeltaPlan& pl, bool reverse, hipStream_t st) {
+hipError_t launch_delta_carry(CarryParams c, const CarryParams* back, const DeltaPlan& pl, hipStream_t st) {
   c.vtiles = (c.V + kCarryColumns - 1) / kCarryColumns;
   c.blocks = (uint32_t)((int64_t)c.map.sequences * c.heads * c.vtiles);
+  CarryParams r = back ? *back : c;
+  r.vtiles = c.vtiles;
+  r.blocks = c.blocks;
   with_keys(pl, [&](auto kp, auto) {
-    constexpr int threads = kp() == 256 ? 512 : kp() * 4;
-    const dim3 grid = grid_of(c.blocks, threads), block(threads);
-    if (reverse)
-      delta_carry<kp(), true><<<grid, block, 0, st>>>(c);
+    constexpr int threads = kCarryThreads<kp()>;
+    const dim3 grid = grid_of(back ? 2 * (int64_t)c.blocks : c.blocks, threads), block(threads);
+    if (back)
+      delta_carry<kp(), true><<<grid, block, 0, st>>>(c, r);
     else
-      delta_carry<kp(), false><<<grid, block, 0, st>>>(c);
+      delta_carry<kp(), false><<<grid, block, 0, st>>>(c, r);
   });
   return hipGetLastError();
 }
