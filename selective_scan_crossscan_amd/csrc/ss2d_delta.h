@@ -89,12 +89,12 @@ struct DeltaParams {
   char* systems;            // (chunk, head): inverse, scores; backward: inverse, transposed inverse and scores
   float* seg_state;         // (slot, head, K, V): what a segment adds, after the carry the state before it
   float* seg_map;           // (slot, head, KP, KP): the segment's map of the state before it
-  float* chunk_state;       // (chunk, head, KP, VP): the state before every chunk, 0 outside K and V
-  float* errors;            // (chunk, head, C, VP): E, 0 behind the chunk's tokens and outside V
+  float* chunk_state;       // (chunk, head, tile, KP, 64): the state before every chunk, 0 outside K and V
+  float* errors;            // (chunk, head, tile, C, 64): E, 0 behind the chunk's tokens and outside V
   SequenceMap map;          // segments
   SequenceMap chunk_map;    // segments of one chunk
   int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], b_stride[3];
-  int VP;  // values padded for the chunks' arrays
+  int tiles;                // of 64 value columns in the chunks' arrays
   int groups, heads, K, V, vtiles, ktiles;  // tiles of the pass's columns of values; of the segment maps' columns
   uint32_t blocks;          // workgroups; of a walk: units of a segment and head, each with its tiles
   float scale;
@@ -207,13 +207,11 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p, int n) {
   return x;
 }
 
-// A padded array's value at rows 16 t + r of a result tile: from a uniform base by a lane's own offset in bytes, the same
-// for all tiles and rows, so that an address takes no registers of its own.
-__device__ __forceinline__ uint32_t tile_bytes(int step, int column) {
-  return 4u * (uint32_t)(4 * ((threadIdx.x & 63) >> 4) * step + column);
-}
-__device__ __forceinline__ float* tile_at(float* base, int t, int r, int step, uint32_t bytes) {
-  return reinterpret_cast<float*>(reinterpret_cast<char*>(base + (t * 16 + r) * step) + bytes);
+// p, uniform, moved by a lane's own bytes: one register of an address, and what is added by constants goes into the
+// instruction (a sum of 32-bit indexes does not, and takes two registers for each).
+template <typename T>
+__device__ __forceinline__ T* by_bytes(T* p, uint32_t bytes) {
+  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
 }
 
 // Two result tiles stacked along their rows as the eight inner values of an operand.

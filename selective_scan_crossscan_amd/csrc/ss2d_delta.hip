@@ -16,7 +16,7 @@ namespace {
 constexpr int kCarryColumns = 32;
 
 template <typename E, int C, int KP, DeltaPass PASS, bool TINY>
-__global__ __launch_bounds__(256, 2) void delta_walk(DeltaParams p) {
+__global__ __launch_bounds__(256, TINY ? 1 : 2) void delta_walk(DeltaParams p) {
   __shared__ WalkTiles<E, C, KP, 64, PASS> lds;
   walk<E, C, KP, 64, 1, PASS, TINY>(p, (uint32_t)block_id(), lds);
 }
@@ -35,6 +35,7 @@ struct CarryTiles {
 template <int KP, bool REVERSE>
 __device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, CarryTiles<KP>& lds) {
   constexpr int NK = KP / 16, NW = NK < 8 ? NK : 8, OWN = NK / NW, NC = KP / 32, NV = kCarryColumns / 16, PF = 3;
+  constexpr bool AHEAD = kAhead<KP>;  // the next segment's M and u wait in registers
   auto& parts = lds.parts;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const int tile = block % p.vtiles, head = block / p.vtiles % p.heads, s = block / p.vtiles / p.heads;
@@ -56,30 +57,44 @@ __device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, Carr
   auto inside = [&](int a, int t, int r) { return row(a, r) < p.K && col(t) < p.V; };
   auto at = [&](int64_t i) { return (slot + (REVERSE ? n - 1 - i : i)) * p.heads + head; };
   f32x4 h[OWN][NV], add[OWN][NV];
-  float m[OWN][NC][8];
-  auto load = [&](int64_t i) {  // segment i's u and M
-    const float *u = p.seg + at(i) * kv, *map = p.seg_map + at(i) * (KP * KP);
+  float m[OWN][AHEAD ? NC : 1][8];
+  auto load_map = [&](int64_t i, int a, int c) {  // segment i's M, 32 columns of the wave's rows
+    const float* map = p.seg_map + at(i) * (KP * KP);
+    const int k = (wave + a * NW) * 16 + l;
+    float(&to)[8] = m[a][AHEAD ? c : 0];
+    if (REVERSE) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        to[r] = map[(c * 32 + 4 * g + r) * KP + k];
+        to[4 + r] = map[(c * 32 + 16 + 4 * g + r) * KP + k];
+      }
+    } else {
+      const float* x = map + k * KP + c * 32 + 4 * g;
+      stack(*reinterpret_cast<const f32x4*>(x), *reinterpret_cast<const f32x4*>(x + 16), to);
+    }
+  };
+  auto load = [&](int64_t i) {  // segment i's u, and M
+    const float* u = p.seg + at(i) * kv;
 #pragma unroll
     for (int a = 0; a < OWN; ++a) {
 #pragma unroll
       for (int t = 0; t < NV; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) add[a][t][r] = u[place(a, t, r)];
-      const int k = (wave + a * NW) * 16 + l;
+      if (AHEAD)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (REVERSE) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            m[a][c][r] = map[(c * 32 + 4 * g + r) * KP + k];
-            m[a][c][4 + r] = map[(c * 32 + 16 + 4 * g + r) * KP + k];
-          }
-        } else {
-          const float* x = map + k * KP + c * 32 + 4 * g;
-          stack(*reinterpret_cast<const f32x4*>(x), *reinterpret_cast<const f32x4*>(x + 16), m[a][c]);
-        }
-      }
+        for (int c = 0; c < NC; ++c) load_map(i, a, c);
     }
+  };
+  auto put = [&](int64_t i) {  // h before (behind) segment i
+    float* u = p.seg + at(i) * kv;
+#pragma unroll
+    for (int a = 0; a < OWN; ++a)
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (inside(a, t, r)) u[place(a, t, r)] = h[a][t][r];
   };
   load(0);
   const float* from = p.from ? p.from + ((int64_t)s * p.heads + head) * kv : nullptr;
@@ -93,15 +108,10 @@ __device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, Carr
         h[a][t][r] = inside(a, t, r) ? x : 0.f;
       }
   for (int64_t i = 0; i < n; ++i) {
-    float* u = p.seg + at(i) * kv;
-#pragma unroll
-    for (int a = 0; a < OWN; ++a)
-#pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (inside(a, t, r)) u[place(a, t, r)] = h[a][t][r];
-    if (i + 1 == n) break;
+    if (i + 1 == n) {
+      put(i);
+      break;
+    }
     auto& buffer = parts[i & 1];
 #pragma unroll
     for (int a = 0; a < OWN; ++a)
@@ -120,20 +130,30 @@ __device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, Carr
           }
         }
       }
-    Frag<uint16_t> f[OWN][NC][PF];
+    Frag<uint16_t> f[AHEAD ? NC : 1][OWN][PF];
+    if (AHEAD)
 #pragma unroll
-    for (int a = 0; a < OWN; ++a) {
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) split_parts(m[a][c], f[a][c]);
+        for (int a = 0; a < OWN; ++a) split_parts(m[a][c], f[AHEAD ? c : 0][a]);
+    __builtin_amdgcn_sched_barrier(0);
+    put(i);  // behind the uses of what was loaded before: a wait for those would be one for these stores too
+#pragma unroll
+    for (int a = 0; a < OWN; ++a)
 #pragma unroll
       for (int t = 0; t < NV; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) h[a][t][r] = inside(a, t, r) ? add[a][t][r] : 0.f;
-    }
     __syncthreads();  // h is whole; the buffer is next written behind the next barrier
-    load(i + 2 < n ? i + 1 : i);
+    if (AHEAD) load(i + 2 < n ? i + 1 : i);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c) {
+      if (!AHEAD)
+#pragma unroll
+        for (int a = 0; a < OWN; ++a) {
+          load_map(i, a, c);
+          split_parts(m[a][0], f[0][a]);
+        }
 #pragma unroll
       for (int t = 0; t < NV; ++t) {
         Frag<uint16_t> b[PF];
@@ -144,8 +164,11 @@ __device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, Carr
 #pragma unroll
           for (int q = 0; q <= x; ++q)
 #pragma unroll
-            for (int a = 0; a < OWN; ++a) h[a][t] = mma(f[a][c][q], b[x - q], h[a][t]);
+            for (int a = 0; a < OWN; ++a) h[a][t] = mma(f[AHEAD ? c : 0][a][q], b[x - q], h[a][t]);
       }
+      if (!AHEAD) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!AHEAD) load(i + 2 < n ? i + 1 : i);
   }
 }
 
@@ -182,7 +205,7 @@ DeltaPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t ke
   AttentionPlan& a = pl.a;
   const int64_t few = dtype == 1 ? 8 : 4;  // values in 16 bytes
   a.tiny = key_dim < few || value_dim < few;
-  a.kp = a.tiny ? 256 : key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
+  a.kp = a.tiny ? (key_dim <= 32 ? 32 : 256) : key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
   a.vt = 64;
   a.vtiles = (int)((value_dim + 63) / 64);
   const int64_t chunk = a.chunk = dtype == 1 ? 64 : 32;

@@ -70,7 +70,7 @@ __device__ __forceinline__ void put4_parts(Tile<float, R, CC, PAD> (&m)[1], int 
 template <typename E, int C, int KP, int NW, bool TINY>
 __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
   const DeltaParams& p = b.d;
-  constexpr int THREADS = NW * 64, NI = C / 16, NK = KP / 16, VT = 64, NV = VT / 16, PF = kFullParts<E>;
+  constexpr int THREADS = NW * 64, NI = C / 16, NK = KP / 16, VT = kArrayTile, NV = VT / 16, PF = kFullParts<E>;
   constexpr int OK = (NK + NW - 1) / NW;
   constexpr int PB = PF > 1 ? 2 : 1;  // parts of U and dZ towards dk, whose products round one operand only
   constexpr int JS = NW / NI < NI ? NW / NI : NI;  // waves that share 16 tokens' scores
@@ -108,14 +108,14 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
   if (n == 0) return;
   const int rep = p.heads / p.groups, group = head / rep, K = p.K;
   const int64_t at = (p.map.cu ? seg.start : 0) + seg.begin, sq = p.map.cu ? 0 : seg.s, token = seg.start + seg.begin;
-  const int64_t kv = (int64_t)KP * p.VP;
-  const float *hb = p.chunk_state + block * kv, *db = b.chunk_dstate + block * kv;
+  const int64_t place = (int64_t)block * p.tiles;  // the first tile of the chunks' arrays
   const E* vb = static_cast<const E*>(p.v) + sq * p.v_stride[0] + at * p.v_stride[1] + head * p.v_stride[2];
   const E* ob = static_cast<const E*>(b.d_o) + sq * b.do_stride[0] + at * b.do_stride[1] + head * b.do_stride[2];
   const int ti = threadIdx.x / TT, tc = threadIdx.x % TT * PC;  // this thread's token and columns
   const int it = wave % NI, share = wave / NI, i0 = it * 16 + l;
-  const float *eb = p.errors + (block * (int64_t)C + ti) * p.VP + tc, *fb = b.df + (block * (int64_t)C + ti) * p.VP + tc;
-  E* vto = static_cast<E*>(b.dv) + ((token + ti) * p.heads + head) * p.V + tc;
+  const uint32_t et = 4 * (ti * kArrayTile + tc);  // bytes into a tile of the chunks' arrays
+  E* vto = static_cast<E*>(b.dv) + (token * p.heads + head) * p.V;
+  const uint32_t vt = (uint32_t)ti * (uint32_t)(p.heads * p.V) + tc;  // 64 tokens' are under 2^32
 
   // a tile of 64 value columns on its way: two tiles' loads are in flight beside one's products
   struct Ahead {
@@ -124,28 +124,37 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
   };
   auto fetch = [&](Ahead& x, int v0) {
     const int nv = min(p.V - v0, VT);
-    x.d.load(ob + v0, b.do_stride[1], n, nv);
-    x.v.load(vb + v0, p.v_stride[1], n, nv);
+    if (kAhead<KP>) {
+      x.d.load(ob + v0, b.do_stride[1], n, nv);
+      x.v.load(vb + v0, p.v_stride[1], n, nv);
+    }
+    const int64_t at = (place + v0 / VT) * (C * kArrayTile);
+    const f32x4 *e = reinterpret_cast<const f32x4*>(by_bytes(p.errors + at, et)),
+                *f = reinterpret_cast<const f32x4*>(by_bytes(b.df + at, et));
 #pragma unroll
     for (int c = 0; c < PC / 4; ++c) {
-      x.e[c] = *reinterpret_cast<const f32x4*>(eb + v0 + 4 * c);
-      x.f[c] = *reinterpret_cast<const f32x4*>(fb + v0 + 4 * c);
+      x.e[c] = e[c];
+      x.f[c] = f[c];
     }
   };
   Ahead x;
   {
-    TileLoad<E, C, KP, 32, THREADS, TINY> q, k;
+    TileLoad<E, C, KP, 32, THREADS, TINY && KP == 32> q, k;
     q.load(static_cast<const E*>(p.q) + sq * p.q_stride[0] + at * p.q_stride[1] + group * p.q_stride[2], p.q_stride[1], n, K);
+    if (!kAhead<KP>) {
+      q.store(qs, n, K);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     k.load(static_cast<const E*>(p.k) + sq * p.k_stride[0] + at * p.k_stride[1] + group * p.k_stride[2], p.k_stride[1], n, K);
     const int64_t t = at + min(lane, n - 1);
     const float decay = p.g[sq * p.g_stride[0] + t * p.g_stride[1] + head * p.g_stride[2]];
     const float beta = p.beta[sq * p.b_stride[0] + t * p.b_stride[1] + head * p.b_stride[2]];
-    fetch(x, 0);
+    if (kAhead<KP>) fetch(x, 0);
     if (wave == 0) {
       if (lane < C) bs[lane] = lane < n ? beta : 0.f;
       scan_decays<C>(lane < n ? decay : 0.f, dec);
     }
-    q.store(qs, n, K);
+    if (kAhead<KP>) q.store(qs, n, K);
     k.store(ks, n, K);
   }
 
@@ -157,26 +166,33 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
 #pragma unroll
     for (int a = 0; a < OK; ++a) dq[a][0][i] = dk[a][0][i] = dz[a][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float xsum = 0.f, bsum = 0.f, vsum = 0.f;
-  for (int v0 = 0; v0 < p.V; v0 += VT) {
-    const int nv = min(p.V - v0, VT);
-    // the state and its gradient: rows k of the wave's key columns, four values at a time
-    f32x4 h[OK][NV], d[OK][NV];
+  // the state and its gradient: rows k of the wave's key columns, four values at a time
+  constexpr int HS = kAhead<KP> ? OK : 1;  // of all key columns, or one after the other
+  f32x4 h[HS][NV], d[HS][NV];
+  auto fetch_states = [&](int v0, int from) {
 #pragma unroll
-    for (int a = 0; a < OK; ++a) {
-      const int row = ((wave + a * NW) % NK * 16 + l) * p.VP + v0 + 4 * g;
+    for (int a = 0; a < HS; ++a) {
+      const int64_t at = (place + v0 / VT) * (KP * kArrayTile);
+      const uint32_t row = 4 * (((wave + (from + a) * NW) % NK * 16 + l) * kArrayTile + 4 * g);
+      const f32x4 *hp = reinterpret_cast<const f32x4*>(by_bytes(p.chunk_state + at, row)),
+                  *dp = reinterpret_cast<const f32x4*>(by_bytes(b.chunk_dstate + at, row));
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        h[a][c] = *reinterpret_cast<const f32x4*>(hb + row + c * 16);
-        d[a][c] = *reinterpret_cast<const f32x4*>(db + row + c * 16);
+        h[a][c] = hp[4 * c];
+        d[a][c] = dp[4 * c];
       }
     }
+  };
+  if (kAhead<KP>) fetch_states(0, 0);
+  for (int v0 = 0; v0 < p.V; v0 += VT) {
+    const int nv = min(p.V - v0, VT);
+    if (!kAhead<KP>) fetch(x, v0);
     __syncthreads();  // the tiles before have been read, the decays are there
     f32x4 zs[PC / 4];
     {
       const float be = bs[ti];
 #pragma unroll
       for (int c = 0; c < PC / 4; ++c) {
-        const int left = ti < n ? nv - tc - 4 * c : 0;
         const f32x4 z = x.f[c] * be;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -184,10 +200,17 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
         }
         put4_parts(m.v.u, ti * m.v.u[0].stride + tc + 4 * c, x.e[c] * be);
         put4_parts(m.v.z, ti * m.v.z[0].stride + tc + 4 * c, z);
-        if (left > 0) store4(vto + v0 + 4 * c, left, z);
         zs[c] = z;
       }
+      if (!kAhead<KP>) {  // tile by tile, with few registers
+        __builtin_amdgcn_sched_barrier(0);
+        x.d.load(ob + v0, b.do_stride[1], n, nv);
+      }
       x.d.store(m.v.d, n, nv);
+      if (!kAhead<KP>) {
+        __builtin_amdgcn_sched_barrier(0);
+        x.v.load(vb + v0, p.v_stride[1], n, nv);
+      }
       x.v.store(vs, n, nv);
     }
     __syncthreads();
@@ -197,7 +220,54 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) vsum = fmaf(zs[c][r], v[r], vsum);
     }
-    fetch(x, v0 + VT < p.V ? v0 + VT : v0);  // always, the last one's again: a load under a condition would be waited for
+#pragma unroll
+    for (int a = 0; a < OK; ++a)
+      if (wave + a * NW < NK) {
+        const int at = kAhead<KP> ? a : 0;
+        if (!kAhead<KP>) {
+          __builtin_amdgcn_sched_barrier(0);
+          fetch_states(v0, a);
+        }
+#pragma unroll
+        for (int c = 0; c < NV; c += 2) {
+          float u[8];
+          Frag<E> fh[PF], fd[1];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            xsum = fmaf(h[at][c][r], d[at][c][r], xsum);
+            xsum = fmaf(h[at][c + 1][r], d[at][c + 1][r], xsum);
+          }
+          stack(h[at][c], h[at][c + 1], u);
+          split_parts(u, fh);
+          stack(d[at][c], d[at][c + 1], u);
+          split_parts(u, fd);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const Frag<E> o = frag_row_split(m.v.d, i * 16 + l, c * 16);
+#pragma unroll
+            for (int q = 0; q < PB; ++q) {
+              dk[a][0][i] = mma(fd[0], frag_row_split(m.v.u[PB - 1 - q], i * 16 + l, c * 16), dk[a][0][i]);
+              dz[a][i] = mma(fh[0], frag_row_split(m.v.z[PB - 1 - q], i * 16 + l, c * 16), dz[a][i]);
+              dq[a][0][i] = mma(fh[PF - 1 - q], o, dq[a][0][i]);
+            }
+            if (PF > PB) dq[a][0][i] = mma(fh[0], o, dq[a][0][i]);
+            if (!kAhead<KP>) __builtin_amdgcn_sched_barrier(0);  // or their registers add up and spill
+          }
+        }
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    // behind the uses of what was loaded before: a wait for that would be one for these stores and loads too
+#pragma unroll
+    for (int c = 0; c < PC / 4; ++c) {
+      const int left = ti < n ? nv - tc - 4 * c : 0;
+      if (left > 0) store4(vto + v0 + vt + 4 * c, left, zs[c]);
+    }
+    const int ahead = v0 + VT < p.V ? v0 + VT : v0;  // always, the last one's again: a load under a condition would be waited for
+    if (kAhead<KP>) {
+      fetch(x, ahead);
+      fetch_states(ahead, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     // (do . u) and (dz . u), transposed: rows j, columns i
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -219,36 +289,10 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
             for (int q = 0; q <= s; ++q) sy[i] = mma(fu[q], fz[s - q], sy[i]);
         }
     }
-#pragma unroll
-    for (int a = 0; a < OK; ++a)
-      if (wave + a * NW < NK) {
-#pragma unroll
-        for (int c = 0; c < NV; c += 2) {
-          float u[8];
-          Frag<E> fh[PF], fd[1];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            xsum = fmaf(h[a][c][r], d[a][c][r], xsum);
-            xsum = fmaf(h[a][c + 1][r], d[a][c + 1][r], xsum);
-          }
-          stack(h[a][c], h[a][c + 1], u);
-          split_parts(u, fh);
-          stack(d[a][c], d[a][c + 1], u);
-          split_parts(u, fd);
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const Frag<E> o = frag_row_split(m.v.d, i * 16 + l, c * 16);
-#pragma unroll
-            for (int q = 0; q < PB; ++q) {
-              dk[a][0][i] = mma(fd[0], frag_row_split(m.v.u[PB - 1 - q], i * 16 + l, c * 16), dk[a][0][i]);
-              dz[a][i] = mma(fh[0], frag_row_split(m.v.z[PB - 1 - q], i * 16 + l, c * 16), dz[a][i]);
-              dq[a][0][i] = mma(fh[PF - 1 - q], o, dq[a][0][i]);
-            }
-            if (PF > PB) dq[a][0][i] = mma(fh[0], o, dq[a][0][i]);
-          }
-        }
-      }
   }
+  // The lane anew, from the hardware: kept over the values' loop its parts would be spilled there.
+  const int at_lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+  const int eg = at_lane >> 4, el = at_lane & 15, ei = it * 16 + el;
   // sums over a token's threads
 #pragma unroll
   for (int s = 1; s < TT; s <<= 1) {
@@ -264,16 +308,16 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
   for (int i = 0; i < NS; ++i) {
     const int jt = i * JS + share;
     if (share < JS && jt <= (it | 1)) {  // the last may be all masked: pairs are read
-      const f32x4 e = dec.between4(i0, jt * 16 + 4 * g);
+      const f32x4 e = dec.between4(ei, jt * 16 + 4 * eg);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int j = jt * 16 + 4 * g + r;
+        const int j = jt * 16 + 4 * eg + r;
         const float x = sx[i][r] * (p.scale * e[r]), y = -sy[i][r] * e[r];
-        sx[i][r] = j <= i0 ? x : 0.f;
-        sy[i][r] = j < i0 ? y : 0.f;
+        sx[i][r] = j <= ei ? x : 0.f;
+        sy[i][r] = j < ei ? y : 0.f;
       }
-      put4_parts(m.s.x, i0 * m.s.x[0].stride + jt * 16 + 4 * g, sx[i]);
-      put4(&m.s.y.e[i0 * m.s.y.stride + jt * 16 + 4 * g], sy[i]);
+      put4_parts(m.s.x, ei * m.s.x[0].stride + jt * 16 + 4 * eg, sx[i]);
+      put4(&m.s.y.e[ei * m.s.y.stride + jt * 16 + 4 * eg], sy[i]);
     }
   }
   __syncthreads();
@@ -286,7 +330,7 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
       const int k0 = (wave + a * NW) * 16;
 #pragma unroll
       for (int x = 0; x < NI; ++x) {
-        const int i = x * 16 + l;
+        const int i = x * 16 + el;
         const float since = __builtin_amdgcn_exp2f(dec.whole[i] + dec.frac[i]);
         dq[a][0][x] *= p.scale * since;
         dk[a][0][x] = dk[a][0][x] * dec.between(C - 1, i) - dz[a][x] * since;
@@ -298,8 +342,8 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
         for (int x = 0; x < NI; ++x) {
           if (x >= j) {  // tokens j .. j + 31 before x
 #pragma unroll
-            for (int q = PF - 1; q >= 0; --q) dq[a][0][x] = mma(fk, frag_row_split(m.s.x[q], x * 16 + l, j * 16), dq[a][0][x]);
-            dk[a][0][x] = mma(fk, frag_row_split(m.s.y, x * 16 + l, j * 16), dk[a][0][x]);
+            for (int q = PF - 1; q >= 0; --q) dq[a][0][x] = mma(fk, frag_row_split(m.s.x[q], x * 16 + el, j * 16), dq[a][0][x]);
+            dk[a][0][x] = mma(fk, frag_row_split(m.s.y, x * 16 + el, j * 16), dk[a][0][x]);
           }
           if (x < j + 2) {  // tokens j .. j + 31 behind x
             dk[a][0][x] = mma(fq, frag_col_split(m.s.x[0], j * 16, x * 16), dk[a][0][x]);
@@ -311,38 +355,39 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
       for (int x = 0; x < NI; ++x)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          fsum[x] = fmaf(load1(&qs.e[(x * 16 + l) * qs.stride + k0 + 4 * g + r]), dq[a][0][x][r], fsum[x]);
+          fsum[x] = fmaf(load1(&qs.e[(x * 16 + el) * qs.stride + k0 + 4 * eg + r]), dq[a][0][x][r], fsum[x]);
       const int64_t stride = (int64_t)p.groups * K, part = (head % rep) * p.map.tokens;
       auto put = [&](void* whole, float* parts, const f32x4 (&x)[1][NI]) {
         if (parts)
-          put_rows<NI, 1>(parts + ((part + token) * p.groups + group) * K, stride, n, K, k0 + 4 * g, 0, l, x);
+          put_rows<NI, 1>(parts + ((part + token) * p.groups + group) * K, stride, n, K, k0 + 4 * eg, 0, el, x);
         else
-          put_rows<NI, 1>(static_cast<E*>(whole) + (token * p.groups + group) * K, stride, n, K, k0 + 4 * g, 0, l, x);
+          put_rows<NI, 1>(static_cast<E*>(whole) + (token * p.groups + group) * K, stride, n, K, k0 + 4 * eg, 0, el, x);
       };
       put(b.dq, b.dq_part, dq[a]);
       put(b.dk, b.dk_part, dk[a]);
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
   for (int x = 0; x < NI; ++x) {
     fsum[x] = across_rows(fsum[x]);
-    if (g == 0) fs[wave][x * 16 + l] = fsum[x];
+    if (eg == 0) fs[wave][x * 16 + el] = fsum[x];
   }
   xsum = wave_sum(xsum);
-  if (lane == 0) xs[wave] = xsum;
+  if (at_lane == 0) xs[wave] = xsum;
   __syncthreads();
   if (wave == 0) {  // the chunk's decay gradients
     float f = 0.f, x = 0.f, y = 0.f;
-    if (lane < n) {
+    if (at_lane < n) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w) f += fs[w][lane];
-      f -= vd[lane];
+      for (int w = 0; w < NW; ++w) f += fs[w][at_lane];
+      f -= vd[at_lane];
     }
 #pragma unroll
     for (int w = 0; w < NW; ++w) x += xs[w];
-    for (int i = lane; i < b.columns; i += 64) y += b.inner[block * (int64_t)b.columns + i];
+    for (int i = at_lane; i < b.columns; i += 64) y += b.inner[block * (int64_t)b.columns + i];
     x = fmaf(x, __builtin_amdgcn_exp2f(dec.whole[C - 1] + dec.frac[C - 1]), wave_sum(y));
-    f = __shfl(wave_scan(__shfl(f, 63 - lane)), 63 - lane);  // from a token on
-    if (lane < n) b.dg[(token + lane) * p.heads + head] = f + x;
+    f = __shfl(wave_scan(__shfl(f, 63 - at_lane)), 63 - at_lane);  // from a token on
+    if (at_lane < n) b.dg[(token + at_lane) * p.heads + head] = f + x;
   }
 }
 
@@ -475,7 +520,7 @@ hipError_t launch_delta_backward(const DeltaBackwardArgs& a, const DeltaPlan& pl
   p.seg_map = at(rg.seg_map);
   p.chunk_state = at(rg.chunk_state);
   p.errors = at(rg.errors);
-  p.VP = (int)padded_values(p.V, pl);
+  p.tiles = (int)padded_values(p.V, pl) / kArrayTile;
   b.d_o = a.d_o;
   for (int i = 0; i < 3; ++i) b.do_stride[i] = a.do_stride[i];
   b.dstate_out = a.dstate_out;

@@ -242,8 +242,8 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
 template <typename E, int C, bool BACK>
 void launch(const DeltaParams& p, const DeltaPlan& pl, hipStream_t st) {
   const dim3 grid = grid_of(p.blocks, C * 4), block(C * 4);
-  if (pl.a.tiny)
-    delta_systems<E, C, 256, BACK, true><<<grid, block, 0, st>>>(p);
+  if (pl.a.tiny && pl.a.kp == 32)
+    delta_systems<E, C, 32, BACK, true><<<grid, block, 0, st>>>(p);  // keys of 16 bytes or more need no care here
   else if (pl.a.kp == 32)
     delta_systems<E, C, 32, BACK, false><<<grid, block, 0, st>>>(p);
   else if (pl.a.kp == 64)

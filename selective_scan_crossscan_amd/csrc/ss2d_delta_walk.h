@@ -11,6 +11,17 @@ namespace {
 
 using namespace tok;
 
+constexpr int kArrayTile = 64;  // columns of a tile of the chunks' arrays
+// Whether the next chunk's loads wait in registers while one is worked on.  256 keys leave no registers for that, and
+// are loaded when the chunk before has been read.
+template <int KP>
+constexpr bool kAhead = KP <= 128;
+
+// Bytes for pieces of 16 by all threads: every thread writes all of its own, those behind the end into room that is not
+// read.  No condition there, on purpose: the compiler has stored spilled registers before it let all threads go on behind
+// one, and read them back for all.
+constexpr int whole_pieces(int bytes, int threads) { return (bytes + 16 * threads - 1) / (16 * threads) * (16 * threads); }
+
 enum DeltaPass { kOutputs, kSegments, kStates };
 
 template <typename E, int C, int KP, int VT, DeltaPass PASS>
@@ -19,7 +30,7 @@ struct WalkTiles {
   Tile<E, PASS == kOutputs ? C : 1, KP> qs;
   Tile<E, C, KP, 16> ks;
   Tile<E, C, VT, 32> vs;
-  __attribute__((aligned(16))) char sys[PASS == kOutputs ? S::kForward : S::kInverse];
+  __attribute__((aligned(16))) char sys[whole_pieces(PASS == kOutputs ? S::kForward : S::kInverse, 256)];
   Rates<C> rates;
 };
 template <typename E, int C, int KP, int VT, int NV, DeltaPass PASS, bool TINY>
@@ -35,6 +46,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   auto& sys = lds.sys;
   auto& rates = lds.rates;
 
+  static_assert(PASS != kStates || VT == kArrayTile, "the chunks' arrays are in this walk's tiles");
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   uint32_t unit, at_tile;
   if (!spread(block, p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles, unit, at_tile)) return;
@@ -47,8 +59,8 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = (map ? tile - p.vtiles : tile) * VT, nv = min((map ? KP : p.V) - v0, VT);
   const int vw = wave * 16 * NV;
+  const uint32_t lane_at = 4 * (4 * g * kArrayTile + vw + l);  // bytes into a tile of the chunks' arrays
   const bool active = PASS == kStates || vw < nv;  // the chunks' arrays are written whole
-  const uint32_t lane_bytes = tile_bytes(p.VP, vw + l);
   const int64_t token0 = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
   const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + token0 * p.q_stride[1] + group * p.q_stride[2];
   const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + token0 * p.k_stride[1] + group * p.k_stride[2];
@@ -60,17 +72,14 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   const int64_t sstep = p.heads * p.system_stride;
 
   struct Chunk {
-    TileLoad<E, PASS == kOutputs ? C : 1, KP, 16, THREADS, TINY> q;
-    TileLoad<E, C, KP, 16, THREADS, TINY> k;
+    TileLoad<E, PASS == kOutputs ? C : 1, KP, 16, THREADS, TINY && KP == 32> q;
+    TileLoad<E, C, KP, 16, THREADS, TINY && KP == 32> k;
     TileLoad<E, C, VT, 32, THREADS, TINY> v;
     uint4 s[kPieces];
     float g, b;
   };
-  auto fetch = [&](Chunk& x, int64_t at) {
+  auto fetch_rest = [&](Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-    if (PASS == kOutputs) x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
-    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
-    if (!map) x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
     const char* from = sb + (at - seg.begin) / C * sstep;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
@@ -79,19 +88,47 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     x.g = gb[t * p.g_stride[1]];
     x.b = bb[t * p.b_stride[1]];
   };
+  auto land_rest = [&](const Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
+    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
+  };
+  auto fetch = [&](Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+    if (PASS == kOutputs) x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    if (!map) x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
+    fetch_rest(x, at);
+  };
   auto land = [&](const Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
     if (PASS == kOutputs) x.q.store(qs, n, K);
     x.k.store(ks, n, K);
     if (!map) x.v.store(vs, n, nv);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (kSystem / 16 % THREADS == 0 || threadIdx.x + i * THREADS < kSystem / 16)
-        *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
-    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
+    land_rest(x, at);
+  };
+  auto bring = [&](int64_t at) {  // tile by tile, with few registers
+    const int n = (int)min((int64_t)C, seg.end - at);
+    Chunk x;
+    if (PASS == kOutputs) {
+      x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+      x.q.store(qs, n, K);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    x.k.store(ks, n, K);
+    __builtin_amdgcn_sched_barrier(0);
+    if (!map) {
+      x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
+      x.v.store(vs, n, nv);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_rest(x, at);
+    land_rest(x, at);
   };
   Chunk first;  // on its way while the state is read
-  if (seg.begin < seg.end) fetch(first, seg.begin);
+  if (kAhead<KP> && seg.begin < seg.end) fetch(first, seg.begin);
 
   // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
   f32x4 h[NK][NV];
@@ -117,7 +154,12 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   }
   if (map)
     for (int i = threadIdx.x; i < C * vs.stride; i += THREADS) vs.e[i] = (E)0;
-  if (seg.begin < seg.end) land(first, seg.begin);
+  if (seg.begin < seg.end) {
+    if (kAhead<KP>)
+      land(first, seg.begin);
+    else
+      bring(seg.begin);
+  }
   for (int64_t at = seg.begin; at < seg.end; at += C) {
     const int n = (int)min((int64_t)C, seg.end - at);
     __syncthreads();  // the chunk has landed
@@ -125,19 +167,20 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     // would be waited for where the paths meet
     Chunk next;
     const int64_t ahead = at + C < seg.end ? at + C : at;
-    fetch(next, ahead);
+    if (kAhead<KP>) fetch(next, ahead);
 
+    f32x4 o[NV][NI];
     if (active) {
       if (PASS == kStates) {
-        float* to = p.chunk_state + ((chunk_number<C>(p.map, seg, at) * p.heads + head) * KP * p.VP + v0);
+        float* to = by_bytes(p.chunk_state + ((chunk_number<C>(p.map, seg, at) * p.heads + head) * p.tiles + tile) * (KP * kArrayTile), lane_at);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int t = 0; t < NV; ++t) *tile_at(to + t * 16, kt, r, p.VP, lane_bytes) = h[kt][t][r];
+            for (int t = 0; t < NV; ++t) to[(kt * 16 + r) * kArrayTile + t * 16] = h[kt][t][r];
       }
-      f32x4 z[NI][NV], o[NV][NI];
+      f32x4 z[NI][NV];
 #pragma unroll
       for (int t = 0; t < NV; ++t)
 #pragma unroll
@@ -213,13 +256,13 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
         __builtin_amdgcn_sched_barrier(0);
       }
       if (PASS == kStates) {
-        float* to = p.errors + ((chunk_number<C>(p.map, seg, at) * p.heads + head) * C * p.VP + v0);
+        float* to = by_bytes(p.errors + ((chunk_number<C>(p.map, seg, at) * p.heads + head) * p.tiles + tile) * (C * kArrayTile), lane_at);
 #pragma unroll
         for (int x = 0; x < NI; ++x)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int t = 0; t < NV; ++t) *tile_at(to + t * 16, x, r, p.VP, lane_bytes) = e[t][x][r];
+            for (int t = 0; t < NV; ++t) to[(x * 16 + r) * kArrayTile + t * 16] = e[t][x][r];
       }
       // U = b E; P U to the outputs, K' (w U) to the state
 #pragma unroll
@@ -249,9 +292,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
               for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], s, o[t][x]);
           }
         }
-        E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-        put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
-        __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
+        __builtin_amdgcn_sched_barrier(0);
       }
       const float all = rates.since[C - 1];
 #pragma unroll
@@ -283,7 +324,16 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
       }
     }
     __syncthreads();  // the chunk has been read
-    land(next, ahead);
+    if (kAhead<KP>)
+      land(next, ahead);
+    else
+      bring(ahead);
+    // Outputs leave last: they are stored under conditions, and the loads before a store of which it is not known whether
+    // it is made are only known to have arrived when the store has.
+    if (PASS == kOutputs && active) {
+      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
+      put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
+    }
   }
 
   float* to = PASS == kSegments ? (map ? p.seg_map + ((int64_t)slot * p.heads + head) * (KP * KP) : p.seg_state + sh)
@@ -308,8 +358,8 @@ struct BackParams {
   int64_t do_stride[3];
   const float* dstate_out;  // or null
   float* seg_dstate;        // (slot, head, K, V): what a segment adds, after the carry the gradient behind it
-  float* chunk_dstate;      // (chunk, head, KP, VP): D behind every chunk
-  float* df;                // (chunk, head, C, VP)
+  float* chunk_dstate;      // (chunk, head, tile, KP, 64): D behind every chunk
+  float* df;                // (chunk, head, tile, C, 64)
   float* inner;             // (chunk, head, 16-column tile): parts of sum_j u_j . (w K D)_j
   void *dq, *dk, *dv;
   float *dq_part, *dk_part;  // (part, token, group, K), or null: dq and dk themselves
@@ -325,7 +375,7 @@ struct BackTiles {
   Tile<E, C, KP, 32> qs;
   Tile<E, C, KP, 16> ks;
   Tile<E, C, VT, 32> ds;
-  __attribute__((aligned(16))) char sys[S::kBackward - S::kInverse];  // the transposed inverse and P'
+  __attribute__((aligned(16))) char sys[whole_pieces(S::kBackward - S::kInverse, VT * 4)];  // the transposed inverse and P'
   Rates<C> rates;
 };
 template <typename E, int C, int KP, int VT, bool SUM, bool TINY>
@@ -352,8 +402,10 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
   if (SUM && seg.begin == 0) return;  // of no use
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), v = wave * 16 + l;
+  // in the chunks' arrays: this wave's tile, this lane's bytes into it
+  const int array_tile = v0 / kArrayTile + wave * 16 / kArrayTile;
+  const uint32_t lane_at = 4 * (4 * g * kArrayTile + wave * 16 % kArrayTile + l);
   const bool active = !SUM || wave * 16 < nv;  // the chunks' arrays are written whole
-  const uint32_t lane_bytes = tile_bytes(p.VP, v);
   const int64_t token0 = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
   const E* qb = static_cast<const E*>(p.q) + sq * p.q_stride[0] + token0 * p.q_stride[1] + group * p.q_stride[2];
   const E* kb = static_cast<const E*>(p.k) + sq * p.k_stride[0] + token0 * p.k_stride[1] + group * p.k_stride[2];
@@ -365,17 +417,14 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
   const int64_t sstep = p.heads * p.system_stride;
 
   struct Chunk {
-    TileLoad<E, C, KP, 32, THREADS, TINY> q;
-    TileLoad<E, C, KP, 16, THREADS, TINY> k;
+    TileLoad<E, C, KP, 32, THREADS, TINY && KP == 32> q;
+    TileLoad<E, C, KP, 16, THREADS, TINY && KP == 32> k;
     TileLoad<E, C, VT, 32, THREADS, TINY> d;
     uint4 s[kPieces];
     float g, b;
   };
-  auto fetch = [&](Chunk& x, int64_t at) {
+  auto fetch_rest = [&](Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-    x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
-    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
-    x.d.load(db + at * b.do_stride[1], b.do_stride[1], n, nv);
     const char* from = sb + (at - seg.begin) / C * sstep;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
@@ -384,20 +433,44 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
     x.g = gb[t * p.g_stride[1]];
     x.b = bb[t * p.b_stride[1]];
   };
+  auto land_rest = [&](const Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
+    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
+  };
+  auto fetch = [&](Chunk& x, int64_t at) {
+    const int n = (int)min((int64_t)C, seg.end - at);
+    x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    x.d.load(db + at * b.do_stride[1], b.do_stride[1], n, nv);
+    fetch_rest(x, at);
+  };
   auto land = [&](const Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
     x.q.store(qs, n, K);
     x.k.store(ks, n, K);
     x.d.store(ds, n, nv);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (kSystem / 16 % THREADS == 0 || threadIdx.x + i * THREADS < kSystem / 16)
-        *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
-    if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
+    land_rest(x, at);
+  };
+  auto bring = [&](int64_t at) {  // tile by tile, with few registers
+    const int n = (int)min((int64_t)C, seg.end - at);
+    Chunk x;
+    x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
+    x.q.store(qs, n, K);
+    __builtin_amdgcn_sched_barrier(0);
+    x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
+    x.k.store(ks, n, K);
+    __builtin_amdgcn_sched_barrier(0);
+    x.d.load(db + at * b.do_stride[1], b.do_stride[1], n, nv);
+    x.d.store(ds, n, nv);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_rest(x, at);
+    land_rest(x, at);
   };
   const int64_t chunks = (seg.end - seg.begin + C - 1) / C;
   Chunk first;  // on its way while the gradient is read
-  if (chunks > 0) fetch(first, seg.begin + (chunks - 1) * C);
+  if (kAhead<KP> && chunks > 0) fetch(first, seg.begin + (chunks - 1) * C);
 
   // D: rows 16 kt + 4 g + r, column v
   f32x4 d[NK];
@@ -411,31 +484,37 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
       const float x = from ? from[(int64_t)min(k, K - 1) * p.V + v0 + min(v, nv - 1)] : 0.f;
       d[kt][r] = k < K && v < nv ? x : 0.f;
     }
-  if (chunks > 0) land(first, seg.begin + (chunks - 1) * C);
+  if (chunks > 0) {
+    if (kAhead<KP>)
+      land(first, seg.begin + (chunks - 1) * C);
+    else
+      bring(seg.begin + (chunks - 1) * C);
+  }
   for (int64_t c = chunks - 1; c >= 0; --c) {
     const int64_t at = seg.begin + c * C;
     __syncthreads();  // the chunk has landed
-    const int64_t chunk = (chunk0 + c) * p.heads + head, rows = chunk * C * p.VP + v0;
+    const int64_t chunk = (chunk0 + c) * p.heads + head, place = chunk * p.tiles + array_tile;
     // The errors before the next chunk's loads and D's stores, all of which would be waited for with them otherwise
     // (memory operations are counted in order).
     f32x4 e[NI];
+    const float* errors = by_bytes(p.errors + place * (C * kArrayTile), lane_at);
     if (!SUM)
 #pragma unroll
       for (int x = 0; x < NI; ++x)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) e[x][r] = *tile_at(p.errors + rows, x, r, p.VP, lane_bytes);
+        for (int r = 0; r < 4; ++r) e[x][r] = errors[(x * 16 + r) * kArrayTile];
     __builtin_amdgcn_sched_barrier(0);
     Chunk next;  // as in the forward
     const int64_t ahead = c > 0 ? at - C : at;
-    fetch(next, ahead);
+    if (kAhead<KP>) fetch(next, ahead);
     __builtin_amdgcn_sched_barrier(0);
     if (active) {
       if (!SUM) {
-        float* to = b.chunk_dstate + chunk * KP * p.VP + v0;
+        float* to = by_bytes(b.chunk_dstate + place * (KP * kArrayTile), lane_at);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) *tile_at(to, kt, r, p.VP, lane_bytes) = d[kt][r];
+          for (int r = 0; r < 4; ++r) to[(kt * 16 + r) * kArrayTile] = d[kt][r];
       }
       // dU = w K D + P' dO
       f32x4 u[NI];
@@ -466,8 +545,8 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
 #pragma unroll
           for (int r = 0; r < 4; ++r) s = v < nv ? fmaf(be[r] * e[x][r], u[x][r], s) : s;
         }
-        s = wave_sum(s);
-        if (lane == 0) b.inner[chunk * b.columns + vt * NW + wave] = s;
+        s = __shfl(wave_sum(s), 0);
+        b.inner[chunk * b.columns + vt * NW + wave] = s;  // by all lanes, which have the same sum
       }
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
@@ -496,11 +575,11 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
         j == 0 ? mma_parts<0, 2>(a, f, z) : mma_parts<0, NI>(a, f, z);
       }
       if (!SUM) {
-        float* to = b.df + rows;
+        float* to = by_bytes(b.df + place * (C * kArrayTile), lane_at);
 #pragma unroll
         for (int x = 0; x < NI; ++x)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) *tile_at(to, x, r, p.VP, lane_bytes) = z[x][r];
+          for (int r = 0; r < 4; ++r) to[(x * 16 + r) * kArrayTile] = z[x][r];
       }
       __builtin_amdgcn_sched_barrier(0);
       // D for the chunk before
@@ -542,7 +621,10 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
       }
     }
     __syncthreads();  // the chunk has been read
-    land(next, ahead);
+    if (kAhead<KP>)
+      land(next, ahead);
+    else
+      bring(ahead);
   }
   float* to = SUM ? b.seg_dstate + sh : seg.begin == 0 && b.dstate_in ? b.dstate_in + qh : nullptr;
   if (to)
@@ -555,11 +637,13 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
       }
 }
 
-// Calls f with the padded key size and whether rows are tiny as constants.
+// Calls f with the padded key size and whether rows are tiny as constants (the keys' only at 32 keys).
 template <typename F>
 void with_keys(const DeltaPlan& pl, F f) {
   using std::integral_constant;
-  if (pl.a.tiny)
+  if (pl.a.tiny && pl.a.kp == 32)
+    f(integral_constant<int, 32>(), integral_constant<bool, true>());
+  else if (pl.a.tiny)
     f(integral_constant<int, 256>(), integral_constant<bool, true>());
   else if (pl.a.kp == 32)
     f(integral_constant<int, 32>(), integral_constant<bool, false>());

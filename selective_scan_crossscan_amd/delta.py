@@ -8,22 +8,67 @@ as in tokens.py; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from ._lib import lib
-from .tokens import _attention_sizes, _call, _code, _empty, _on_stream, _ptr, _require, _workspace
+from ._lib import check, lib
+from .tokens import _call, _code, _empty, _on_stream, _ptr, _require, _workspace
 
 _DELTA_SIZES = ctypes.c_int64 * 24  # ss2d_delta_sizes: linear attention's 21, beta's three strides
 _QK_SIZES = ctypes.c_int64 * 19     # ss2d_qk_sizes: seven sizes, four times three strides
 
 
 # ------------------------------------------------------------------ delta rule
-def _delta_sizes(q, k, v, log_decay, beta, cu_seqlens, do=None):
-    sizes, lead, S, G, H, K, V, code = _attention_sizes(q, k, v, log_decay, cu_seqlens, do)
-    _require(v, ("beta", beta, torch.float32, lead + (H,), False))
-    sb = beta.stride()
-    return _DELTA_SIZES(*sizes, *((0,) + sb if cu_seqlens is not None else sb)), lead, S, G, H, K, V, code
+@functools.lru_cache(maxsize=1024)
+def _delta_plan(q, k, v, g, b, do, cu, code):
+    """Sizes for the C ABI, bytes of workspace and the states' shape, from the shapes and strides of the tensors; kept, as a
+    layer calls with the same ones again and again (7 us of a short prompt's 19 otherwise).  do: None for the forward."""
+    (qs, qt), (ks, kt), (vs, vt), (gs, gt), (bs, bt) = q, k, v, g, b
+    packed = cu is not None
+    n = 3 if packed else 4
+    if len(vs) != n or len(qs) != n or len(ks) != n:
+        raise ValueError("q, k, v must be (T, heads, dim) with cu_seqlens, else (S, L, heads, dim)")
+    lead, (G, K), (H, V) = tuple(vs[:-2]), qs[-2:], vs[-2:]
+    ds, dt = (vs, vt) if do is None else do
+    for name, have, want in (("q", qs, lead + (G, K)), ("k", ks, lead + (G, K)), ("log_decay", gs, lead + (H,)),
+                             ("beta", bs, lead + (H,)), ("do", ds, tuple(vs))):
+        if have != want:
+            raise ValueError(f"{name} must be {want}")
+    if G < 1 or H % G != 0:
+        raise ValueError("the heads of v must be a multiple of those of q and k")
+    if packed and (len(cu) != 1 or cu[0] < 2):
+        raise ValueError("cu_seqlens must be (sequences + 1,)")
+    if (K > 1 and (qt[-1] != 1 or kt[-1] != 1)) or (V > 1 and (vt[-1] != 1 or dt[-1] != 1)):
+        raise ValueError("the last axis of q, k, v and do must be dense")
+    S, T = (cu[0] - 1, lead[0]) if packed else (lead[0], lead[0] * lead[1])
+    three = (lambda t: (0,) + t[:2]) if packed else (lambda t: t[:3])
+    sizes = _DELTA_SIZES(S, T, G, H, K, V, *three(qt), *three(kt), *three(vt), *three(gt), *three(dt), *three(bt))
+    L = lib()
+    need = (L.ss2d_delta_rule_workspace if do is None else L.ss2d_delta_rule_backward_workspace)(sizes, int(packed), code)
+    if need < 0:
+        check(int(need))
+    return sizes, need, (S, H, K, V)
+
+
+def _delta_inputs(q, k, v, log_decay, beta, cu_seqlens, do, states):
+    """Checked plan and code; states: (name, tensor or None) of the states' shape."""
+    code, dtype = _code(v), v.dtype
+    plan = _delta_plan((q.shape, q.stride()), (k.shape, k.stride()), (v.shape, v.stride()),
+                       (log_decay.shape, log_decay.stride()), (beta.shape, beta.stride()),
+                       None if do is None else (do.shape, do.stride()),
+                       None if cu_seqlens is None else cu_seqlens.shape, code)
+    items = [("v", v, dtype, None, False), ("q", q, dtype, None, False), ("k", k, dtype, None, False),
+             ("log_decay", log_decay, torch.float32, None, False), ("beta", beta, torch.float32, None, False)]
+    if cu_seqlens is not None:
+        items.append(("cu_seqlens", cu_seqlens, torch.int32, None, True))
+    if do is not None:
+        items.append(("do", do, dtype, None, False))
+    for name, t in states:
+        if t is not None:
+            items.append((name, t, torch.float32, plan[2], True))
+    _require(v, *items)
+    return plan, code
 
 
 def delta_rule(q, k, v, log_decay, beta, state=None, cu_seqlens=None, scale: float = 1.0, final_state: bool = False,
@@ -39,18 +84,15 @@ def delta_rule(q, k, v, log_decay, beta, state=None, cu_seqlens=None, scale: flo
     if stream is not None:
         return _on_stream(stream, v.device, delta_rule, q, k, v, log_decay, beta, state, cu_seqlens, scale,
                           final_state, out)
-    sizes, lead, S, G, H, K, V, code = _delta_sizes(q, k, v, log_decay, beta, cu_seqlens)
+    (sizes, nbytes, shape), code = _delta_inputs(q, k, v, log_decay, beta, cu_seqlens, None, (("state", state),))
     device = v.device
-    if state is not None:
-        _require(v, ("state", state, torch.float32, (S, H, K, V), True))
     if out is None:
         out = _empty(v)
     else:
         _require(v, ("out", out, v.dtype, v.shape, True))
-    last = torch.empty((S, H, K, V), dtype=torch.float32, device=device) if final_state else None
-    L = lib()
-    nbytes = L.ss2d_delta_rule_workspace(sizes, 0 if cu_seqlens is None else 1, code)
+    last = torch.empty(shape, dtype=torch.float32, device=device) if final_state else None
     ws, at = _workspace(nbytes, device)
+    L = lib()
     _call(L.ss2d_delta_rule, device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
           _ptr(state), _ptr(cu_seqlens), out.data_ptr(), _ptr(last), sizes, scale, code, at, nbytes)
     return (out, last) if final_state else out
@@ -67,19 +109,14 @@ def delta_rule_backward(q, k, v, log_decay, beta, do, state=None, dfinal_state=N
     if stream is not None:
         return _on_stream(stream, v.device, delta_rule_backward, q, k, v, log_decay, beta, do, state, dfinal_state,
                           cu_seqlens, scale)
-    sizes, lead, S, G, H, K, V, code = _delta_sizes(q, k, v, log_decay, beta, cu_seqlens, do)
+    (sizes, nbytes, shape), code = _delta_inputs(q, k, v, log_decay, beta, cu_seqlens, do,
+                                                 (("state", state), ("dfinal_state", dfinal_state)))
     device = v.device
-    for name, t in (("state", state), ("dfinal_state", dfinal_state)):
-        if t is not None:
-            _require(v, (name, t, torch.float32, (S, H, K, V), True))
-    out = {"dq": _empty(q), "dk": _empty(k), "dv": _empty(v)}
-    for name in ("dlog_decay", "dbeta"):
-        out[name] = torch.empty(lead + (H,), dtype=torch.float32, device=device)
+    out = {"dq": _empty(q), "dk": _empty(k), "dv": _empty(v), "dlog_decay": _empty(log_decay), "dbeta": _empty(beta)}
     if state is not None:
-        out["dstate"] = torch.empty((S, H, K, V), dtype=torch.float32, device=device)
-    L = lib()
-    nbytes = L.ss2d_delta_rule_backward_workspace(sizes, 0 if cu_seqlens is None else 1, code)
+        out["dstate"] = torch.empty(shape, dtype=torch.float32, device=device)
     ws, at = _workspace(nbytes, device)
+    L = lib()
     _call(L.ss2d_delta_rule_backward, device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
           beta.data_ptr(), _ptr(state), _ptr(cu_seqlens), do.data_ptr(), _ptr(dfinal_state), out["dq"].data_ptr(),
           out["dk"].data_ptr(), out["dv"].data_ptr(), out["dlog_decay"].data_ptr(), out["dbeta"].data_ptr(),
@@ -135,40 +172,65 @@ def rotation_table(positions: int, rotated: int, base: float = 10000.0, device="
     return torch.cat([angle.cos(), angle.sin()], -1).float()
 
 
-def _three(x):
-    """Strides of sequence, token and head."""
-    s = x.stride()
-    return (0, s[0], s[1]) if len(s) == 3 else s[:3]
-
-
-def _qk_inputs(q, k, q_weight, k_weight, rotation, positions, others):
-    """Checked (sizes without the strides, code); others: (name, tensor, q or k) of the same shapes and dtype."""
-    n = q.dim()
-    if n not in (3, 4) or k.dim() != n:
+@functools.lru_cache(maxsize=1024)
+def _qk_sizes(q, k, to_q, to_k, table, positions):
+    """Sizes for the C ABI from the shapes and strides of queries, keys and their outputs (None: dense), the table's and
+    the positions' shapes; kept, as for the delta rule."""
+    (qs, qt), (ks, kt) = q, k
+    n = len(qs)
+    if n not in (3, 4) or len(ks) != n:
         raise ValueError("q and k must be (T, heads, dim) or (S, L, heads, dim)")
-    code, dtype = _code(q), q.dtype
-    lead, (Hq, D), Hk = q.shape[:-2], q.shape[-2:], k.shape[-2]
-    items = [("q", q, dtype, None, False), ("k", k, dtype, lead + (Hk, D), False)]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            items.append((name, w, torch.float32, (D,), True))
+    lead, (Hq, D), Hk = tuple(qs[:-2]), qs[-2:], ks[-2]
+    if tuple(ks) != lead + (Hk, D):
+        raise ValueError(f"k must be {lead + (Hk, D)}")
+    strides = [qt, kt]
+    for name, to, shape in (("queries", to_q, tuple(qs)), ("keys", to_k, tuple(ks))):
+        if to is None:
+            t = [1]
+            for m in shape[:0:-1]:
+                t.append(t[-1] * m)
+            to = shape, tuple(t[::-1])
+        if tuple(to[0]) != shape:
+            raise ValueError(f"the {name}' outputs must be {shape}")
+        strides.append(to[1])
+    if D > 1 and any(t[-1] != 1 for t in strides):
+        raise ValueError("the last axis of queries, keys and their outputs must be dense")
     rows = rot = 0
-    if rotation is not None:
-        items.append(("rotation", rotation, torch.float32, None, True))
-        if rotation.dim() != 2:
+    if table is not None:
+        if len(table) != 2:
             raise ValueError("rotation must be (positions, rotated)")
-        rows, rot = rotation.shape
+        rows, rot = table
         if rot < 2 or rot % 2 or rot > D or rows < 1:
             raise ValueError("rotation must have an even number of columns, 2 to dim, and at least one row")
-        if positions is not None:
-            items.append(("positions", positions, torch.int32, lead, True))
+        if positions is not None and tuple(positions) != lead:
+            raise ValueError(f"positions must be {lead}")
     elif positions is not None:
         raise ValueError("positions without a rotation table")
-    items += [(name, x, dtype, like.shape, False) for name, x, like in others]
+    first = (1,) + lead if n == 3 else lead
+    return _QK_SIZES(*first, Hq, Hk, D, rot, rows, *(x for t in strides for x in ((0,) + t[:2] if n == 3 else t[:3])))
+
+
+def _qk_inputs(q, k, q_weight, k_weight, rotation, positions, to_q, to_k):
+    """Checked (sizes, code); to_q, to_k: the outputs, or their gradients, or None for dense ones."""
+    code, dtype = _code(q), q.dtype
+    sizes = _qk_sizes((q.shape, q.stride()), (k.shape, k.stride()), None if to_q is None else (to_q.shape, to_q.stride()),
+                      None if to_k is None else (to_k.shape, to_k.stride()), None if rotation is None else rotation.shape,
+                      None if positions is None else positions.shape)
+    items = [("q", q, dtype, None, False), ("k", k, dtype, None, False)]
+    D = (q.shape[-1],)
+    if q_weight is not None:
+        items.append(("q_weight", q_weight, torch.float32, D, True))
+    if k_weight is not None:
+        items.append(("k_weight", k_weight, torch.float32, D, True))
+    if rotation is not None:
+        items.append(("rotation", rotation, torch.float32, None, True))
+    if positions is not None:
+        items.append(("positions", positions, torch.int32, None, True))
+    if to_q is not None:
+        items.append(("the queries' outputs", to_q, dtype, None, False))
+        items.append(("the keys' outputs", to_k, dtype, None, False))
     _require(q, *items)
-    if D > 1 and any(x.stride(-1) != 1 for x in [q, k] + [x for _, x, _ in others]):
-        raise ValueError("the last axis of queries, keys and their outputs must be dense")
-    return ((1,) if n == 3 else ()) + tuple(lead) + (Hq, Hk, D, rot, rows), code
+    return sizes, code
 
 
 def qk_norm(q, k, q_weight=None, k_weight=None, rotation=None, positions=None, interleaved: bool = False,
@@ -190,13 +252,13 @@ def qk_norm(q, k, q_weight=None, k_weight=None, rotation=None, positions=None, i
                 x.record_stream(stream)
         return _on_stream(stream, q.device, qk_norm, q, k, q_weight, k_weight, rotation, positions, interleaved, eps,
                           out)
+    to_q, to_k = (None, None) if out is None else out
+    sizes, code = _qk_inputs(q, k, q_weight, k_weight, rotation, positions, to_q, to_k)
     if out is None:
-        out = _empty(q), _empty(k)
-    sizes, code = _qk_inputs(q, k, q_weight, k_weight, rotation, positions, (("out[0]", out[0], q), ("out[1]", out[1], k)))
-    sizes = _QK_SIZES(*sizes, *_three(q), *_three(k), *_three(out[0]), *_three(out[1]))
+        to_q, to_k = _empty(q), _empty(k)
     _call(lib().ss2d_qk_norm, q.device, q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(rotation),
-          _ptr(positions), out[0].data_ptr(), out[1].data_ptr(), sizes, eps, 1 if interleaved else 0, code)
-    return out[0], out[1]
+          _ptr(positions), to_q.data_ptr(), to_k.data_ptr(), sizes, eps, 1 if interleaved else 0, code)
+    return to_q, to_k
 
 
 def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rotation=None, positions=None,
@@ -207,8 +269,7 @@ def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rotatio
     if stream is not None:
         return _on_stream(stream, q.device, qk_norm_backward, q, k, dq_out, dk_out, q_weight, k_weight, rotation,
                           positions, interleaved, eps)
-    sizes, code = _qk_inputs(q, k, q_weight, k_weight, rotation, positions, (("dq_out", dq_out, q), ("dk_out", dk_out, k)))
-    sizes = _QK_SIZES(*sizes, *_three(q), *_three(k), *_three(dq_out), *_three(dk_out))
+    sizes, code = _qk_inputs(q, k, q_weight, k_weight, rotation, positions, dq_out, dk_out)
     out = {"dq": _empty(q), "dk": _empty(k)}
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         if w is not None:
