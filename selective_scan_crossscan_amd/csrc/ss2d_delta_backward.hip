@@ -183,10 +183,12 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
       }
     }
   };
-  if (kAhead<KP>) fetch_states(0, 0);
   for (int v0 = 0; v0 < p.V; v0 += VT) {
     const int nv = min(p.V - v0, VT);
-    if (!kAhead<KP>) fetch(x, v0);
+    if (kAhead<KP>)
+      fetch_states(v0, 0);
+    else
+      fetch(x, v0);
     __syncthreads();  // the tiles before have been read, the decays are there
     f32x4 zs[PC / 4];
     {
@@ -214,6 +216,7 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
       x.v.store(vs, n, nv);
     }
     __syncthreads();
+    if (kAhead<KP>) fetch(x, v0 + VT < p.V ? v0 + VT : v0);  // always: a load under a condition would be waited for
 #pragma unroll
     for (int c = 0; c < PC / 4; ++c) {
       const f32x4 v = load4(&vs.e[ti * vs.stride + tc + 4 * c], 4);
@@ -261,11 +264,6 @@ __global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
     for (int c = 0; c < PC / 4; ++c) {
       const int left = ti < n ? nv - tc - 4 * c : 0;
       if (left > 0) store4(vto + v0 + vt + 4 * c, left, zs[c]);
-    }
-    const int ahead = v0 + VT < p.V ? v0 + VT : v0;  // always, the last one's again: a load under a condition would be waited for
-    if (kAhead<KP>) {
-      fetch(x, ahead);
-      fetch_states(ahead, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
     // (do . u) and (dz . u), transposed: rows j, columns i

@@ -124,6 +124,24 @@ def delta_rule_backward(q, k, v, log_decay, beta, do, state=None, dfinal_state=N
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _step_sizes(q, k, v, cache):
+    """Rows, slots, groups, heads, key and value sizes and the rows' strides for the C ABI."""
+    (qs, qt), (ks, kt), (vs, vt) = q, k, v
+    if len(vs) != 3 or len(qs) != 3 or len(cache) != 4:
+        raise ValueError("q, k must be (B,G,K), v (B,H,V), state (slots,H,K,V)")
+    (B, H, V), (G, K) = vs, qs[1:]
+    for name, have, want in (("q", qs, (B, G, K)), ("k", ks, (B, G, K)), ("state", cache, (cache[0], H, K, V))):
+        if have != want:
+            raise ValueError(f"{name} must be {want}")
+    if G < 1 or H % G != 0:
+        raise ValueError("the heads of v must be a multiple of those of q and k")
+    for name, st, n, d in (("q", qt, G, K), ("k", kt, G, K), ("v", vt, H, V)):
+        if (n > 1 and st[1] != d) or (d > 1 and st[2] != 1):
+            raise ValueError(f"{name} must be dense inside a row")
+    return B, cache[0], G, H, K, V, qt[0], kt[0], vt[0]
+
+
 def delta_rule_step(q, k, v, log_decay, beta, state, state_index=None, scale: float = 1.0, out=None, stream=None):
     """One token per row over a cache of states, updated in place (ss2d_delta_rule_step).
 
@@ -134,30 +152,21 @@ def delta_rule_step(q, k, v, log_decay, beta, state, state_index=None, scale: fl
     """
     if stream is not None:
         return _on_stream(stream, v.device, delta_rule_step, q, k, v, log_decay, beta, state, state_index, scale, out)
-    if v.dim() != 3 or q.dim() != 3 or state.dim() != 4:
-        raise ValueError("q, k must be (B,G,K), v (B,H,V), state (slots,H,K,V)")
     code, dtype = _code(v), v.dtype
-    B, H, V = v.shape
-    qshape, cache = q.shape, state.shape
-    G, K = qshape[1:]
-    _require(v, ("v", v, dtype, None, False), ("q", q, dtype, (B, G, K), False), ("k", k, dtype, qshape, False),
-             ("log_decay", log_decay, torch.float32, (B, H), True), ("beta", beta, torch.float32, (B, H), True),
-             ("state", state, torch.float32, (cache[0], H, K, V), True))
-    if G < 1 or H % G != 0:
-        raise ValueError("the heads of v must be a multiple of those of q and k")
+    sizes = _step_sizes((q.shape, q.stride()), (k.shape, k.stride()), (v.shape, v.stride()), state.shape)
+    rates = v.shape[:2]
+    items = [("v", v, dtype, None, False), ("q", q, dtype, None, False), ("k", k, dtype, None, False),
+             ("log_decay", log_decay, torch.float32, rates, True), ("beta", beta, torch.float32, rates, True),
+             ("state", state, torch.float32, None, True)]
     if state_index is not None:
-        _require(v, ("state_index", state_index, torch.int32, (B,), True))
-    rows = [x.stride() for x in (q, k, v)]
-    for name, st, n, d in (("q", rows[0], G, K), ("k", rows[1], G, K), ("v", rows[2], H, V)):
-        if (n > 1 and st[1] != d) or (d > 1 and st[2] != 1):
-            raise ValueError(f"{name} must be dense inside a row")
+        items.append(("state_index", state_index, torch.int32, rates[:1], True))
+    if out is not None:
+        items.append(("out", out, dtype, v.shape, True))
+    _require(v, *items)
     if out is None:
         out = _empty(v)
-    else:
-        _require(v, ("out", out, dtype, (B, H, V), True))
     _call(lib().ss2d_delta_rule_step, v.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-          beta.data_ptr(), state.data_ptr(), _ptr(state_index), out.data_ptr(), B, cache[0], G, H, K, V, rows[0][0],
-          rows[1][0], rows[2][0], scale, code)
+          beta.data_ptr(), state.data_ptr(), _ptr(state_index), out.data_ptr(), *sizes, scale, code)
     return out
 
 
