@@ -27,13 +27,13 @@ template <typename E, int C>
 struct Systems {
   static constexpr int NI = C / 16;
   static constexpr int kFrags = NI / 2 * (NI / 2 + 1);
-  static constexpr int kParts = sizeof(E) == 2 ? 2 : 1;       // of an inverse without its diagonal of ones
-  static constexpr int kScoreParts = sizeof(E) == 2 ? 3 : 1;  // of the gradients' P'
+  static constexpr int kParts = sizeof(E) == 2 ? 3 : 1;       // of an inverse without its diagonal of ones, and of P'
+  static constexpr int kScoreParts = sizeof(E) == 2 ? 2 : 1;  // of the forward's P
   static constexpr int kFragBytes = 64 * 8 * (int)sizeof(E);
   static constexpr int kInverse = kFrags * kParts * kFragBytes;
-  static constexpr int kScores = kFrags * kFragBytes;  // one part: the forward's P
+  static constexpr int kScores = kFrags * kScoreParts * kFragBytes;
   static constexpr int kForward = kInverse + kScores;
-  static constexpr int kBackward = 2 * kInverse + kScoreParts * kScores;
+  static constexpr int kBackward = 3 * kInverse;
   // Rows i, columns j <= i: tile row x has the pairs 0 .. x / 2.
   static __host__ __device__ constexpr int lower(int x, int pair) { return (x / 2) * (x / 2 + 1) + (x & 1) * (x / 2 + 1) + pair; }
   // Rows j, columns i >= j: tile row x has the pairs x / 2 .. NI / 2 - 1; the mirror image.

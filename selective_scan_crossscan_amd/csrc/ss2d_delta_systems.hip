@@ -4,10 +4,10 @@
 // chunk of C tokens and head
 //   forward    N = (1 + L diag(b))^-1 - 1 in parts and P in one;
 //   gradients  the same N, and ((1 + diag(b) L)^-1)' - 1 and P' in parts,
-// as fragments in the order in which the walks read them.  Parts: P' becomes an fp32 result and keeps 24 bits in three.
-// Of an inverse the ones on the diagonal are left to the walks, which add their operand as it is, and the rest, entries of
-// about beta k_i . k_j, takes two parts: 17 bits of what is added to the operand, a quarter of it for keys that are
-// nothing to each other (error of a state of 2048 tokens 1.8e-7 with three parts, 2.6e-7 with two).
+// as fragments in the order in which the walks read them.  Parts: what becomes an fp32 result, errors and states, keeps 24
+// bits in three, the ones on the diagonal left to the walks; P, which ends in an output of the storage type, 16 in two.
+// (With the inverses in two as well, 17 bits of what they add to an error, states were up to 1.6e-6 off where elementary
+// fp32 operations are 1.8e-7, for 5% of the time.)
 //
 // A triangle is inverted in blocks of 16.  A diagonal block by substitution: a lane holds one row of the inverse and
 // the block's entries are read by all lanes at once; as stable as the system is, where a series of powers would cancel
@@ -190,9 +190,9 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
     for (int pair = 0; pair < NI / 2; ++pair)
       if (BACK ? pair >= w / 2 : pair <= w / 2) {
         if (BACK)
-          put_frag<S::kScoreParts, E>(out + 2 * S::kInverse + S::upper(w, pair) * S::kScoreParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
+          put_frag<S::kParts, E>(out + 2 * S::kInverse + S::upper(w, pair) * S::kParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
         else
-          put_frag<1, E>(out + S::kInverse + S::lower(w, pair) * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
+          put_frag<S::kScoreParts, E>(out + S::kInverse + S::lower(w, pair) * S::kScoreParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
       }
   }
   __syncthreads();  // the queries have been read

@@ -38,6 +38,9 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   constexpr int NW = VT / 16 / NV, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   using S = Systems<E, C>;
   constexpr int PN = S::kParts;
+  // Parts of what ends in an output of the storage type: two of all operands leave an output its own rounding alone (one
+  // of each: 1.5 to 1.8 times its error).
+  constexpr int PO = S::kScoreParts;
   constexpr int kSystem = PASS == kOutputs ? S::kForward : S::kInverse;  // bytes read per chunk
   constexpr int kPieces = (kSystem / 16 + THREADS - 1) / THREADS;
   auto& qs = lds.qs;
@@ -99,7 +102,6 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     if (PASS == kOutputs) x.q.load(qb + at * p.q_stride[1], p.q_stride[1], n, K);
     x.k.load(kb + at * p.k_stride[1], p.k_stride[1], n, K);
     if (!map) x.v.load(vb + at * p.v_stride[1], p.v_stride[1], n, nv);
-    fetch_rest(x, at);
   };
   auto land = [&](const Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
@@ -128,7 +130,10 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     land_rest(x, at);
   };
   Chunk first;  // on its way while the state is read
-  if (kAhead<KP> && seg.begin < seg.end) fetch(first, seg.begin);
+  if (kAhead<KP> && seg.begin < seg.end) {
+    fetch(first, seg.begin);
+    fetch_rest(first, seg.begin);
+  }
 
   // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
   f32x4 h[NK][NV];
@@ -168,8 +173,8 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     Chunk next;
     const int64_t ahead = at + C < seg.end ? at + C : at;
     if (kAhead<KP>) fetch(next, ahead);
+    if (kAhead<KP> && PASS != kOutputs) fetch_rest(next, ahead);
 
-    f32x4 o[NV][NI];
     if (active) {
       if (PASS == kStates) {
         float* to = by_bytes(p.chunk_state + ((chunk_number<C>(p.map, seg, at) * p.heads + head) * p.tiles + tile) * (KP * kArrayTile), lane_at);
@@ -180,7 +185,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 #pragma unroll
             for (int t = 0; t < NV; ++t) to[(kt * 16 + r) * kArrayTile + t * 16] = h[kt][t][r];
       }
-      f32x4 z[NI][NV];
+      f32x4 z[NI][NV], o[NV][NI];
 #pragma unroll
       for (int t = 0; t < NV; ++t)
 #pragma unroll
@@ -209,7 +214,9 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
           for (int x = 0; x < NI; ++x) {
             const Frag<E> f = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-            for (int t = 0; t < NV; ++t) o[t][x] = mma(b[t][0], f, o[t][x]);
+            for (int q = PO - 1; q >= 0; --q)
+#pragma unroll
+              for (int t = 0; t < NV; ++t) o[t][x] = mma(b[t][q], f, o[t][x]);
           }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -274,9 +281,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
       if (PASS == kOutputs) {
 #pragma unroll
         for (int j = 0; j < NI; j += 2) {
-          // two parts: the scores and the state are rounded once, and so is all that an output is made of
-          constexpr int PU = PF > 1 ? 2 : 1;
-          Frag<E> a[NV][PU];
+          Frag<E> a[NV][PO];
 #pragma unroll
           for (int t = 0; t < NV; ++t) {
             float u[8];
@@ -285,15 +290,23 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
           }
 #pragma unroll
           for (int x = j; x < NI; ++x) {
-            const Frag<E> s = system_frag<E>(sys + S::kInverse + S::lower(x, j / 2) * S::kFragBytes);
+            Frag<E> s[PO];
 #pragma unroll
-            for (int q = PU - 1; q >= 0; --q)
+            for (int q = 0; q < PO; ++q) s[q] = system_frag<E>(sys + S::kInverse + (S::lower(x, j / 2) * PO + q) * S::kFragBytes);
 #pragma unroll
-              for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], s, o[t][x]);
+            for (int n = PO - 1; n >= 0; --n)
+#pragma unroll
+              for (int q = 0; q <= n; ++q)
+#pragma unroll
+                for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], s[n - q], o[t][x]);
           }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
+        put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
+        __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
       }
+      // The next systems, late, in registers that the outputs had; loads under the condition, alike for a wave's threads.
+      if (kAhead<KP> && PASS == kOutputs) fetch_rest(next, ahead);
       const float all = rates.since[C - 1];
 #pragma unroll
       for (int kt = 0; kt < NK; ++kt)
@@ -323,17 +336,12 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if (kAhead<KP> && PASS == kOutputs && !active) fetch_rest(next, ahead);
     __syncthreads();  // the chunk has been read
     if (kAhead<KP>)
       land(next, ahead);
     else
       bring(ahead);
-    // Outputs leave last: they are stored under conditions, and the loads before a store of which it is not known whether
-    // it is made are only known to have arrived when the store has.
-    if (PASS == kOutputs && active) {
-      E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-      put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
-    }
   }
 
   float* to = PASS == kSegments ? (map ? p.seg_map + ((int64_t)slot * p.heads + head) * (KP * KP) : p.seg_state + sh)
@@ -372,9 +380,8 @@ struct BackParams {
 template <typename E, int C, int KP, int VT>
 struct BackTiles {
   using S = Systems<E, C>;
-  Tile<E, C, KP, 32> qs;
-  Tile<E, C, KP, 16> ks;
-  Tile<E, C, VT, 32> ds;
+  Tile<E, C, KP, 16> qs, ks;  // 16 all: two workgroups' fit a CU at 128 keys and 64 values
+  Tile<E, C, VT, 16> ds;
   __attribute__((aligned(16))) char sys[whole_pieces(S::kBackward - S::kInverse, VT * 4)];  // the transposed inverse and P'
   Rates<C> rates;
 };
@@ -417,9 +424,8 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
   const int64_t sstep = p.heads * p.system_stride;
 
   struct Chunk {
-    TileLoad<E, C, KP, 32, THREADS, TINY && KP == 32> q;
-    TileLoad<E, C, KP, 16, THREADS, TINY && KP == 32> k;
-    TileLoad<E, C, VT, 32, THREADS, TINY> d;
+    TileLoad<E, C, KP, 16, THREADS, TINY && KP == 32> q, k;
+    TileLoad<E, C, VT, 16, THREADS, TINY> d;
     uint4 s[kPieces];
     float g, b;
   };
