@@ -65,12 +65,15 @@ __device__ __forceinline__ void put4_parts(Tile<float, R, CC, PAD> (&m)[1], int 
   put4(&m[0].e[at], x);
 }
 
+// Eight waves also for few keys (2 x 2048 tokens of 16 heads, all gradients: 64 keys 248 us, with four waves 256; 32 keys
+// 215 and 219; 128 keys 343 and 358).
+constexpr int kGradientWaves = 8;
 // One workgroup per chunk and head; a wave owns key columns wave, wave + NW, ... by 16 and their dq and dk, transposed
 // (rows k, columns token); the values are gone through in tiles of 64 columns.
-template <typename E, int C, int KP, int NW, bool TINY>
-__global__ __launch_bounds__(NW * 64) void delta_gradients(BackParams b) {
+template <typename E, int C, int KP, bool TINY>
+__global__ __launch_bounds__(kGradientWaves * 64) void delta_gradients(BackParams b) {
   const DeltaParams& p = b.d;
-  constexpr int THREADS = NW * 64, NI = C / 16, NK = KP / 16, VT = kArrayTile, NV = VT / 16, PF = kFullParts<E>;
+  constexpr int NW = kGradientWaves, THREADS = NW * 64, NI = C / 16, NK = KP / 16, VT = kArrayTile, NV = VT / 16, PF = kFullParts<E>;
   constexpr int OK = (NK + NW - 1) / NW;
   constexpr int PB = PF > 1 ? 2 : 1;  // parts of U and dZ towards dk, whose products round one operand only
   constexpr int JS = NW / NI < NI ? NW / NI : NI;  // waves that share 16 tokens' scores
@@ -402,7 +405,9 @@ __global__ __launch_bounds__(256) void sum_parts(const float* __restrict__ parts
 }
 
 // ------------------------------------------------------------------ launches
-// Value columns of a workgroup that walks back, and the parts of `inner` they leave.
+// Value columns of a workgroup that walks back, and the parts of `inner` they leave.  Of 128 values half the workgroups
+// read the keys and systems once (2 x 2048 tokens, 16 heads of 128, all gradients 342 us, 364 in tiles of 64; 64 and 32
+// keys alike).
 int back_tile(int64_t V, const DeltaPlan& pl) { return V <= 64 || pl.a.tiny ? 64 : 128; }
 int columns_of(int64_t V, const DeltaPlan& pl) {
   const int vt = back_tile(V, pl);
@@ -484,8 +489,8 @@ hipError_t launch_gradients(BackParams b, const DeltaPlan& pl, hipStream_t st) {
   b.blocks = (uint32_t)(pl.a.chunks * b.d.heads);
   b.columns = columns_of(b.d.V, pl);
   with_keys(pl, [&](auto kp, auto tiny) {
-    constexpr int NW = kp() >= 128 ? 8 : 4;
-    delta_gradients<E, C, kp(), NW, tiny()><<<grid_of(b.blocks, NW * 64), dim3(NW * 64), 0, st>>>(b);
+    constexpr int threads = kGradientWaves * 64;
+    delta_gradients<E, C, kp(), tiny()><<<grid_of(b.blocks, threads), dim3(threads), 0, st>>>(b);
   });
   return hipGetLastError();
 }

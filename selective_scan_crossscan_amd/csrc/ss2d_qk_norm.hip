@@ -289,7 +289,8 @@ int threads_of(int64_t dim, int64_t rotated) {
 }
 // Heads in a run, and the gradients' workgroups of both sides at most: 16384 tokens of 16 + 16 heads of 128 in bf16, us of
 // runs of 1, 2 and 4 heads 65, 52, 48; gradients of runs of 1, 2 and 4 by 1024 to 4096 workgroups 89 to 103, 88 to 98 and
-// 89 (the fewer the better).
+// 89 (the fewer the better).  A run shares its token's angles and has more loads in flight; where rows are few, runs of 1
+// are no faster (64 and 512 tokens: 6.4 and 5.2 us, in runs of 4 7.6 and 4.7).
 constexpr int kRun = 4, kBackRun = 2;
 constexpr int64_t kMost = 1024;
 void share(int64_t tokens, const int64_t (&heads)[2], int threads, int run, int (&blocks)[2]) {
@@ -322,13 +323,13 @@ void with_threads(const QkParams& p, F f) {
   }
 }
 
-template <typename S, int RUN>
+template <typename S>
 void launch_forward(const QkArgs& a, hipStream_t st) {
-  const QkParams p = params_of(a, RUN);
+  const QkParams p = params_of(a, kRun);
   const int t = threads_of(p.dim, p.rotated);
   const int64_t items = (int64_t)p.tokens * (p.runs[0] + p.runs[1]);
   const dim3 grid = grid_of((items + 256 / t - 1) / (256 / t), 256), block(256);
-  with_threads(p, [&](auto threads, auto whole) { qk_norm_kernel<S, threads(), RUN, whole()><<<grid, block, 0, st>>>(p); });
+  with_threads(p, [&](auto threads, auto whole) { qk_norm_kernel<S, threads(), kRun, whole()><<<grid, block, 0, st>>>(p); });
 }
 template <typename S>
 void launch_backward(const QkArgs& a, hipStream_t st) {
@@ -352,12 +353,7 @@ size_t qk_norm_backward_workspace_bytes(int64_t tokens, const int64_t (&heads)[2
 }
 
 hipError_t launch_qk_norm(const QkArgs& a) {
-  // Runs of heads share a token's angles and have more loads in flight; few rows are spread over the CUs instead.
-  const bool few = a.sequences * a.length * (a.heads[0] + a.heads[1]) < 16384;
-  if (a.dtype == 1)
-    few ? launch_forward<uint16_t, 1>(a, a.stream) : launch_forward<uint16_t, kRun>(a, a.stream);
-  else
-    few ? launch_forward<float, 1>(a, a.stream) : launch_forward<float, kRun>(a, a.stream);
+  a.dtype == 1 ? launch_forward<uint16_t>(a, a.stream) : launch_forward<float>(a, a.stream);
   return hipGetLastError();
 }
 
