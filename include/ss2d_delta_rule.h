@@ -41,11 +41,11 @@ typedef struct {
  *              precision with it.
  * Outputs must not overlap inputs, but state_out may be state_in itself
  * (SS2D_ERR_ALIAS).  States, decays, sums and the triangular systems of 64 tokens
- * (32 in fp32) are fp32, decays summed in fp64.  For bf16 an output takes the masked
- * scores and the state rounded to bf16 once, its own rounding being as large; what the
- * state itself is made of keeps all its bits.  NaN and Inf
- * propagate: from a token to its sequence's outputs from up to 63 tokens before it on,
- * so padding behind a sequence's end has to be finite, or left out by cu_seqlens.
+ * (32 in fp32) are fp32, decays summed in fp64.  For bf16 an output takes 16 bits of the
+ * masked scores, the replaced values and the state, so its own rounding alone is seen;
+ * what the state itself is made of keeps 24.  NaN and Inf propagate: from a token to its
+ * sequence's outputs from up to 63 tokens before it on, so padding behind a sequence's
+ * end has to be finite, or left out by cu_seqlens.
  * Results do not depend on the workspace, other sequences or streams.
  * SS2D_ERR_SHAPE for sizes out of ss2d_linear_attention's ranges, and over 2^30
  * workgroups: chunks of 64 (32) tokens times heads, or segments times heads times tiles
@@ -57,8 +57,8 @@ int ss2d_delta_rule(const void* q, const void* k, const void* v, const float* lo
                     void* stream);
 
 /* Bytes of workspace ss2d_delta_rule needs, or a negative status.  packed: 1 if it will
- * be given cu_seqlens, else 0.  About 400 bytes per token and head (270 in fp32), and
- * the states of segments where few sequences and heads have to be cut. */
+ * be given cu_seqlens, else 0.  30 KiB per 64 tokens and head (8 KiB per 32 in fp32),
+ * and the states of segments where few sequences and heads have to be cut. */
 int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int dtype);
 
 /*
@@ -73,9 +73,9 @@ int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int
  *                       value, the gradient of each of its uses)
  *           dstate_in   [sequences, heads, key_dim, value_dim] fp32 or NULL
  * Outputs are overwritten, not added to; tokens outside the sequences keep what they
- * were.  Outputs must not overlap inputs or each other.  For bf16 dk takes the states,
- * their gradients and the masked products rounded to bf16 once each; the other outputs
- * keep all bits up to their own rounding.
+ * were.  Outputs must not overlap inputs or each other.  For bf16 each product of dk
+ * has one operand (a state, its gradient, masked products) rounded to bf16 once; the
+ * other outputs keep 16 bits or more up to their own rounding.
  */
 int ss2d_delta_rule_backward(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
                              const float* state_in, const int32_t* cu_seqlens, const void* d_o,
@@ -133,7 +133,7 @@ typedef struct {
  *   q_out, k_out  as q and k, strided; each may be q or k itself (the same strides), and
  *              the two sides may lie in the same rows, as slices of one projection do
  * All arithmetic is fp32, each output rounded once.  A head with squares that overflow
- * fp32 (values over 2^63) gives 0.  At most 2^31-1 tokens times heads, dim 1..256,
+ * fp32 (values over 2^63) gives 0, a head of zeros 0 too, but NaN if eps is 0.  At most 2^31-1 tokens times heads, dim 1..256,
  * eps >= 0 and finite (SS2D_ERR_SHAPE otherwise).  One kernel, no workspace.
  */
 int ss2d_qk_norm(const void* q, const void* k, const float* q_weight, const float* k_weight, const float* rotation,

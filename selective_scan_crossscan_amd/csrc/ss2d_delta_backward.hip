@@ -18,6 +18,9 @@
 // walk backwards, which is the same kind of recurrence (a wave owns value columns and needs nothing from other waves);
 // all else chunk by chunk, in any order, with no walk to wait for.  A segment's map of D is the transpose of its map of
 // the state, so cut sequences' maps are formed once.
+//
+// us of 2 x 4096 tokens, 16 heads of 128, bf16: systems 47, both ways' segments 171 and carries 37, states 86, the walk
+// back 128, all else 202 (192 KiB of H, D, E and dF in fp32 per chunk and head, at 2 TB/s).
 #include "ss2d_delta_walk.h"
 
 namespace ss2d {

@@ -2,7 +2,7 @@
 //
 // With L_ij = exp(G_i - G_j) k_i . k_j for j < i, b = beta and P_ij = scale exp(G_i - G_j) q_i . k_j for j <= i, per
 // chunk of C tokens and head
-//   forward    N = (1 + L diag(b))^-1 - 1 in parts and P in one;
+//   forward    N = (1 + L diag(b))^-1 - 1 and P in parts;
 //   gradients  the same N, and ((1 + diag(b) L)^-1)' - 1 and P' in parts,
 // as fragments in the order in which the walks read them.  Parts: what becomes an fp32 result, errors and states, keeps 24
 // bits in three, the ones on the diagonal left to the walks; P, which ends in an output of the storage type, 16 in two.
@@ -14,6 +14,9 @@
 // (keys that repeat: powers up to 6435 of entries up to 1).  The other blocks X_tw = -X_tt sum_c Z_tc X_cw on the
 // matrix cores in fp32 (16x16x4), one block column per wave: a result tile is the next product's second operand as it
 // lies.
+//
+// Bound by memory: 16 x 2048 tokens, 16 heads of 128 in bf16, take 99 us: 32 KiB read and 30 KiB written per chunk and
+// head at 5.2 TB/s.
 #include <type_traits>
 
 #include "ss2d_delta.h"

@@ -1,5 +1,14 @@
 // The gated delta rule: the walks over the chunks, forwards and backwards, as what kernels of either kind, or of both,
 // are made of (ss2d_delta.hip, ss2d_delta_backward.hip).
+//
+// One workgroup walks a segment of one sequence and head for VT value columns; a wave owns 16 NV of them, and the state,
+// errors and outputs of its columns never leave its registers.  Keys, queries, values and the chunk's systems come
+// through LDS, read by all waves.  Three passes share the forward walk: outputs; a segment's own part of the state and
+// its map of the state before it; the states before all chunks and the errors, for the gradients.
+//
+// Bound by latency and issue, not by memory: of 16 x 2048 tokens, 16 heads of 128 in bf16, the outputs' walk takes
+// 335 us, vector instructions 36% and matrix instructions 32% of the SIMDs' cycles, the waves waiting 38% of their time
+// (chunk after chunk barriers, reads from LDS, and products that need the ones before); without its loads 70 us less.
 #pragma once
 
 #include <type_traits>
@@ -13,7 +22,8 @@ using namespace tok;
 
 constexpr int kArrayTile = 64;  // columns of a tile of the chunks' arrays
 // Whether the next chunk's loads wait in registers while one is worked on.  256 keys leave no registers for that, and
-// are loaded when the chunk before has been read.
+// are loaded when the chunk before has been read.  (128 keys, forward of 2 x 16384 tokens of 16 heads 687 us, loaded late
+// 705; 2 x 2048 tokens 140 and 136.)
 template <int KP>
 constexpr bool kAhead = KP <= 128;
 
