@@ -73,9 +73,8 @@ int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int
  *                       value, the gradient of each of its uses)
  *           dstate_in   [sequences, heads, key_dim, value_dim] fp32 or NULL
  * Outputs are overwritten, not added to; tokens outside the sequences keep what they
- * were.  Outputs must not overlap inputs or each other.  For bf16 each product of dk
- * has one operand (a state, its gradient, masked products) rounded to bf16 once; the
- * other outputs keep 16 bits or more up to their own rounding.
+ * were.  Outputs must not overlap inputs or each other.  What enters a product keeps 24
+ * bits in either type, so dq, dk and dv in bf16 show their own rounding alone.
  */
 int ss2d_delta_rule_backward(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
                              const float* state_in, const int32_t* cu_seqlens, const void* d_o,

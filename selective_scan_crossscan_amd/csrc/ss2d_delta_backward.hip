@@ -78,16 +78,15 @@ __global__ __launch_bounds__(kGradientWaves * 64) void delta_gradients(BackParam
   const DeltaParams& p = b.d;
   constexpr int NW = kGradientWaves, THREADS = NW * 64, NI = C / 16, NK = KP / 16, VT = kArrayTile, NV = VT / 16, PF = kFullParts<E>;
   constexpr int OK = (NK + NW - 1) / NW;
-  constexpr int PB = PF > 1 ? 2 : 1;  // parts of U and dZ towards dk, whose products round one operand only
   constexpr int JS = NW / NI < NI ? NW / NI : NI;  // waves that share 16 tokens' scores
   constexpr int NS = NI / JS;                      // score tiles of a wave
   constexpr int TT = THREADS / C, PC = VT / TT;    // threads per token, each with PC columns of values
   static_assert(NW >= NI && PC % 4 == 0, "score tiles and columns are dealt evenly");
   struct Values {
-    Tile<E, C, VT> d, z[PB], u[PF];
+    Tile<E, C, VT> d, z[PF], u[PF];
   };
   struct Scores {
-    Tile<E, C, C> x[PF], y;
+    Tile<E, C, C> x[PF], y[PF];
   };
   __shared__ Tile<E, C, KP, 32> qs, ks;
   __shared__ union {
@@ -240,27 +239,38 @@ __global__ __launch_bounds__(kGradientWaves * 64) void delta_gradients(BackParam
 #pragma unroll
         for (int c = 0; c < NV; c += 2) {
           float u[8];
-          Frag<E> fh[PF], fd[1];
+          Frag<E> f[PF];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             xsum = fmaf(h[at][c][r], d[at][c][r], xsum);
             xsum = fmaf(h[at][c + 1][r], d[at][c + 1][r], xsum);
           }
-          stack(h[at][c], h[at][c + 1], u);
-          split_parts(u, fh);
+          // parts in the order in which each tile's are read once: the largest of one with all of the other's first
           stack(d[at][c], d[at][c + 1], u);
-          split_parts(u, fd);
+          split_parts(u, f);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+#pragma unroll
+            for (int q = 0; q < PF; ++q) {
+              const Frag<E> x = frag_row_split(m.v.u[q], i * 16 + l, c * 16);
+#pragma unroll
+              for (int n = PF - 1 - q; n >= 0; --n) dk[a][0][i] = mma(f[n], x, dk[a][0][i]);
+            }
+            if (!kAhead<KP>) __builtin_amdgcn_sched_barrier(0);  // or their registers add up and spill
+          }
+          stack(h[at][c], h[at][c + 1], u);
+          split_parts(u, f);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             const Frag<E> o = frag_row_split(m.v.d, i * 16 + l, c * 16);
 #pragma unroll
-            for (int q = 0; q < PB; ++q) {
-              dk[a][0][i] = mma(fd[0], frag_row_split(m.v.u[PB - 1 - q], i * 16 + l, c * 16), dk[a][0][i]);
-              dz[a][i] = mma(fh[0], frag_row_split(m.v.z[PB - 1 - q], i * 16 + l, c * 16), dz[a][i]);
-              dq[a][0][i] = mma(fh[PF - 1 - q], o, dq[a][0][i]);
+            for (int q = 0; q < PF; ++q) {
+              const Frag<E> x = frag_row_split(m.v.z[q], i * 16 + l, c * 16);
+#pragma unroll
+              for (int n = PF - 1 - q; n >= 0; --n) dz[a][i] = mma(f[n], x, dz[a][i]);
+              dq[a][0][i] = mma(f[PF - 1 - q], o, dq[a][0][i]);
             }
-            if (PF > PB) dq[a][0][i] = mma(fh[0], o, dq[a][0][i]);
-            if (!kAhead<KP>) __builtin_amdgcn_sched_barrier(0);  // or their registers add up and spill
+            if (!kAhead<KP>) __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
@@ -280,15 +290,16 @@ __global__ __launch_bounds__(kGradientWaves * 64) void delta_gradients(BackParam
 #pragma unroll
         for (int c = 0; c < VT; c += 32) {
           const Frag<E> fd = frag_row(m.v.d, i0, c);
-          Frag<E> fu[PF], fz[PB];
+          Frag<E> fu[PF], fz[PF];
 #pragma unroll
-          for (int q = 0; q < PF; ++q) fu[q] = frag_row(m.v.u[q], jt * 16 + l, c);
-#pragma unroll
-          for (int q = 0; q < PB; ++q) fz[q] = frag_row(m.v.z[q], i0, c);
+          for (int q = 0; q < PF; ++q) {
+            fu[q] = frag_row(m.v.u[q], jt * 16 + l, c);
+            fz[q] = frag_row(m.v.z[q], i0, c);
+          }
 #pragma unroll
           for (int q = PF - 1; q >= 0; --q) sx[i] = mma(fu[q], fd, sx[i]);
 #pragma unroll
-          for (int s = PB - 1; s >= 0; --s)
+          for (int s = PF - 1; s >= 0; --s)
 #pragma unroll
             for (int q = 0; q <= s; ++q) sy[i] = mma(fu[q], fz[s - q], sy[i]);
         }
@@ -321,7 +332,7 @@ __global__ __launch_bounds__(kGradientWaves * 64) void delta_gradients(BackParam
         sy[i][r] = j < ei ? y : 0.f;
       }
       put4_parts(m.s.x, ei * m.s.x[0].stride + jt * 16 + 4 * eg, sx[i]);
-      put4(&m.s.y.e[ei * m.s.y.stride + jt * 16 + 4 * eg], sy[i]);
+      put4_parts(m.s.y, ei * m.s.y[0].stride + jt * 16 + 4 * eg, sy[i]);
     }
   }
   __syncthreads();
@@ -346,13 +357,17 @@ __global__ __launch_bounds__(kGradientWaves * 64) void delta_gradients(BackParam
         for (int x = 0; x < NI; ++x) {
           if (x >= j) {  // tokens j .. j + 31 before x
 #pragma unroll
-            for (int q = PF - 1; q >= 0; --q) dq[a][0][x] = mma(fk, frag_row_split(m.s.x[q], x * 16 + el, j * 16), dq[a][0][x]);
-            dk[a][0][x] = mma(fk, frag_row_split(m.s.y, x * 16 + el, j * 16), dk[a][0][x]);
+            for (int q = PF - 1; q >= 0; --q) {
+              dq[a][0][x] = mma(fk, frag_row_split(m.s.x[q], x * 16 + el, j * 16), dq[a][0][x]);
+              dk[a][0][x] = mma(fk, frag_row_split(m.s.y[q], x * 16 + el, j * 16), dk[a][0][x]);
+            }
           }
-          if (x < j + 2) {  // tokens j .. j + 31 behind x
-            dk[a][0][x] = mma(fq, frag_col_split(m.s.x[0], j * 16, x * 16), dk[a][0][x]);
-            dk[a][0][x] = mma(fk, frag_col_split(m.s.y, j * 16, x * 16), dk[a][0][x]);
-          }
+          if (x < j + 2)  // tokens j .. j + 31 behind x
+#pragma unroll
+            for (int q = PF - 1; q >= 0; --q) {
+              dk[a][0][x] = mma(fq, frag_col_split(m.s.x[q], j * 16, x * 16), dk[a][0][x]);
+              dk[a][0][x] = mma(fk, frag_col_split(m.s.y[q], j * 16, x * 16), dk[a][0][x]);
+            }
         }
       }
 #pragma unroll
