@@ -41,9 +41,8 @@ typedef struct {
  *              precision with it.
  * Outputs must not overlap inputs, but state_out may be state_in itself
  * (SS2D_ERR_ALIAS).  States, decays, sums and the triangular systems of 64 tokens
- * (32 in fp32) are fp32, decays summed in fp64.  For bf16 an output takes 16 bits of the
- * masked scores, the replaced values and the state, so its own rounding alone is seen;
- * what the state itself is made of keeps 24.  NaN and Inf propagate: from a token to its
+ * (32 in fp32) are fp32, decays summed in fp64, and what enters a product keeps 24 bits
+ * in either type: an output in bf16 shows its own rounding alone.  NaN and Inf propagate: from a token to its
  * sequence's outputs from up to 63 tokens before it on, so padding behind a sequence's
  * end has to be finite, or left out by cu_seqlens.
  * Results do not depend on the workspace, other sequences or streams.
@@ -57,7 +56,7 @@ int ss2d_delta_rule(const void* q, const void* k, const void* v, const float* lo
                     void* stream);
 
 /* Bytes of workspace ss2d_delta_rule needs, or a negative status.  packed: 1 if it will
- * be given cu_seqlens, else 0.  30 KiB per 64 tokens and head (8 KiB per 32 in fp32),
+ * be given cu_seqlens, else 0.  24 KiB per 64 tokens and head (8 KiB per 32 in fp32),
  * and the states of segments where few sequences and heads have to be cut. */
 int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int dtype);
 

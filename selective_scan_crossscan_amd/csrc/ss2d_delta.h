@@ -21,19 +21,17 @@
 
 namespace ss2d {
 
-// Sizes of a chunk's systems in memory: fragments in the order of their tiles, those
-// of a triangle's 16-row tiles x by pairs of 16-column tiles.
+// Sizes of a chunk's systems: fragments in the order of their tiles, those of a triangle's
+// 16-row tiles x by pairs of 16-column tiles; in memory in fp32, in the walks' LDS in parts.
 template <typename E, int C>
 struct Systems {
   static constexpr int NI = C / 16;
   static constexpr int kFrags = NI / 2 * (NI / 2 + 1);
-  static constexpr int kParts = sizeof(E) == 2 ? 3 : 1;       // of an inverse without its diagonal of ones, and of P'
-  static constexpr int kScoreParts = sizeof(E) == 2 ? 2 : 1;  // of the forward's P
-  static constexpr int kFragBytes = 64 * 8 * (int)sizeof(E);
-  static constexpr int kInverse = kFrags * kParts * kFragBytes;
-  static constexpr int kScores = kFrags * kScoreParts * kFragBytes;
-  static constexpr int kForward = kInverse + kScores;
-  static constexpr int kBackward = 3 * kInverse;
+  static constexpr int kParts = sizeof(E) == 2 ? 3 : 1;  // into which the walks split them
+  static constexpr int kFragBytes = 64 * 8 * (int)sizeof(E);  // of one part
+  static constexpr int kOne = kFrags * 64 * 8 * 4;  // an inverse without its diagonal of ones, or scores
+  static constexpr int kForward = 2 * kOne;
+  static constexpr int kBackward = 3 * kOne;
   // Rows i, columns j <= i: tile row x has the pairs 0 .. x / 2.
   static __host__ __device__ constexpr int lower(int x, int pair) { return (x / 2) * (x / 2 + 1) + (x & 1) * (x / 2 + 1) + pair; }
   // Rows j, columns i >= j: tile row x has the pairs x / 2 .. NI / 2 - 1; the mirror image.
@@ -168,13 +166,49 @@ __device__ __forceinline__ bool spread(uint32_t block, uint32_t units, uint32_t 
   return unit < units;
 }
 
-// A lane's fragment at `at` of a chunk's systems.
+// Part q of fragment `at` of a chunk's systems.
 template <typename E>
-__device__ __forceinline__ Frag<E> system_frag(const char* at) {
+__device__ __forceinline__ Frag<E> system_frag(const char* sys, int at, int q) {
   Frag<E> f;
-  __builtin_memcpy(&f, __builtin_assume_aligned(at + (threadIdx.x & 63) * (8 * sizeof(E)), 16), sizeof(f));
+  __builtin_memcpy(&f, __builtin_assume_aligned(sys + (at * Systems<E, 32>::kParts + q) * Systems<E, 32>::kFragBytes +
+                                                    (threadIdx.x & 63) * (8 * sizeof(E)), 16), sizeof(f));
   return f;
 }
+// A chunk's systems on their way from memory, BYTES by THREADS threads; stored as fragments in parts.  Split here, fp32 takes
+// two thirds of the parts' bytes in memory (16 x 2048 tokens of 16 heads of 128: 393 us, with parts in memory 412).  Every
+// thread has whole pieces and no condition stands around them, on purpose: the compiler has stored spilled registers before
+// it let all threads go on behind one, and read them back for all.
+template <typename E, int BYTES, int THREADS>
+struct SystemLoad {
+  static constexpr int kPieces = BYTES / 16 / THREADS;
+  static_assert(kPieces * 16 * THREADS == BYTES, "a thread's pieces are whole");
+  f32x4 x[kPieces];
+  __device__ __forceinline__ void load(const char* from) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) x[i] = *reinterpret_cast<const f32x4*>(from + (threadIdx.x + i * THREADS) * 16);
+  }
+  __device__ __forceinline__ void store(char* sys) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = threadIdx.x + i * THREADS;  // half of a lane's eight values
+      if constexpr (sizeof(E) == 4) {
+        *reinterpret_cast<f32x4*>(sys + piece * 16) = x[i];
+      } else {
+        f32x4 rest = x[i];
+#pragma unroll
+        for (int q = 0; q < Systems<E, 32>::kParts; ++q) {
+          const uint32_t w[2] = {pack_bf16(rest[0], rest[1]), pack_bf16(rest[2], rest[3])};
+          __builtin_memcpy(__builtin_assume_aligned(sys + ((piece / 128 * Systems<E, 32>::kParts + q) * 128 + piece % 128) * 8, 8), w, 8);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            rest[2 * r] -= __uint_as_float(w[r] << 16);
+            rest[2 * r + 1] -= __uint_as_float(w[r] & 0xffff0000u);
+          }
+        }
+      }
+    }
+  }
+};
 
 // Four consecutive elements of a row of which the first n are there (the others are 0).
 __device__ __forceinline__ f32x4 load4(const float* p, int n) {

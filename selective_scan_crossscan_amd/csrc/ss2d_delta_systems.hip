@@ -2,12 +2,12 @@
 //
 // With L_ij = exp(G_i - G_j) k_i . k_j for j < i, b = beta and P_ij = scale exp(G_i - G_j) q_i . k_j for j <= i, per
 // chunk of C tokens and head
-//   forward    N = (1 + L diag(b))^-1 - 1 and P in parts;
-//   gradients  the same N, and ((1 + diag(b) L)^-1)' - 1 and P' in parts,
-// as fragments in the order in which the walks read them.  Parts: what becomes an fp32 result, errors and states, keeps 24
-// bits in three, the ones on the diagonal left to the walks; P, which ends in an output of the storage type, 16 in two.
-// (With the inverses in two as well, 17 bits of what they add to an error, states were up to 1.6e-6 off where elementary
-// fp32 operations are 1.8e-7, for 5% of the time.)
+//   forward    N = (1 + L diag(b))^-1 - 1 and P;
+//   gradients  the same N, and ((1 + diag(b) L)^-1)' - 1 and P',
+// in fp32, as fragments in the order in which the walks read them, the ones on the diagonal left to those.  The walks take
+// all 24 bits in three bf16 parts: with two of an inverse states were up to 1.6e-6 off where elementary fp32 operations are
+// 1.8e-7; with two of P, of the replaced values and of the state towards an output bf16 outputs were 1.1e-4 from those of
+// elementary fp32 operations in the norm, with three 3.8e-5.
 //
 // A triangle is inverted in blocks of 16.  A diagonal block by substitution: a lane holds one row of the inverse and
 // the block's entries are read by all lanes at once; as stable as the system is, where a series of powers would cancel
@@ -102,17 +102,11 @@ __device__ __forceinline__ void drop_ones(int w, f32x4 (&x)[NI]) {
     for (int r = 0; r < 4; ++r) x[t][r] = t == w && 4 * g + r == l ? 0.f : x[t][r];
 }
 
-// Two stacked tiles to memory as a fragment's N parts.
-template <int N, typename E>
-__device__ __forceinline__ void put_frag(char* at, const f32x4& a, const f32x4& b) {
-  float u[8];
-  stack(a, b, u);
-  Frag<E> f[N];
-  split_parts(u, f);
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-    __builtin_memcpy(__builtin_assume_aligned(at + n * Systems<E, 32>::kFragBytes + (threadIdx.x & 63) * sizeof(f[n]), 16),
-                     &f[n], sizeof(f[n]));
+// Two stacked tiles to memory as fragment `at`.
+__device__ __forceinline__ void put_frag(char* out, int at, const f32x4& a, const f32x4& b) {
+  f32x4* to = reinterpret_cast<f32x4*>(out) + (at * 64 + (threadIdx.x & 63)) * 2;
+  to[0] = a;
+  to[1] = b;
 }
 
 // exp(G_i - G_j) for i .. i + 3
@@ -193,9 +187,9 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
     for (int pair = 0; pair < NI / 2; ++pair)
       if (BACK ? pair >= w / 2 : pair <= w / 2) {
         if (BACK)
-          put_frag<S::kParts, E>(out + 2 * S::kInverse + S::upper(w, pair) * S::kParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
+          put_frag(out + 2 * S::kOne, S::upper(w, pair), s[2 * pair], s[2 * pair + 1]);
         else
-          put_frag<S::kScoreParts, E>(out + S::kInverse + S::lower(w, pair) * S::kScoreParts * S::kFragBytes, s[2 * pair], s[2 * pair + 1]);
+          put_frag(out + S::kOne, S::lower(w, pair), s[2 * pair], s[2 * pair + 1]);
       }
   }
   __syncthreads();  // the queries have been read
@@ -218,7 +212,7 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
 #pragma unroll
   for (int pair = 0; pair < NI / 2; ++pair)
     if (pair <= w / 2)
-      put_frag<S::kParts, E>(out + S::lower(w, pair) * S::kParts * S::kFragBytes, x[2 * pair], x[2 * pair + 1]);
+      put_frag(out, S::lower(w, pair), x[2 * pair], x[2 * pair + 1]);
   if (!BACK) return;
   // (1 + diag(b) L)^-1, a lower triangle: rows i, columns j
   __syncthreads();  // the first triangle has been read
@@ -239,7 +233,7 @@ __global__ __launch_bounds__(C * 4) void delta_systems(DeltaParams p) {
 #pragma unroll
   for (int pair = 0; pair < NI / 2; ++pair)
     if (pair >= w / 2)
-      put_frag<S::kParts, E>(out + S::kInverse + S::upper(w, pair) * S::kParts * S::kFragBytes, x[2 * pair], x[2 * pair + 1]);
+      put_frag(out + S::kOne, S::upper(w, pair), x[2 * pair], x[2 * pair + 1]);
 }
 
 template <typename E, int C, bool BACK>

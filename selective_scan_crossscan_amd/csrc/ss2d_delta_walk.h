@@ -27,11 +27,6 @@ constexpr int kArrayTile = 64;  // columns of a tile of the chunks' arrays
 template <int KP>
 constexpr bool kAhead = KP <= 128;
 
-// Bytes for pieces of 16 by all threads: every thread writes all of its own, those behind the end into room that is not
-// read.  No condition there, on purpose: the compiler has stored spilled registers before it let all threads go on behind
-// one, and read them back for all.
-constexpr int whole_pieces(int bytes, int threads) { return (bytes + 16 * threads - 1) / (16 * threads) * (16 * threads); }
-
 enum DeltaPass { kOutputs, kSegments, kStates };
 
 template <typename E, int C, int KP, int VT, DeltaPass PASS>
@@ -39,8 +34,8 @@ struct WalkTiles {
   using S = Systems<E, C>;
   Tile<E, PASS == kOutputs ? C : 1, KP> qs;
   Tile<E, C, KP, 16> ks;
-  Tile<E, C, VT, 32> vs;
-  __attribute__((aligned(16))) char sys[whole_pieces(PASS == kOutputs ? S::kForward : S::kInverse, 256)];
+  Tile<E, C, VT, PASS == kOutputs ? 16 : 32> vs;  // 16: two workgroups' outputs fit a CU at 128 keys
+  __attribute__((aligned(16))) char sys[(PASS == kOutputs ? 2 : 1) * S::kFrags * S::kParts * S::kFragBytes];
   Rates<C> rates;
 };
 template <typename E, int C, int KP, int VT, int NV, DeltaPass PASS, bool TINY>
@@ -48,11 +43,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   constexpr int NW = VT / 16 / NV, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   using S = Systems<E, C>;
   constexpr int PN = S::kParts;
-  // Parts of what ends in an output of the storage type: two of all operands leave an output its own rounding alone (one
-  // of each: 1.5 to 1.8 times its error).
-  constexpr int PO = S::kScoreParts;
-  constexpr int kSystem = PASS == kOutputs ? S::kForward : S::kInverse;  // bytes read per chunk
-  constexpr int kPieces = (kSystem / 16 + THREADS - 1) / THREADS;
+  constexpr int kSystem = PASS == kOutputs ? S::kForward : S::kOne;  // bytes read per chunk
   auto& qs = lds.qs;
   auto& ks = lds.ks;
   auto& vs = lds.vs;
@@ -87,24 +78,21 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   struct Chunk {
     TileLoad<E, PASS == kOutputs ? C : 1, KP, 16, THREADS, TINY && KP == 32> q;
     TileLoad<E, C, KP, 16, THREADS, TINY && KP == 32> k;
-    TileLoad<E, C, VT, 32, THREADS, TINY> v;
-    uint4 s[kPieces];
+    TileLoad<E, C, VT, PASS == kOutputs ? 16 : 32, THREADS, TINY> v;
+    SystemLoad<E, kSystem, THREADS> s;
     float g, b;
   };
   auto fetch_rest = [&](Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
     const char* from = sb + (at - seg.begin) / C * sstep;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      x.s[i] = *reinterpret_cast<const uint4*>(from + min((int)threadIdx.x + i * THREADS, kSystem / 16 - 1) * 16);
+    x.s.load(from);
     const int64_t t = at + min(lane, n - 1);
     x.g = gb[t * p.g_stride[1]];
     x.b = bb[t * p.b_stride[1]];
   };
   auto land_rest = [&](const Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
+    x.s.store(sys);
     if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
   };
   auto fetch = [&](Chunk& x, int64_t at) {
@@ -224,7 +212,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
           for (int x = 0; x < NI; ++x) {
             const Frag<E> f = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-            for (int q = PO - 1; q >= 0; --q)
+            for (int q = PF - 1; q >= 0; --q)
 #pragma unroll
               for (int t = 0; t < NV; ++t) o[t][x] = mma(b[t][q], f, o[t][x]);
           }
@@ -261,7 +249,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 #pragma unroll
         for (int x = j; x < NI; ++x)
 #pragma unroll
-          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys + (S::lower(x, j / 2) * PN + q) * S::kFragBytes);
+          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys, S::lower(x, j / 2), q);
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
           float u[8];
@@ -291,7 +279,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
       if (PASS == kOutputs) {
 #pragma unroll
         for (int j = 0; j < NI; j += 2) {
-          Frag<E> a[NV][PO];
+          Frag<E> a[NV][PF];
 #pragma unroll
           for (int t = 0; t < NV; ++t) {
             float u[8];
@@ -300,11 +288,11 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
           }
 #pragma unroll
           for (int x = j; x < NI; ++x) {
-            Frag<E> s[PO];
+            Frag<E> s[PF];
 #pragma unroll
-            for (int q = 0; q < PO; ++q) s[q] = system_frag<E>(sys + S::kInverse + (S::lower(x, j / 2) * PO + q) * S::kFragBytes);
+            for (int q = 0; q < PF; ++q) s[q] = system_frag<E>(sys, S::kFrags + S::lower(x, j / 2), q);
 #pragma unroll
-            for (int n = PO - 1; n >= 0; --n)
+            for (int n = PF - 1; n >= 0; --n)
 #pragma unroll
               for (int q = 0; q <= n; ++q)
 #pragma unroll
@@ -392,7 +380,7 @@ struct BackTiles {
   using S = Systems<E, C>;
   Tile<E, C, KP, 16> qs, ks;  // 16 all: two workgroups' fit a CU at 128 keys and 64 values
   Tile<E, C, VT, 16> ds;
-  __attribute__((aligned(16))) char sys[whole_pieces(S::kBackward - S::kInverse, VT * 4)];  // the transposed inverse and P'
+  __attribute__((aligned(16))) char sys[2 * S::kFrags * S::kParts * S::kFragBytes];  // the transposed inverse and P'
   Rates<C> rates;
 };
 template <typename E, int C, int KP, int VT, bool SUM, bool TINY>
@@ -401,8 +389,7 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
   constexpr int NW = VT / 16, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   using S = Systems<E, C>;
   constexpr int PN = S::kParts;
-  constexpr int kSystem = S::kBackward - S::kInverse;  // the transposed inverse and P'
-  constexpr int kPieces = (kSystem / 16 + THREADS - 1) / THREADS;
+  constexpr int kSystem = S::kBackward - S::kOne;  // the transposed inverse and P'
   auto& qs = lds.qs;
   auto& ks = lds.ks;
   auto& ds = lds.ds;
@@ -430,29 +417,26 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
   const float* gb = p.g + sq * p.g_stride[0] + token0 * p.g_stride[1] + head * p.g_stride[2];
   const float* bb = p.beta + sq * p.b_stride[0] + token0 * p.b_stride[1] + head * p.b_stride[2];
   const int64_t chunk0 = chunk_number<C>(p.map, seg, seg.begin);
-  const char* sb = p.systems + (chunk0 * p.heads + head) * p.system_stride + S::kInverse;
+  const char* sb = p.systems + (chunk0 * p.heads + head) * p.system_stride + S::kOne;
   const int64_t sstep = p.heads * p.system_stride;
 
   struct Chunk {
     TileLoad<E, C, KP, 16, THREADS, TINY && KP == 32> q, k;
     TileLoad<E, C, VT, 16, THREADS, TINY> d;
-    uint4 s[kPieces];
+    SystemLoad<E, kSystem, THREADS> s;
     float g, b;
   };
   auto fetch_rest = [&](Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
     const char* from = sb + (at - seg.begin) / C * sstep;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      x.s[i] = *reinterpret_cast<const uint4*>(from + min((int)threadIdx.x + i * THREADS, kSystem / 16 - 1) * 16);
+    x.s.load(from);
     const int64_t t = at + min(lane, n - 1);
     x.g = gb[t * p.g_stride[1]];
     x.b = bb[t * p.b_stride[1]];
   };
   auto land_rest = [&](const Chunk& x, int64_t at) {
     const int n = (int)min((int64_t)C, seg.end - at);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(sys + (threadIdx.x + i * THREADS) * 16) = x.s[i];
+    x.s.store(sys);
     if (wave == 0) scan_rates<C>(lane < n ? x.g : 0.f, lane < n ? x.b : 0.f, rates);
   };
   auto fetch = [&](Chunk& x, int64_t at) {
@@ -571,7 +555,7 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
         for (int q = PF - 1; q >= 0; --q)
 #pragma unroll
           for (int x = 0; x < j + 2; ++x)
-            u[x] = mma(system_frag<E>(sys + S::kInverse + (S::upper(x, j / 2) * PF + q) * S::kFragBytes), f, u[x]);
+            u[x] = mma(system_frag<E>(sys, S::kFrags + S::upper(x, j / 2), q), f, u[x]);
       }
       __builtin_amdgcn_sched_barrier(0);
       // dF = dU + N' dU
@@ -585,7 +569,7 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
 #pragma unroll
         for (int x = 0; x < j + 2; ++x)
 #pragma unroll
-          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys + (S::upper(x, j / 2) * PN + q) * S::kFragBytes);
+          for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys, S::upper(x, j / 2), q);
         stack(u[j], u[j + 1], y);
         split_parts(y, f);
         j == 0 ? mma_parts<0, 2>(a, f, z) : mma_parts<0, NI>(a, f, z);

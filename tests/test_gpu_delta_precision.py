@@ -1,4 +1,4 @@
-"""The bits that the delta rule's gradients keep in bf16, on the GPU.
+"""The bits that the delta rule keeps in bf16, on the GPU.
 
 Differences that only whole operands leave: each call below is made so that one entry of a result is the difference of
 two sums of 1 + 2^-9 and more, one of them 2^-20 larger.  Every product and sum on the way to it is exact in fp32 in any
@@ -13,6 +13,7 @@ import pytest
 
 from delta_reference import gradient_terms, make, values
 from oracle import delta
+from test_gpu_delta import CASES, _dev, _host, _lib, packed
 from test_gpu_delta_backward import CASES as GRADIENT_CASES, run
 
 pytestmark = pytest.mark.gpu
@@ -27,6 +28,42 @@ def _zeros(T, K=40, V=24):
     """q, k, v, g, beta, state, do, dstate of one head, all 0, as arrays that a case fills in."""
     return {"q": np.zeros((T, 1, K)), "k": np.zeros((T, 1, K)), "v": np.zeros((T, 1, V)), "g": np.zeros((T, 1)),
             "b": np.zeros((T, 1)), "st": np.zeros((1, 1, K, V)), "do": np.zeros((T, 1, V)), "dl": np.zeros((1, 1, K, V))}
+
+
+def _state(x):
+    """o = h' q, h in 24 bits."""
+    x["st"][0, 0, 5, 7], x["st"][0, 0, 33, 7] = LONG, SHORT
+    x["q"][2, 0, [5, 33]] = 1, -1
+    return 2, 7
+
+
+def _scores(x):
+    """o_40 = P u_0 + P u_1, P in 24 bits; the second token's value makes its u 1."""
+    x["k"][0, 0, [0, 1, 35]] = 1, A, E
+    x["k"][1, 0, [0, 1]] = -1, -A
+    x["v"][0, 0], x["v"][1, 0], x["b"][:2] = 1, -(A * A), 1
+    x["q"][40, 0, [0, 1, 35]] = 1, B, E
+    return 40, 3
+
+
+def _replaced(x):
+    """o_20 = u_0 - u_1, u in 24 bits by beta."""
+    x["k"][0, 0, 3] = x["k"][1, 0, 38] = 1
+    x["v"][:2, 0], x["b"][0], x["b"][1] = 1, LONG, SHORT
+    x["q"][20, 0, [3, 38]] = 1, -1
+    return 20, 11
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [_state, _scores, _replaced], ids=lambda f: f.__name__[1:])
+def test_outputs_of_whole_operands(case, dtype):
+    x = _zeros(41)
+    t, c = case(x)
+    args = tuple(x[n] for n in ("q", "k", "v", "g", "b", "st"))
+    want = delta.delta_rule(*args[:5], [41], args[5])[0]
+    assert want[t, 0, c] == 2.0 ** -20
+    got = _host(packed(args, [41], dtype)[0])
+    assert got[t, 0, c] == 2.0 ** -20
 
 
 def _behind(x):
@@ -125,6 +162,20 @@ def _beyond(name, got, ref, terms, n):
     norm, whole = np.linalg.norm(over), 2 * np.sqrt(n) * 2.0 ** -24 * np.linalg.norm(terms) + 1e-37
     print(f"[delta] {name}: beyond half a step / tolerance {np.max(over / tol):.3f}, of the norm {norm / whole:.3f}", flush=True)
     assert np.all(over <= tol) and norm <= whole, name
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_outputs_show_their_own_rounding_alone(case):
+    lens, G, H, K, V = case
+    args = make(lens, G, H, K, V, "bf16", seed=len(lens) * K + V + 1)
+    q, k, v, g, b, st = args
+    scale = K ** -0.5
+    o = _host(packed(args, lens, "bf16", scale)[0])
+    terms, mass = delta.delta_rule_terms(q, k, v, g, b, lens, st, scale, 64)
+    # what is in the state before a chunk has its own errors, in every direction
+    over = scale * np.repeat(np.linalg.norm(q, axis=-1), H // G, 1)[..., None]
+    per = np.concatenate([np.broadcast_to(mass[s], (n,) + mass.shape[1:]) for s, n in enumerate(lens)])
+    _beyond("o", o, delta.delta_rule(q, k, v, g, b, lens, st, scale)[0], terms + over * np.maximum(per, terms), K + V + 64)
 
 
 @pytest.mark.parametrize("case", GRADIENT_CASES, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
