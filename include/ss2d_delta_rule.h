@@ -128,8 +128,10 @@ typedef struct {
  *              number in its sequence.  Clamped to 0..table_rows-1 on the device
  *   interleaved  0: channels i and i + rotated / 2 are a pair (i < rotated / 2);
  *              1: channels 2 i and 2 i + 1
- *   q_out, k_out  as q and k, strided; each may be q or k itself (the same strides), and
- *              the two sides may lie in the same rows, as slices of one projection do
+ *   q_out, k_out  as q and k, strided; each may be its own input (the same strides), and
+ *              the two sides may lie in one tensor in any layout that leaves them no
+ *              address in common: slices of a projection's rows, q, k and v side by side
+ *              for each head, heads or planes before tokens (SS2D_ERR_ALIAS otherwise)
  * All arithmetic is fp32, each output rounded once.  A head with squares that overflow
  * fp32 (values over 2^63) gives 0, a head of zeros 0 too, but NaN if eps is 0.  At most 2^31-1 tokens times heads, dim 1..256,
  * eps >= 0 and finite (SS2D_ERR_SHAPE otherwise).  One kernel, no workspace.

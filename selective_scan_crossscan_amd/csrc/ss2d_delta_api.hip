@@ -78,17 +78,49 @@ bool apart(const Rows& r, const ss2d_qk_sizes& z) {
   }
   return true;
 }
-// Whether two tensors have no address in common: by their bytes, or as different columns of the same rows.
+// Whether x + sum of c s lies within `width` of 0 for some whole c in lo .. hi of each step; steps descend.  A step that is
+// as wide as all that follow span leaves two or three c to look at; where steps mix so that there would be many, true.
+struct Step {
+  int64_t s, lo, hi;
+};
+bool meets(const Step* at, const Step* end, int64_t x, int64_t width, int& tries) {
+  if (at == end) return x < width && -x < width;
+  if (--tries < 0) return true;
+  int64_t low = 1 - width, high = width - 1;  // what the others leave to come within reach
+  for (const Step* i = at + 1; i < end; ++i) {
+    low -= i->hi * i->s;
+    high -= i->lo * i->s;
+  }
+  const int64_t from = low - x, to = high - x;
+  int64_t c = from / at->s + (from % at->s > 0), last = to / at->s - (to % at->s < 0);
+  if (c < at->lo) c = at->lo;
+  if (last > at->hi) last = at->hi;
+  for (; c <= last; ++c)
+    if (meets(at + 1, end, x + c * at->s, width, tries)) return true;
+  return false;
+}
+// Whether two tensors have no address in common, whatever the order of their axes in memory.
 bool disjoint(const Rows& a, const Rows& b, const ss2d_qk_sizes& z, int64_t e) {
   if (!overlap(Range{a.p, bytes_of(a, z, e)}, Range{b.p, bytes_of(b, z, e)})) return true;
-  const int64_t step = z.tokens > 1 ? a.stride[1] : a.stride[0];
-  if (z.tokens > 1 && a.stride[1] != b.stride[1]) return false;
-  if (z.sequences > 1 && (a.stride[0] != b.stride[0] || (z.tokens > 1 && a.stride[0] % step != 0))) return false;
-  const int64_t wa = (a.heads - 1) * a.stride[2] + z.dim, wb = (b.heads - 1) * b.stride[2] + z.dim;
-  const int64_t off = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
-  if (off % e != 0) return false;
-  const int64_t d = off / e;
-  return d >= 0 ? d >= wa && d + wb <= step : -d >= wb && wa - d <= step;
+  const int64_t na[3] = {z.sequences, z.tokens, a.heads}, nb[3] = {z.sequences, z.tokens, b.heads};
+  Step steps[6];
+  int n = 0;
+  auto add = [&](int64_t stride, int64_t lo, int64_t hi) {
+    if (stride == 0 || lo == hi) return;
+    int i = n++;
+    for (; i > 0 && steps[i - 1].s < stride * e; --i) steps[i] = steps[i - 1];
+    steps[i] = Step{stride * e, lo, hi};
+  };
+  for (int i = 0; i < 3; ++i) {
+    if (a.stride[i] == b.stride[i]) {  // one step: the difference of the places
+      add(a.stride[i], 1 - na[i], nb[i] - 1);
+    } else {
+      add(na[i] > 1 ? a.stride[i] : 0, 1 - na[i], 0);
+      add(nb[i] > 1 ? b.stride[i] : 0, 0, nb[i] - 1);
+    }
+  }
+  int tries = 1 << 12;
+  return !meets(steps, steps + n, (int64_t)((uintptr_t)b.p - (uintptr_t)a.p), z.dim * e, tries);
 }
 
 int check_qk(const void* q, const void* k, const float* qw, const float* kw, const float* table,

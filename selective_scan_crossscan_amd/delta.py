@@ -252,7 +252,8 @@ def qk_norm(q, k, q_weight=None, k_weight=None, rotation=None, positions=None, i
     float32: a position's cosines, then its sines (rotation_table), the first `rotated` channels of a head turn; None:
     no rotation.  positions: int32 of the leading axes (clamped to the table), or None: the token's number in its
     sequence.  interleaved: channels 2i and 2i+1 are a pair instead of i and i + rotated/2.  D <= 256.
-    out: a pair of tensors for the results, any strides with a dense last axis; q and k themselves too.
+    out: a pair of tensors for the results, any strides with a dense last axis that leave their elements apart; q and k
+    themselves too, also as slices of one tensor in any layout that leaves the two no address in common.
     Returns (q, k) normed and rotated.
     """
     if stream is not None:
