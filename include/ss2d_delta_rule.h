@@ -57,7 +57,10 @@ int ss2d_delta_rule(const void* q, const void* k, const void* v, const float* lo
 
 /* Bytes of workspace ss2d_delta_rule needs, or a negative status.  packed: 1 if it will
  * be given cu_seqlens, else 0.  24 KiB per 64 tokens and head (8 KiB per 32 in fp32),
- * and the states of segments where few sequences and heads have to be cut. */
+ * each packed sequence's last chunk counted whole; and where long sequences of few heads
+ * are cut, packed ones too that might be long, a state and a key_dim x key_dim map per
+ * segment and head: at most about 2048 / tiles of 64 value columns of these, however many
+ * sequences there are. */
 int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int dtype);
 
 /*

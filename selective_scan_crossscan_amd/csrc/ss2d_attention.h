@@ -140,8 +140,10 @@ __device__ __forceinline__ int64_t chunk_number(const SequenceMap& m, const Segm
   return (m.cu ? g.start / C + g.s : g.s * ((m.len + C - 1) / C)) + at / C;
 }
 
-// False where no segment has this slot.
-__device__ __forceinline__ bool find_segment(const SequenceMap& m, int64_t slot, Segment& g) {
+// False where no segment has this slot.  cut: slots of packed sequences that have several segments alone, first ones
+// 2 cu[s] / seg_len: a sequence of n >= 2 segments is longer than (n - 1) seg_len, so all later ones' first slots are at
+// least 2 (n - 1) >= n on, and 2 tokens / seg_len + 1 slots are enough however many sequences there are.
+__device__ __forceinline__ bool find_segment(const SequenceMap& m, int64_t slot, Segment& g, bool cut = false) {
   int64_t seg;
   if (!m.cu) {
     g.s = (int)(slot / m.nseg);
@@ -157,7 +159,8 @@ __device__ __forceinline__ bool find_segment(const SequenceMap& m, int64_t slot,
     for (int left = m.sequences, step; left > 1; left = min(left, step)) {
       step = (left + 63) / 64;
       const int ahead = min((int)(threadIdx.x & 63) * step, left);
-      const bool before = ahead < left && (int64_t)((uint32_t)cu_at(m, lo + min(ahead, left - 1)) / seg_len) + lo + ahead <= slot;
+      const uint32_t at = (uint32_t)cu_at(m, lo + min(ahead, left - 1));
+      const bool before = ahead < left && (cut ? (int64_t)(2 * at / seg_len) : (int64_t)(at / seg_len) + lo + ahead) <= slot;
       const int count = (int)__popcll(__ballot(before));
       const int skip = count > 1 ? (count - 1) * step : 0;  // offsets that do not ascend may leave none
       lo += skip;
@@ -167,8 +170,8 @@ __device__ __forceinline__ bool find_segment(const SequenceMap& m, int64_t slot,
     g.start = cu_at(m, lo);
     const int64_t end = cu_at(m, lo + 1);
     g.len = end > g.start ? end - g.start : 0;
-    seg = slot - (g.start / m.seg_len + lo);
-    if (seg < 0) return false;
+    seg = slot - (cut ? 2 * g.start / m.seg_len : g.start / m.seg_len + lo);
+    if (seg < 0 || (cut && g.len <= m.seg_len)) return false;
   }
   g.begin = seg * m.seg_len;
   if (g.begin > 0 && g.begin >= g.len) return false;

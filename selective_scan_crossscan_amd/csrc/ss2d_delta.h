@@ -47,6 +47,8 @@ struct DeltaArgs {
 struct DeltaPlan {
   AttentionPlan a;      // kp, chunk, segments, slots, chunks; vt the walk's
   bool backward;
+  bool cut;             // segments' states are kept for sequences of several segments alone
+  int64_t parts;        // segments whose states are kept, an upper bound
 };
 DeltaPlan plan_delta(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
                      int dtype);
@@ -85,8 +87,8 @@ struct DeltaParams {
   void* o;
   float* state_out;         // or null
   char* systems;            // (chunk, head): inverse, scores; backward: inverse, transposed inverse and scores
-  float* seg_state;         // (slot, head, K, V): what a segment adds, after the carry the state before it
-  float* seg_map;           // (slot, head, KP, KP): the segment's map of the state before it
+  float* seg_state;         // (part, head, K, V): what a segment adds, after the carry the state before it
+  float* seg_map;           // (part, head, KP, KP): the segment's map of the state before it
   float* chunk_state;       // (chunk, head, tile, KP, 64): the state before every chunk, 0 outside K and V
   float* errors;            // (chunk, head, tile, C, 64): E, 0 behind the chunk's tokens and outside V
   SequenceMap map;          // segments
@@ -97,6 +99,7 @@ struct DeltaParams {
   uint32_t blocks;          // workgroups; of a walk: units of a segment and head, each with its tiles
   float scale;
   bool split;               // segments start from seg_state
+  bool cut;                 // parts are the slots of sequences of several segments alone; else of all
   bool last_maps;           // segment maps of the sequences' last segments too, for the way back
   int64_t system_stride;    // bytes of a chunk's and head's systems
 };
@@ -109,10 +112,11 @@ hipError_t launch_delta_segments(DeltaParams p, const DeltaPlan& pl, int dtype, 
 hipError_t launch_delta_states(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st);
 // seg: what segments add to the state (backwards: to its gradient) becomes the states before (the gradients behind) them.
 struct CarryParams {
-  float* seg;            // (slot, head, K, V)
-  const float* seg_map;  // (slot, head, KP, KP)
+  float* seg;            // (part, head, K, V)
+  const float* seg_map;  // (part, head, KP, KP)
   const float* from;     // (sequence, head, K, V) or null
   SequenceMap map;
+  bool cut;
   int heads, K, V, vtiles;
   uint32_t blocks;
 };
@@ -122,6 +126,13 @@ hipError_t launch_delta_carry(CarryParams p, const CarryParams* back, const Delt
 int64_t system_bytes(const DeltaPlan& pl, int dtype);
 
 namespace tok {
+
+// A segment's part.
+__device__ __forceinline__ int64_t part_number(const SequenceMap& m, bool cut, const Segment& g) {
+  const uint32_t seg_len = (uint32_t)m.seg_len, seg = (uint32_t)g.begin / seg_len;
+  if (!m.cu) return (int64_t)g.s * m.nseg + seg;
+  return (int64_t)((cut ? 2 : 1) * (uint32_t)g.start / seg_len) + (cut ? 0 : g.s) + seg;
+}
 
 // c[x] += a[x] b for x in from .. to - 1, both operands in parts: those whose share of the product lies under the last
 // part's (p + q >= N) are left out, the smallest come first, and products of different x stand next to each other.

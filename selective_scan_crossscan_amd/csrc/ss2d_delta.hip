@@ -38,17 +38,12 @@ __device__ __forceinline__ void carry(const CarryParams& p, uint32_t block, Carr
   constexpr bool AHEAD = kAhead<KP>;  // the next segment's M and u wait in registers
   auto& parts = lds.parts;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const int tile = block % p.vtiles, head = block / p.vtiles % p.heads, s = block / p.vtiles / p.heads;
-  int64_t slot, len;
-  if (p.map.cu) {
-    const int64_t start = cu_at(p.map, s), end = cu_at(p.map, s + 1);
-    slot = start / p.map.seg_len + s;
-    len = end - start;
-  } else {
-    slot = (int64_t)s * p.map.nseg;
-    len = p.map.len;
-  }
-  const int64_t n = (len + p.map.seg_len - 1) / p.map.seg_len;  // segments
+  const int tile = block % p.vtiles, head = block / p.vtiles % p.heads, unit = block / p.vtiles / p.heads;
+  Segment first;  // a sequence's; the unit is its part, of equal lengths the sequence
+  const int64_t slot = p.map.cu ? unit : (int64_t)unit * p.map.nseg;
+  if (!find_segment(p.map, slot, first, p.cut) || first.begin > 0) return;
+  const int s = first.s;
+  const int64_t n = (first.len + p.map.seg_len - 1) / p.map.seg_len;  // segments
   if (n < 2) return;
   const int64_t kv = (int64_t)p.K * p.V;
   auto row = [&](int a, int r) { return (wave + a * NW) * 16 + 4 * g + r; };
@@ -187,7 +182,7 @@ template <typename E, int C, DeltaPass PASS>
 hipError_t launch_walk(DeltaParams p, const DeltaPlan& pl, hipStream_t st) {
   p.vtiles = (p.V + 63) / 64;
   p.ktiles = (pl.a.kp + 63) / 64;
-  p.blocks = (uint32_t)(pl.a.slots * p.heads);
+  p.blocks = (uint32_t)((PASS == kSegments ? pl.parts : pl.a.slots) * p.heads);
   const int64_t blocks = spread_blocks(p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles);
   with_keys(pl, [&](auto kp, auto tiny) {
     delta_walk<E, C, kp(), PASS, tiny()><<<grid_of(blocks, 256), dim3(256), 0, st>>>(p);
@@ -222,6 +217,10 @@ DeltaPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t ke
   a.seg_len = seg;
   a.nseg = (int)((longest + seg - 1) / seg);
   a.slots = packed ? tokens / seg + sequences : sequences * a.nseg;
+  // Packed sequences' kept segments are numbered as their slots are, or with many sequences those of the cut ones alone:
+  // 1024 sequences of 64 tokens, 16 heads of 128, keep 68 MiB for them instead of 2080, 1395 us instead of 1646.
+  pl.cut = packed && sequences > tokens / seg + 2;
+  pl.parts = pl.cut ? 2 * tokens / seg + 2 : a.slots;
   a.chunks = packed ? tokens / chunk + sequences : sequences * ((longest + chunk - 1) / chunk);
   return pl;
 }
@@ -238,8 +237,8 @@ Regions regions(const DeltaPlan& pl, int64_t heads, int64_t K, int64_t V, int dt
     return here;
   };
   r.systems = take(pl.a.chunks * heads * system_bytes(pl, dtype));
-  r.seg_state = take(pl.a.split ? pl.a.slots * heads * K * V * 4 : 0);
-  r.seg_map = take(pl.a.split ? pl.a.slots * heads * pl.a.kp * pl.a.kp * 4 : 0);
+  r.seg_state = take(pl.a.split ? pl.parts * heads * K * V * 4 : 0);
+  r.seg_map = take(pl.a.split ? pl.parts * heads * pl.a.kp * pl.a.kp * 4 : 0);
   r.end = at;
   return r;
 }
@@ -262,7 +261,9 @@ DeltaPlan plan_delta_backward(int64_t sequences, int64_t tokens, int64_t heads, 
 
 int64_t delta_blocks(const DeltaPlan& pl, int64_t sequences, int64_t heads, int64_t value_dim) {
   const int64_t v = (value_dim + 63) / 64, k = (pl.a.kp + 63) / 64;
-  const int64_t walk = spread_blocks(pl.a.slots * heads, (int)(2 * v + k)), systems = pl.a.chunks * heads, carry = 2 * sequences * heads * ((value_dim + kCarryColumns - 1) / kCarryColumns);
+  const int64_t most = pl.a.slots > pl.parts ? pl.a.slots : pl.parts, walk = spread_blocks(most * heads, (int)(2 * v + k)),
+                systems = pl.a.chunks * heads,
+                carry = 2 * (sequences > pl.parts ? sequences : pl.parts) * heads * ((value_dim + kCarryColumns - 1) / kCarryColumns);
   return walk > systems ? (walk > carry ? walk : carry) : systems > carry ? systems : carry;
 }
 
@@ -298,6 +299,7 @@ DeltaParams delta_params(const DeltaArgs& a, const DeltaPlan& pl) {
   p.V = (int)f.value_dim;
   p.scale = f.scale;
   p.split = pl.a.split;
+  p.cut = pl.cut;
   p.system_stride = system_bytes(pl, f.dtype);
   return p;
 }
@@ -305,13 +307,13 @@ DeltaParams delta_params(const DeltaArgs& a, const DeltaPlan& pl) {
 hipError_t launch_delta_segments(DeltaParams p, const DeltaPlan& pl, int dtype, hipStream_t st) {
   const hipError_t e = dtype == 1 ? launch_walk<uint16_t, 64, kSegments>(p, pl, st) : launch_walk<float, 32, kSegments>(p, pl, st);
   if (e != hipSuccess) return e;
-  const CarryParams c{p.seg_state, p.seg_map, p.state_in, p.map, p.heads, p.K, p.V, 0, 0};
+  const CarryParams c{p.seg_state, p.seg_map, p.state_in, p.map, p.cut, p.heads, p.K, p.V, 0, 0};
   return launch_delta_carry(c, nullptr, pl, st);
 }
 
 hipError_t launch_delta_carry(CarryParams c, const CarryParams* back, const DeltaPlan& pl, hipStream_t st) {
   c.vtiles = (c.V + kCarryColumns - 1) / kCarryColumns;
-  c.blocks = (uint32_t)((int64_t)c.map.sequences * c.heads * c.vtiles);
+  c.blocks = (uint32_t)((c.map.cu ? pl.parts : (int64_t)c.map.sequences) * c.heads * c.vtiles);
   CarryParams r = back ? *back : c;
   r.vtiles = c.vtiles;
   r.blocks = c.blocks;

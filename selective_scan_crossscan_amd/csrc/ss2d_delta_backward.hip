@@ -452,9 +452,9 @@ Regions regions(const DeltaPlan& pl, int64_t tokens, int64_t groups, int64_t hea
   };
   const AttentionPlan& a = pl.a;
   r.systems = take(a.chunks * heads * (system_bytes(pl, dtype) / 4));
-  r.seg_state = take(a.split ? a.slots * heads * K * V : 0);
-  r.seg_map = take(a.split ? a.slots * heads * a.kp * a.kp : 0);
-  r.seg_dstate = take(a.split ? a.slots * heads * K * V : 0);
+  r.seg_state = take(a.split ? pl.parts * heads * K * V : 0);
+  r.seg_map = take(a.split ? pl.parts * heads * a.kp * a.kp : 0);
+  r.seg_dstate = take(a.split ? pl.parts * heads * K * V : 0);
   const int64_t per = a.chunks * heads * padded_values(V, pl);
   r.chunk_state = take(per * a.kp);
   r.chunk_dstate = take(per * a.kp);
@@ -489,7 +489,7 @@ hipError_t launch_segments(DeltaParams p, BackParams b, const DeltaPlan& pl, hip
   p.last_maps = true;
   p.vtiles = b.d.vtiles = (p.V + 63) / 64;
   p.ktiles = (pl.a.kp + 63) / 64;
-  p.blocks = b.blocks = (uint32_t)(pl.a.slots * p.heads);
+  p.blocks = b.blocks = (uint32_t)(pl.parts * p.heads);
   const int64_t first = spread_blocks(p.blocks, p.vtiles + p.ktiles);
   with_keys(pl, [&](auto kp, auto tiny) {
     delta_segment_pair<E, C, kp(), tiny()>
@@ -497,8 +497,8 @@ hipError_t launch_segments(DeltaParams p, BackParams b, const DeltaPlan& pl, hip
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const CarryParams c{p.seg_state, p.seg_map, p.state_in, p.map, p.heads, p.K, p.V, 0, 0};
-  const CarryParams r{b.seg_dstate, p.seg_map, b.dstate_out, p.map, p.heads, p.K, p.V, 0, 0};
+  const CarryParams c{p.seg_state, p.seg_map, p.state_in, p.map, p.cut, p.heads, p.K, p.V, 0, 0};
+  const CarryParams r{b.seg_dstate, p.seg_map, b.dstate_out, p.map, p.cut, p.heads, p.K, p.V, 0, 0};
   return launch_delta_carry(c, &r, pl, st);
 }
 

@@ -55,9 +55,9 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   uint32_t unit, at_tile;
   if (!spread(block, p.blocks, PASS == kSegments ? p.vtiles + p.ktiles : p.vtiles, unit, at_tile)) return;
   const int tile = at_tile, head = unit % p.heads;
-  const int64_t slot = unit / p.heads;
+  const int64_t slot = unit / p.heads;  // of kSegments a part
   Segment seg;
-  if (!find_segment(p.map, slot, seg)) return;
+  if (!find_segment(p.map, slot, seg, PASS == kSegments && p.cut)) return;
   const bool map = PASS == kSegments && tile >= p.vtiles;  // columns of the identity instead of values
   if (PASS == kSegments && seg.last && !(map && p.last_maps && seg.begin > 0)) return;  // of no use
   const int group = head / (p.heads / p.groups);
@@ -135,8 +135,8 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 
   // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
   f32x4 h[NK][NV];
-  const int64_t kv = (int64_t)K * p.V, sh = ((int64_t)slot * p.heads + head) * kv, qh = ((int64_t)seg.s * p.heads + head) * kv;
-  const float* from = PASS == kSegments ? nullptr : p.split && seg.several() ? p.seg_state + sh : p.state_in ? p.state_in + qh : nullptr;
+  const int64_t kv = (int64_t)K * p.V, qh = ((int64_t)seg.s * p.heads + head) * kv;
+  const float* from = PASS == kSegments ? nullptr : p.split && seg.several() ? p.seg_state + (part_number(p.map, p.cut, seg) * p.heads + head) * kv : p.state_in ? p.state_in + qh : nullptr;
 #pragma unroll
   for (int t = 0; t < NV; ++t) {
     const int v = vw + t * 16 + l;
@@ -342,7 +342,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
       bring(ahead);
   }
 
-  float* to = PASS == kSegments ? (map ? p.seg_map + ((int64_t)slot * p.heads + head) * (KP * KP) : p.seg_state + sh)
+  float* to = PASS == kSegments ? (map ? p.seg_map + (slot * p.heads + head) * (KP * KP) : p.seg_state + (slot * p.heads + head) * kv)
               : PASS == kOutputs && seg.last && p.state_out ? p.state_out + qh : nullptr;
   if (to) {
     const int rows = map ? KP : K, step = map ? KP : p.V;
@@ -363,7 +363,7 @@ struct BackParams {
   const void* d_o;
   int64_t do_stride[3];
   const float* dstate_out;  // or null
-  float* seg_dstate;        // (slot, head, K, V): what a segment adds, after the carry the gradient behind it
+  float* seg_dstate;        // (part, head, K, V): what a segment adds, after the carry the gradient behind it
   float* chunk_dstate;      // (chunk, head, tile, KP, 64): D behind every chunk
   float* df;                // (chunk, head, tile, C, 64)
   float* inner;             // (chunk, head, 16-column tile): parts of sum_j u_j . (w K D)_j
@@ -400,9 +400,9 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
   uint32_t unit, tile;
   if (!spread(block, b.blocks, p.vtiles, unit, tile)) return;
   const int vt = tile, head = unit % p.heads;
-  const int64_t slot = unit / p.heads;
+  const int64_t slot = unit / p.heads;  // of SUM a part
   Segment seg;
-  if (!find_segment(p.map, slot, seg)) return;
+  if (!find_segment(p.map, slot, seg, SUM && p.cut)) return;
   if (SUM && seg.begin == 0) return;  // of no use
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = vt * VT, nv = min(p.V - v0, VT), v = wave * 16 + l;
@@ -474,8 +474,8 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
 
   // D: rows 16 kt + 4 g + r, column v
   f32x4 d[NK];
-  const int64_t kv = (int64_t)K * p.V, sh = (slot * p.heads + head) * kv, qh = ((int64_t)seg.s * p.heads + head) * kv;
-  const float* from = SUM ? nullptr : !seg.last ? b.seg_dstate + sh : b.dstate_out ? b.dstate_out + qh : nullptr;
+  const int64_t kv = (int64_t)K * p.V, qh = ((int64_t)seg.s * p.heads + head) * kv;
+  const float* from = SUM ? nullptr : !seg.last ? b.seg_dstate + (part_number(p.map, p.cut, seg) * p.heads + head) * kv : b.dstate_out ? b.dstate_out + qh : nullptr;
 #pragma unroll
   for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
@@ -626,7 +626,7 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
     else
       bring(ahead);
   }
-  float* to = SUM ? b.seg_dstate + sh : seg.begin == 0 && b.dstate_in ? b.dstate_in + qh : nullptr;
+  float* to = SUM ? b.seg_dstate + (slot * p.heads + head) * kv : seg.begin == 0 && b.dstate_in ? b.dstate_in + qh : nullptr;
   if (to)
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
