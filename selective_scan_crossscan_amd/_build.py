@@ -2,8 +2,11 @@
 from __future__ import annotations
 
 import os
+import re
 import shutil
+import struct
 import subprocess
+import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +50,47 @@ def _run(cmd, verbose):
         print(out)
 
 
+def vector_spills(path: str) -> dict:
+    """Kernel (mangled name) -> vector registers spilled to memory, of all gfx950 kernels in a library or object that hipcc
+    built, from the metadata beside their code."""
+    tool = next((c for c in (os.path.join(os.path.dirname(os.path.realpath(hipcc())), "..", "llvm", "bin", "llvm-readelf"),
+                             "/opt/rocm/llvm/bin/llvm-readelf", shutil.which("llvm-readelf")) if c and os.path.exists(c)), None)
+    if tool is None:
+        raise RuntimeError("llvm-readelf not found (it comes with ROCm's compiler)")
+    with open(path, "rb") as f:
+        data = f.read()
+    out = {}
+    magic = b"__CLANG_OFFLOAD_BUNDLE__"
+    at = data.find(magic)
+    while at >= 0:
+        entry = at + len(magic) + 8
+        for _ in range(struct.unpack_from("<Q", data, entry - 8)[0]):
+            begin, size, length = struct.unpack_from("<QQQ", data, entry)
+            name = data[entry + 24:entry + 24 + length]
+            entry += 24 + length
+            if name.endswith(b"gfx950"):
+                with tempfile.NamedTemporaryFile() as code:
+                    code.write(data[at + begin:at + begin + size])
+                    code.flush()
+                    notes = subprocess.run([tool, "--notes", code.name], capture_output=True, text=True, check=True).stdout
+                # one kernel's fields are in the order of their names
+                for kernel, scratch, spilled in re.findall(
+                        r"^ +\.name: +(\S+)\n(?:(?! +\.name:).*\n)*? +\.private_segment_fixed_size: (\d+)\n"
+                        r"(?:(?! +\.name:).*\n)*? +\.vgpr_spill_count: (\d+)", notes, flags=re.M):
+                    out[kernel] = max(out.get(kernel, 0), int(spilled), 1 if int(scratch) else 0)
+        at = data.find(magic, at + 1)
+    return out
+
+
+def check_registers(path: str) -> None:
+    """Kernels of the delta rule must keep all vector registers.  Compiled with too few, those of 256 keys stored some to
+    memory while only part of a wave's threads were active and read them back for all: wrong results, and addresses out of
+    range."""
+    bad = {k: n for k, n in vector_spills(path).items() if n and "delta_" in k}
+    if bad:
+        raise RuntimeError(f"spilled vector registers where none may be: {bad}")
+
+
 def build(verbose: bool = False, jobs: int = 0) -> str:
     """Compile every HIP source into selective_scan_crossscan_amd/libss2d.so; returns its path."""
     tag = f".tmp{os.getpid()}"
@@ -63,9 +107,10 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
                 f.result()
         tmp = LIB + tag
         _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
+        check_registers(tmp)
         os.replace(tmp, LIB)
     finally:
-        for o in objs:
+        for o in objs + [LIB + tag]:
             if os.path.exists(o):
                 os.remove(o)
     return LIB
