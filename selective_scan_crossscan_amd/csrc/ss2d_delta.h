@@ -51,9 +51,7 @@ struct DeltaPlan {
   int64_t parts;        // segments whose states are kept, an upper bound
 };
 DeltaPlan plan_delta(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
-                     int dtype);
-DeltaPlan plan_delta_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
-                              bool packed, int dtype);
+                     int dtype, bool backward);
 size_t delta_workspace_bytes(const DeltaPlan& pl, int64_t heads, int64_t key_dim, int64_t value_dim, int dtype);
 hipError_t launch_delta(const DeltaArgs& a, const DeltaPlan& pl);
 

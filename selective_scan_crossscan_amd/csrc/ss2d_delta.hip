@@ -17,7 +17,7 @@ constexpr int kCarryColumns = 32;
 template <typename E, int C, int KP, DeltaPass PASS, bool TINY>
 __global__ __launch_bounds__(256, TINY ? 1 : 2) void delta_walk(DeltaParams p) {
   __shared__ WalkTiles<E, C, KP, 64, PASS> lds;
-  walk<E, C, KP, 64, 1, PASS, TINY>(p, (uint32_t)block_id(), lds);
+  walk<E, C, KP, 64, PASS, TINY>(p, (uint32_t)block_id(), lds);
 }
 
 // One workgroup carries 32 value columns of a head along its sequence's segments: h <- M h + u forwards, h <- M' h + u
@@ -190,41 +190,6 @@ hipError_t launch_walk(DeltaParams p, const DeltaPlan& pl, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Chunks of 64 tokens (32 in fp32).  Sequences are cut so that there are about two workgroups per CU, packed ones, of which
-// only some may be long, four; into three segments at least, as two would be walked twice for less than twice the speed.
-// 16 heads of 128, us for 2, 3 and 4 workgroups per CU with inverses in two parts: 8192 tokens in one sequence 220, 258,
-// 283, 38144 in six packed ones 897, 771, 750; gradients of 2 x 4096 tokens 718 (one 846, four 799).
-DeltaPlan make_plan(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
-                    int dtype, int64_t want, int least) {
-  DeltaPlan pl;
-  AttentionPlan& a = pl.a;
-  const int64_t few = dtype == 1 ? 8 : 4;  // values in 16 bytes
-  a.tiny = key_dim < few || value_dim < few;
-  a.kp = a.tiny ? (key_dim <= 32 ? 32 : 256) : key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
-  a.vt = 64;
-  a.vtiles = (int)((value_dim + 63) / 64);
-  const int64_t chunk = a.chunk = dtype == 1 ? 64 : 32;
-  const int64_t longest = packed ? tokens : tokens / sequences;
-  if (packed && sequences > 1) want *= 2;
-  const int64_t each = want / (heads * a.vtiles);  // segments of all sequences together
-  int64_t parts = packed ? (each - sequences > each / 2 ? each - sequences : each / 2) : each / sequences;
-  if (parts < 1) parts = 1;
-  int64_t seg = (longest + parts - 1) / parts;
-  if (seg < 4 * chunk) seg = 4 * chunk;
-  seg = (seg + chunk - 1) / chunk * chunk;
-  a.split = longest > (least - 1) * seg;
-  if (!a.split) seg = (longest + chunk - 1) / chunk * chunk;
-  a.seg_len = seg;
-  a.nseg = (int)((longest + seg - 1) / seg);
-  a.slots = packed ? tokens / seg + sequences : sequences * a.nseg;
-  // Packed sequences' kept segments are numbered as their slots are, or with many sequences those of the cut ones alone:
-  // 1024 sequences of 64 tokens, 16 heads of 128, keep 68 MiB for them instead of 2080, 1395 us instead of 1646.
-  pl.cut = packed && sequences > tokens / seg + 2;
-  pl.parts = pl.cut ? 2 * tokens / seg + 2 : a.slots;
-  a.chunks = packed ? tokens / chunk + sequences : sequences * ((longest + chunk - 1) / chunk);
-  return pl;
-}
-
 struct Regions {
   size_t systems, seg_state, seg_map, end;
 };
@@ -245,17 +210,38 @@ Regions regions(const DeltaPlan& pl, int64_t heads, int64_t K, int64_t V, int dt
 
 }  // namespace
 
+// Chunks of 64 tokens (32 in fp32).  Sequences are cut so that there are about two workgroups per CU, packed ones, of which
+// only some may be long, four; into three segments at least, as two would be walked twice for less than twice the speed.
+// 16 heads of 128, us for 2, 3 and 4 workgroups per CU with inverses in two parts: 8192 tokens in one sequence 220, 258,
+// 283, 38144 in six packed ones 897, 771, 750; gradients of 2 x 4096 tokens 718 (one 846, four 799).
 DeltaPlan plan_delta(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
-                     int dtype) {
-  DeltaPlan pl = make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, 512, 3);
-  pl.backward = false;
-  return pl;
-}
-
-DeltaPlan plan_delta_backward(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim,
-                              bool packed, int dtype) {
-  DeltaPlan pl = make_plan(sequences, tokens, heads, key_dim, value_dim, packed, dtype, 512, 3);
-  pl.backward = true;
+                     int dtype, bool backward) {
+  DeltaPlan pl;
+  pl.backward = backward;
+  AttentionPlan& a = pl.a;
+  const int64_t few = dtype == 1 ? 8 : 4;  // values in 16 bytes
+  a.tiny = key_dim < few || value_dim < few;
+  a.kp = a.tiny ? (key_dim <= 32 ? 32 : 256) : key_dim <= 32 ? 32 : key_dim <= 64 ? 64 : key_dim <= 128 ? 128 : 256;
+  a.vt = 64;
+  a.vtiles = (int)((value_dim + 63) / 64);
+  const int64_t chunk = a.chunk = dtype == 1 ? 64 : 32;
+  const int64_t longest = packed ? tokens : tokens / sequences;
+  const int64_t each = (packed && sequences > 1 ? 1024 : 512) / (heads * a.vtiles);  // segments of all sequences together
+  int64_t parts = packed ? (each - sequences > each / 2 ? each - sequences : each / 2) : each / sequences;
+  if (parts < 1) parts = 1;
+  int64_t seg = (longest + parts - 1) / parts;
+  if (seg < 4 * chunk) seg = 4 * chunk;
+  seg = (seg + chunk - 1) / chunk * chunk;
+  a.split = longest > 2 * seg;
+  if (!a.split) seg = (longest + chunk - 1) / chunk * chunk;
+  a.seg_len = seg;
+  a.nseg = (int)((longest + seg - 1) / seg);
+  a.slots = packed ? tokens / seg + sequences : sequences * a.nseg;
+  // Packed sequences' kept segments are numbered as their slots are, or with many sequences those of the cut ones alone:
+  // 1024 sequences of 64 tokens, 16 heads of 128, keep 68 MiB for them instead of 2080, 1395 us instead of 1646.
+  pl.cut = packed && sequences > tokens / seg + 2;
+  pl.parts = pl.cut ? 2 * tokens / seg + 2 : a.slots;
+  a.chunks = packed ? tokens / chunk + sequences : sequences * ((longest + chunk - 1) / chunk);
   return pl;
 }
 

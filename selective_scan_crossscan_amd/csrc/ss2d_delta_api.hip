@@ -13,11 +13,8 @@ namespace {
 using namespace ss2d::checks;
 
 // ------------------------------------------------------------------ delta rule
-ss2d::DeltaPlan plan_of(const ss2d_attention_sizes& z, bool packed, int dtype) {
-  return ss2d::plan_delta(z.sequences, z.tokens, z.heads, z.key_dim, z.value_dim, packed, dtype);
-}
-ss2d::DeltaPlan backward_plan_of(const ss2d_attention_sizes& z, bool packed, int dtype) {
-  return ss2d::plan_delta_backward(z.sequences, z.tokens, z.heads, z.key_dim, z.value_dim, packed, dtype);
+ss2d::DeltaPlan plan_of(const ss2d_attention_sizes& z, bool packed, int dtype, bool backward) {
+  return ss2d::plan_delta(z.sequences, z.tokens, z.heads, z.key_dim, z.value_dim, packed, dtype, backward);
 }
 
 constexpr int64_t kMostBlocks = (int64_t)1 << 30;
@@ -192,7 +189,7 @@ extern "C" {
 int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int dtype) {
   const int rc = check_attention_sizes(sizes ? &sizes->a : nullptr, packed != 0, dtype);
   if (rc != SS2D_OK) return rc;
-  const ss2d::DeltaPlan pl = plan_of(sizes->a, packed != 0, dtype);
+  const ss2d::DeltaPlan pl = plan_of(sizes->a, packed != 0, dtype, false);
   if (!grid_ok(pl, sizes->a)) return SS2D_ERR_SHAPE;
   return (int64_t)ss2d::delta_workspace_bytes(pl, sizes->a.heads, sizes->a.key_dim, sizes->a.value_dim, dtype);
 }
@@ -217,7 +214,7 @@ int ss2d_delta_rule(const void* q, const void* k, const void* v, const float* lo
   for (const Range& r : in)
     if (r.bytes < 0) return SS2D_ERR_SHAPE;
   const Range ro{o, z.tokens * z.heads * z.value_dim * e}, rs{state_out, in[6].bytes};
-  const ss2d::DeltaPlan pl = plan_of(z, packed, dtype);
+  const ss2d::DeltaPlan pl = plan_of(z, packed, dtype, false);
   if (!grid_ok(pl, z)) return SS2D_ERR_SHAPE;
   const int64_t need = (int64_t)ss2d::delta_workspace_bytes(pl, z.heads, z.key_dim, z.value_dim, dtype);
   const Range rw{workspace, need};
@@ -241,7 +238,7 @@ int64_t ss2d_delta_rule_backward_workspace(const ss2d_delta_sizes* sizes, int pa
   const int rc = check_attention_sizes(sizes ? &sizes->a : nullptr, packed != 0, dtype);
   if (rc != SS2D_OK) return rc;
   const ss2d_attention_sizes& z = sizes->a;
-  const ss2d::DeltaPlan pl = backward_plan_of(z, packed != 0, dtype);
+  const ss2d::DeltaPlan pl = plan_of(z, packed != 0, dtype, true);
   if (!backward_grid_ok(pl, z)) return SS2D_ERR_SHAPE;
   return (int64_t)ss2d::delta_backward_workspace_bytes(pl, z.tokens, z.groups, z.heads, z.key_dim, z.value_dim, dtype);
 }
@@ -269,7 +266,7 @@ int ss2d_delta_rule_backward(const void* q, const void* k, const void* v, const 
                        {dstate_out, st}};
   for (const Range& r : in)
     if (r.bytes < 0) return SS2D_ERR_SHAPE;
-  const ss2d::DeltaPlan pl = backward_plan_of(z, packed, dtype);
+  const ss2d::DeltaPlan pl = plan_of(z, packed, dtype, true);
   if (!backward_grid_ok(pl, z)) return SS2D_ERR_SHAPE;
   const int64_t need = (int64_t)ss2d::delta_backward_workspace_bytes(pl, z.tokens, z.groups, z.heads, z.key_dim,
                                                                      z.value_dim, dtype);

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256, 2) void delta_segment_pair(DeltaParams p, Back
   } lds;
   const uint32_t block = (uint32_t)block_id();
   if (block < first)
-    walk<E, C, KP, 64, 1, kSegments, TINY>(p, block, lds.w);
+    walk<E, C, KP, 64, kSegments, TINY>(p, block, lds.w);
   else
     walk_back<E, C, KP, 64, true, TINY>(b, block - first, lds.b);
 }

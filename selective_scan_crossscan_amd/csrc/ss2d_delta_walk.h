@@ -1,7 +1,7 @@
 // The gated delta rule: the walks over the chunks, forwards and backwards, as what kernels of either kind, or of both,
 // are made of (ss2d_delta.hip, ss2d_delta_backward.hip).
 //
-// One workgroup walks a segment of one sequence and head for VT value columns; a wave owns 16 NV of them, and the state,
+// One workgroup walks a segment of one sequence and head for VT value columns; a wave owns 16 of them, and the state,
 // errors and outputs of its columns never leave its registers.  Keys, queries, values and the chunk's systems come
 // through LDS, read by all waves.  Three passes share the forward walk: outputs; a segment's own part of the state and
 // its map of the state before it; the states before all chunks and the errors, for the gradients.
@@ -38,9 +38,9 @@ struct WalkTiles {
   __attribute__((aligned(16))) char sys[(PASS == kOutputs ? 2 : 1) * S::kFrags * S::kParts * S::kFragBytes];
   Rates<C> rates;
 };
-template <typename E, int C, int KP, int VT, int NV, DeltaPass PASS, bool TINY>
+template <typename E, int C, int KP, int VT, DeltaPass PASS, bool TINY>
 __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkTiles<E, C, KP, VT, PASS>& lds) {
-  constexpr int NW = VT / 16 / NV, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
+  constexpr int NW = VT / 16, THREADS = NW * 64, NI = C / 16, NK = KP / 16, PF = kFullParts<E>;
   using S = Systems<E, C>;
   constexpr int PN = S::kParts;
   constexpr int kSystem = PASS == kOutputs ? S::kForward : S::kOne;  // bytes read per chunk
@@ -62,7 +62,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
   if (PASS == kSegments && seg.last && !(map && p.last_maps && seg.begin > 0)) return;  // of no use
   const int group = head / (p.heads / p.groups);
   const int K = p.K, v0 = (map ? tile - p.vtiles : tile) * VT, nv = min((map ? KP : p.V) - v0, VT);
-  const int vw = wave * 16 * NV;
+  const int vw = wave * 16, v = vw + l;
   const uint32_t lane_at = 4 * (4 * g * kArrayTile + vw + l);  // bytes into a tile of the chunks' arrays
   const bool active = PASS == kStates || vw < nv;  // the chunks' arrays are written whole
   const int64_t token0 = p.map.cu ? seg.start : 0, sq = p.map.cu ? 0 : seg.s;
@@ -133,28 +133,24 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     fetch_rest(first, seg.begin);
   }
 
-  // the state: rows 16 kt + 4 g + r, column vw + 16 t + l
-  f32x4 h[NK][NV];
+  // the state: rows 16 kt + 4 g + r, column v
+  f32x4 h[NK];
   const int64_t kv = (int64_t)K * p.V, qh = ((int64_t)seg.s * p.heads + head) * kv;
   const float* from = PASS == kSegments ? nullptr : p.split && seg.several() ? p.seg_state + (part_number(p.map, p.cut, seg) * p.heads + head) * kv : p.state_in ? p.state_in + qh : nullptr;
-#pragma unroll
-  for (int t = 0; t < NV; ++t) {
-    const int v = vw + t * 16 + l;
-    if (from) {
-      const float* c = from + v0 + min(v, nv - 1);
-#pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h[kt][t][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
-    }
+  if (from) {
+    const float* c = from + v0 + min(v, nv - 1);
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = kt * 16 + 4 * g + r;
-        h[kt][t][r] = from ? (k < K && v < nv ? h[kt][t][r] : 0.f) : map && k == v0 + v && k < K ? 1.f : 0.f;
-      }
+      for (int r = 0; r < 4; ++r) h[kt][r] = c[(int64_t)min(kt * 16 + 4 * g + r, K - 1) * p.V];
   }
+#pragma unroll
+  for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int k = kt * 16 + 4 * g + r;
+      h[kt][r] = from ? (k < K && v < nv ? h[kt][r] : 0.f) : map && k == v0 + v && k < K ? 1.f : 0.f;
+    }
   if (map)
     for (int i = threadIdx.x; i < C * vs.stride; i += THREADS) vs.e[i] = (E)0;
   if (seg.begin < seg.end) {
@@ -179,69 +175,51 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) to[(kt * 16 + r) * kArrayTile + t * 16] = h[kt][t][r];
+          for (int r = 0; r < 4; ++r) to[(kt * 16 + r) * kArrayTile] = h[kt][r];
       }
-      f32x4 z[NI][NV], o[NV][NI];
+      f32x4 z[NI], o[1][NI];
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int x = 0; x < NI; ++x) z[x][t] = o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < NI; ++x) z[x] = o[0][x] = f32x4{0.f, 0.f, 0.f, 0.f};
       // K h and h' Q'
 #pragma unroll
       for (int c = 0; c < NK; c += 2) {
-        Frag<E> b[NV][PF];
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          stack(h[c][t], h[c + 1][t], u);
-          split_parts(u, b[t]);
-        }
+        Frag<E> b[PF];
+        float u[8];
+        stack(h[c], h[c + 1], u);
+        split_parts(u, b);
         Frag<E> k[NI];
 #pragma unroll
         for (int x = 0; x < NI; ++x) k[x] = frag_row_split(ks, x * 16 + l, c * 16);
 #pragma unroll
         for (int q = PF - 1; q >= 0; --q)  // independent products next to each other
 #pragma unroll
-          for (int x = 0; x < NI; ++x)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) z[x][t] = mma(k[x], b[t][q], z[x][t]);
+          for (int x = 0; x < NI; ++x) z[x] = mma(k[x], b[q], z[x]);
         if (PASS == kOutputs)
 #pragma unroll
           for (int x = 0; x < NI; ++x) {
             const Frag<E> f = frag_row_split(qs, x * 16 + l, c * 16);
 #pragma unroll
-            for (int q = PF - 1; q >= 0; --q)
-#pragma unroll
-              for (int t = 0; t < NV; ++t) o[t][x] = mma(b[t][q], f, o[t][x]);
+            for (int q = PF - 1; q >= 0; --q) o[0][x] = mma(b[q], f, o[0][x]);
           }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (PASS == kOutputs)
 #pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const float f = p.scale * rates.since[x * 16 + l];
-#pragma unroll
-          for (int t = 0; t < NV; ++t) o[t][x] *= f;
-        }
+        for (int x = 0; x < NI; ++x) o[0][x] *= p.scale * rates.since[x * 16 + l];
       // the errors E = Z + N Z, Z = V - exp(G) K h
-      f32x4 e[NV][NI];
+      f32x4 e[NI];
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
         const f32x4 f0 = rates.four(&rates.since[j * 16 + 4 * g]), f1 = rates.four(&rates.since[j * 16 + 16 + 4 * g]);
+        float u[8];
+        frag_values(frag_col_split(vs, j * 16, vw), u);
 #pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          frag_values(frag_col_split(vs, j * 16, vw + t * 16), u);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            z[j][t][r] = fmaf(-f0[r], z[j][t][r], u[r]);
-            z[j + 1][t][r] = fmaf(-f1[r], z[j + 1][t][r], u[4 + r]);
-          }
-          e[t][j] = z[j][t];
-          e[t][j + 1] = z[j + 1][t];
+        for (int r = 0; r < 4; ++r) {
+          z[j][r] = fmaf(-f0[r], z[j][r], u[r]);
+          z[j + 1][r] = fmaf(-f1[r], z[j + 1][r], u[4 + r]);
         }
+        e[j] = z[j];
+        e[j + 1] = z[j + 1];
       }
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
@@ -250,14 +228,11 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
         for (int x = j; x < NI; ++x)
 #pragma unroll
           for (int q = 0; q < PN; ++q) a[x][q] = system_frag<E>(sys, S::lower(x, j / 2), q);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          Frag<E> b[PN];
-          stack(z[j][t], z[j + 1][t], u);
-          split_parts(u, b);
-          j == 0 ? mma_parts<0, NI>(a, b, e[t]) : mma_parts<2, NI>(a, b, e[t]);
-        }
+        float u[8];
+        Frag<E> b[PN];
+        stack(z[j], z[j + 1], u);
+        split_parts(u, b);
+        j == 0 ? mma_parts<0, NI>(a, b, e) : mma_parts<2, NI>(a, b, e);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (PASS == kStates) {
@@ -265,27 +240,18 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 #pragma unroll
         for (int x = 0; x < NI; ++x)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) to[(x * 16 + r) * kArrayTile + t * 16] = e[t][x][r];
+          for (int r = 0; r < 4; ++r) to[(x * 16 + r) * kArrayTile] = e[x][r];
       }
       // U = b E; P U to the outputs, K' (w U) to the state
 #pragma unroll
-      for (int x = 0; x < NI; ++x) {
-        const f32x4 b = rates.four(&rates.beta[x * 16 + 4 * g]);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) e[t][x] *= b;
-      }
+      for (int x = 0; x < NI; ++x) e[x] *= rates.four(&rates.beta[x * 16 + 4 * g]);
       if (PASS == kOutputs) {
 #pragma unroll
         for (int j = 0; j < NI; j += 2) {
-          Frag<E> a[NV][PF];
-#pragma unroll
-          for (int t = 0; t < NV; ++t) {
-            float u[8];
-            stack(e[t][j], e[t][j + 1], u);
-            split_parts(u, a[t]);
-          }
+          Frag<E> a[PF];
+          float u[8];
+          stack(e[j], e[j + 1], u);
+          split_parts(u, a);
 #pragma unroll
           for (int x = j; x < NI; ++x) {
             Frag<E> s[PF];
@@ -294,42 +260,33 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 #pragma unroll
             for (int n = PF - 1; n >= 0; --n)
 #pragma unroll
-              for (int q = 0; q <= n; ++q)
-#pragma unroll
-                for (int t = 0; t < NV; ++t) o[t][x] = mma(a[t][q], s[n - q], o[t][x]);
+              for (int q = 0; q <= n; ++q) o[0][x] = mma(a[q], s[n - q], o[0][x]);
           }
         }
         E* ob = static_cast<E*>(p.o) + ((seg.start + at) * p.heads + head) * p.V + v0;
-        put_rows<NI, NV>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 16, l, o);
+        put_rows<NI, 1>(ob, (int64_t)p.heads * p.V, n, nv, vw + 4 * g, 0, l, o);
         __builtin_amdgcn_sched_barrier(0);  // the outputs' registers are free for what follows
       }
       // The next systems, late, in registers that the outputs had; loads under the condition, alike for a wave's threads.
       if (kAhead<KP> && PASS == kOutputs) fetch_rest(next, ahead);
       const float all = rates.since[C - 1];
 #pragma unroll
-      for (int kt = 0; kt < NK; ++kt)
-#pragma unroll
-        for (int t = 0; t < NV; ++t) h[kt][t] *= all;
+      for (int kt = 0; kt < NK; ++kt) h[kt] *= all;
 #pragma unroll
       for (int j = 0; j < NI; j += 2) {
-        Frag<E> b[NV][PF];
+        Frag<E> b[PF];
         const f32x4 w0 = rates.four(&rates.left[j * 16 + 4 * g]), w1 = rates.four(&rates.left[j * 16 + 16 + 4 * g]);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          float u[8];
-          stack(e[t][j] * w0, e[t][j + 1] * w1, u);
-          split_parts(u, b[t]);
-        }
+        float u[8];
+        stack(e[j] * w0, e[j + 1] * w1, u);
+        split_parts(u, b);
 #pragma unroll
         for (int kt = 0; kt < NK; kt += 2) {
           const Frag<E> k0 = frag_col_split(ks, j * 16, kt * 16), k1 = frag_col_split(ks, j * 16, kt * 16 + 16);
 #pragma unroll
-          for (int q = PF - 1; q >= 0; --q)
-#pragma unroll
-            for (int t = 0; t < NV; ++t) {
-              h[kt][t] = mma(k0, b[t][q], h[kt][t]);
-              h[kt + 1][t] = mma(k1, b[t][q], h[kt + 1][t]);
-            }
+          for (int q = PF - 1; q >= 0; --q) {
+            h[kt] = mma(k0, b[q], h[kt]);
+            h[kt + 1] = mma(k1, b[q], h[kt + 1]);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -349,12 +306,10 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
 #pragma unroll
     for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int k = kt * 16 + 4 * g + r, v = vw + t * 16 + l;
-          if (k < rows && v < nv) to[(int64_t)k * step + v0 + v] = h[kt][t][r];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int k = kt * 16 + 4 * g + r;
+        if (k < rows && v < nv) to[(int64_t)k * step + v0 + v] = h[kt][r];
+      }
   }
 }
 
