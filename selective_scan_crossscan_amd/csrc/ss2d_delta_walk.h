@@ -295,7 +295,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, uint32_t block, WalkT
     __syncthreads();  // the chunk has been read
     if (kAhead<KP>)
       land(next, ahead);
-    else
+    else if (at + C < seg.end)  // all waves alike
       bring(ahead);
   }
 
@@ -578,7 +578,7 @@ __device__ __forceinline__ void walk_back(const BackParams& b, uint32_t block, B
     __syncthreads();  // the chunk has been read
     if (kAhead<KP>)
       land(next, ahead);
-    else
+    else if (c > 0)
       bring(ahead);
   }
   float* to = SUM ? b.seg_dstate + (slot * p.heads + head) * kv : seg.begin == 0 && b.dstate_in ? b.dstate_in + qh : nullptr;
