@@ -77,6 +77,10 @@ int64_t ss2d_delta_rule_workspace(const ss2d_delta_sizes* sizes, int packed, int
  * Outputs are overwritten, not added to; tokens outside the sequences keep what they
  * were.  Outputs must not overlap inputs or each other.  What enters a product keeps 24
  * bits in either type, so dq, dk and dv in bf16 show their own rounding alone.
+ * dlog_decay sums terms of its chunk that cancel, q.dq - dv.v of the tokens behind it and
+ * the state with its gradient, and its error is fp32's relative to those terms' sizes: the
+ * gradient of a token that forgets nearly everything, near exp(g), may have no correct
+ * digits.
  */
 int ss2d_delta_rule_backward(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
                              const float* state_in, const int32_t* cu_seqlens, const void* d_o,

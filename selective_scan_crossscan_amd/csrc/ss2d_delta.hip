@@ -5,8 +5,8 @@
 // affine, h -> M h + u: u is the walk from 0, M (keys x keys) the walk from the identity with values 0, both by the same
 // kernel, and a carry along the segments gives the states before them.
 //
-// us of 38144 packed tokens in six sequences, 16 heads of 128, bf16: systems 109, segments 396, carry 87, outputs 400; of
-// 16 x 2048 tokens systems 99, outputs 335.
+// us of 38144 packed tokens in six sequences, 16 heads of 128, bf16: systems 98, segments 344, carry 81, outputs 382; of
+// 16 x 2048 tokens systems 90, outputs 329.
 #include "ss2d_delta_walk.h"
 
 namespace ss2d {
@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256, TINY ? 1 : 2) void delta_walk(DeltaParams p) {
 // backwards, h before (behind) each segment in the place of its u.  The first one's too: the last segment's workgroup may
 // write the final state over the initial one before the first has begun.  A wave owns 16 (at 256 keys 32) rows of the
 // result and reads those of M alone, the next segment's while this one's are multiplied; h goes round through LDS as
-// fragments in parts: 3.7 us a segment of 128 keys, the latency of M's loads, the parts and the barrier one after the
+// fragments in parts: 3.5 us a segment of 128 keys, the latency of M's loads, the parts and the barrier one after the
 // other.  (With 16 columns per wave and all of M read by each 10 us.)
 template <int KP>
 constexpr int kCarryThreads = KP == 256 ? 512 : KP * 4;
@@ -212,8 +212,8 @@ Regions regions(const DeltaPlan& pl, int64_t heads, int64_t K, int64_t V, int dt
 
 // Chunks of 64 tokens (32 in fp32).  Sequences are cut so that there are about two workgroups per CU, packed ones, of which
 // only some may be long, four; into three segments at least, as two would be walked twice for less than twice the speed.
-// 16 heads of 128, us for 2, 3 and 4 workgroups per CU with inverses in two parts: 8192 tokens in one sequence 220, 258,
-// 283, 38144 in six packed ones 897, 771, 750; gradients of 2 x 4096 tokens 718 (one 846, four 799).
+// 16 heads of 128, us for 1, 2, 3 and 4 workgroups per CU: 8192 tokens in one sequence 255, 257, 298, 316, gradients of
+// 2 x 4096 tokens 718, 622, 704, 688; for twice as many of each, 38144 tokens in six packed sequences 1075, 886, 960, 973.
 DeltaPlan plan_delta(int64_t sequences, int64_t tokens, int64_t heads, int64_t key_dim, int64_t value_dim, bool packed,
                      int dtype, bool backward) {
   DeltaPlan pl;

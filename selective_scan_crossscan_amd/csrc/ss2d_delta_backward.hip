@@ -19,8 +19,9 @@
 // all else chunk by chunk, in any order, with no walk to wait for.  A segment's map of D is the transpose of its map of
 // the state, so cut sequences' maps are formed once.
 //
-// us of 2 x 4096 tokens, 16 heads of 128, bf16: systems 47, both ways' segments 171 and carries 37, states 86, the walk
-// back 128, all else 202 (192 KiB of H, D, E and dF in fp32 per chunk and head, at 2 TB/s).
+// us of 2 x 4096 tokens, 16 heads of 128, bf16: systems 39, both ways' segments 151 and carries 35, states 80, the walk
+// back 113, all else 217 (192 KiB of H, D, E and dF in fp32 per chunk and head at 1.9 TB/s; matrix instructions 20% of the
+// SIMDs' cycles, the waves waiting 58% of their time).
 #include "ss2d_delta_walk.h"
 
 namespace ss2d {
@@ -68,8 +69,7 @@ __device__ __forceinline__ void put4_parts(Tile<float, R, CC, PAD> (&m)[1], int 
   put4(&m[0].e[at], x);
 }
 
-// Eight waves also for few keys (2 x 2048 tokens of 16 heads, all gradients: 64 keys 248 us, with four waves 256; 32 keys
-// 215 and 219; 128 keys 343 and 358).
+// Eight waves also for few keys: four would spill registers.
 constexpr int kGradientWaves = 8;
 // One workgroup per chunk and head; a wave owns key columns wave, wave + NW, ... by 16 and their dq and dk, transposed
 // (rows k, columns token); the values are gone through in tiles of 64 columns.
@@ -424,8 +424,8 @@ __global__ __launch_bounds__(256) void sum_parts(const float* __restrict__ parts
 
 // ------------------------------------------------------------------ launches
 // Value columns of a workgroup that walks back, and the parts of `inner` they leave.  Of 128 values half the workgroups
-// read the keys and systems once (2 x 2048 tokens, 16 heads of 128, all gradients 342 us, 364 in tiles of 64; 64 and 32
-// keys alike).
+// read the keys and systems once (2 x 2048 tokens, 16 heads of 128, all gradients 368 us, 387 in tiles of 64; 64 keys 258
+// and 257, 32 keys 210 and 209).
 int back_tile(int64_t V, const DeltaPlan& pl) { return V <= 64 || pl.a.tiny ? 64 : 128; }
 int columns_of(int64_t V, const DeltaPlan& pl) {
   const int vt = back_tile(V, pl);

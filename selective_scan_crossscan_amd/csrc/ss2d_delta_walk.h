@@ -7,8 +7,8 @@
 // its map of the state before it; the states before all chunks and the errors, for the gradients.
 //
 // Bound by latency and issue, not by memory: of 16 x 2048 tokens, 16 heads of 128 in bf16, the outputs' walk takes
-// 335 us, vector instructions 36% and matrix instructions 32% of the SIMDs' cycles, the waves waiting 38% of their time
-// (chunk after chunk barriers, reads from LDS, and products that need the ones before); without its loads 70 us less.
+// 329 us, vector instructions 42% and matrix instructions 36% of the SIMDs' cycles, the waves waiting 38% of their time
+// (chunk after chunk barriers, reads from LDS, and products that need the ones before).
 #pragma once
 
 #include <type_traits>
@@ -22,8 +22,8 @@ using namespace tok;
 
 constexpr int kArrayTile = 64;  // columns of a tile of the chunks' arrays
 // Whether the next chunk's loads wait in registers while one is worked on.  256 keys leave no registers for that, and
-// are loaded when the chunk before has been read.  (128 keys, forward of 2 x 16384 tokens of 16 heads 687 us, loaded late
-// 705; 2 x 2048 tokens 140 and 136.)
+// are loaded when the chunk before has been read.  (128 keys, forward of 2 x 16384 tokens of 16 heads 701 us, loaded late
+// 729; 2 x 2048 tokens 134 and 129.)
 template <int KP>
 constexpr bool kAhead = KP <= 128;
 
@@ -333,7 +333,7 @@ struct BackParams {
 template <typename E, int C, int KP, int VT>
 struct BackTiles {
   using S = Systems<E, C>;
-  Tile<E, C, KP, 16> qs, ks;  // 16 all: two workgroups' fit a CU at 128 keys and 64 values
+  Tile<E, C, KP, 16> qs, ks;  // 16 all: at 128 keys two workgroups of a pair of segment passes fit a CU
   Tile<E, C, VT, 16> ds;
   __attribute__((aligned(16))) char sys[2 * S::kFrags * S::kParts * S::kFragBytes];  // the transposed inverse and P'
   Rates<C> rates;
