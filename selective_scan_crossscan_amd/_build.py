@@ -86,7 +86,10 @@ def check_registers(path: str) -> None:
     """Kernels of the delta rule must keep all vector registers.  Compiled with too few, those of 256 keys stored some to
     memory while only part of a wave's threads were active and read them back for all: wrong results, and addresses out of
     range."""
-    bad = {k: n for k, n in vector_spills(path).items() if n and "delta_" in k}
+    spills = vector_spills(path)
+    if not spills:
+        raise RuntimeError(f"no kernels' metadata found in {path}")
+    bad = {k: n for k, n in spills.items() if n and "delta_" in k}
     if bad:
         raise RuntimeError(f"spilled vector registers where none may be: {bad}")
 

@@ -42,6 +42,10 @@ def test_spilled_registers_are_found_and_refused(tmp_path):
     _build.check_registers(other)
     with pytest.raises(RuntimeError, match="delta_many"):
         _build.check_registers(many)
+    nothing = tmp_path / "nothing"
+    nothing.write_bytes(b"no kernels")
+    with pytest.raises(RuntimeError, match="metadata"):
+        _build.check_registers(str(nothing))
 
 
 def test_the_library_keeps_them():
