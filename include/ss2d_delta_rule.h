@@ -42,10 +42,12 @@ typedef struct {
  * Outputs must not overlap inputs, but state_out may be state_in itself
  * (SS2D_ERR_ALIAS).  States, decays, sums and the triangular systems of 64 tokens
  * (32 in fp32) are fp32, decays summed in fp64, and what enters a product keeps 24 bits
- * in either type: an output in bf16 shows its own rounding alone.  NaN and Inf propagate: from a token to its
- * sequence's outputs from up to 63 tokens before it on, so padding behind a sequence's
- * end has to be finite, or left out by cu_seqlens.
- * Results do not depend on the workspace, other sequences or streams.
+ * in either type: an output in bf16 shows its own rounding alone.  NaN and Inf
+ * propagate: from a token to its sequence's outputs from up to 63 tokens before it on, so
+ * padding behind a sequence's end has to be finite, or left out by cu_seqlens.
+ * Results do not depend on the workspace, streams, or other sequences' values.  Where
+ * long sequences are cut goes by the sizes of the call, so another packing of the same
+ * sequence may round differently.
  * SS2D_ERR_SHAPE for sizes out of ss2d_linear_attention's ranges, and over 2^30
  * workgroups: chunks of 64 (32) tokens times heads, or segments times heads times tiles
  * of 64 value and key columns.

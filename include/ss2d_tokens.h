@@ -76,8 +76,9 @@ typedef struct {
  * the state itself is made of keeps all its bits.  NaN and Inf propagate: from a token to its
  * sequence's outputs from up to 63 tokens before it on (tokens are taken in chunks as
  * matrix products), so padding behind a sequence's end has to be finite, or left out
- * by cu_seqlens.  Results do not depend on the
- * workspace, other sequences or streams: no atomics, sums in a fixed order.
+ * by cu_seqlens.  Results do not depend on the workspace, streams, or other sequences'
+ * values: no atomics, sums in a fixed order.  Where long sequences are cut goes by the
+ * sizes of the call, so another packing of the same sequence may round differently.
  * SS2D_ERR_SHAPE for sizes outside the ranges above, token strides of 2^24 and more,
  * and over 2^30 tiles of 64 value columns of all heads and segments (a sequence has one
  * or more) or blocks of 256 entries of all states.
