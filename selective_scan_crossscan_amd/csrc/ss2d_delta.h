@@ -185,8 +185,8 @@ __device__ __forceinline__ Frag<E> system_frag(const char* sys, int at, int q) {
 }
 // A chunk's systems on their way from memory, BYTES by THREADS threads; stored as fragments in parts.  Split here, fp32 takes
 // two thirds of the parts' bytes in memory (16 x 2048 tokens of 16 heads of 128: 393 us, with parts in memory 412).  Every
-// thread has whole pieces and no condition stands around them, on purpose: the compiler has stored spilled registers before
-// it let all threads go on behind one, and read them back for all.
+// thread has whole pieces, and no condition that only some threads meet stands around them, on purpose: the compiler has
+// stored spilled registers before it let all threads go on behind one, and read them back for all.
 template <typename E, int BYTES, int THREADS>
 struct SystemLoad {
   static constexpr int kPieces = BYTES / 16 / THREADS;
